@@ -332,6 +332,131 @@ int tr_sparseconv_spatial2channel(const int32_t* children, int64_t n_coarse, con
                                   void* x_coarse, int c_fine, int dtype, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Voxel tokens: per-head norm with position rotation, and windowed attention.
+ * The layers of the structured-latent flow and decoder transformers that stand
+ * next to the convolutions: their tokens are the active voxels, their positions
+ * the voxels' coordinates, and a batch holds its objects one after the other.
+ * ------------------------------------------------------------------------ */
+
+/* A [tokens, heads, dim] view: the dim elements of a row are adjacent, strides
+ * are in elements (so q, k and v may lie side by side in a projection's rows).
+ * data and both strides are multiples of 16 bytes. */
+typedef struct {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+  int heads;
+} tr_sc_heads;
+
+/* Position rotation. Pair i of a row -- elements (2 i, 2 i + 1) if interleaved,
+ * else (i, i + dim / 2) -- turns by the angle pos[t][axis] * freqs[i]: the first
+ * pairs[0] pairs by axis 0, the next pairs[1] by axis 1, the next pairs[2] by
+ * axis 2; pairs past them stay as they are.
+ * pos    device int32, element (t, axis) at t * pos_stride + axis (e.g. the
+ *        x, y, z of coordinate rows, with stride 4).
+ * freqs  device fp32 [dim / 2]. */
+typedef struct {
+  const int32_t* pos;
+  int64_t pos_stride;
+  const float* freqs;
+  int axes; /* 1 .. 3 */
+  int pairs[3];
+  int interleaved;
+} tr_sc_rotation;
+
+/* Norm and rotation of queries and keys in one pass: for each token t and head h
+ *     y = x / sqrt(mean(x^2) + eps) * gain[h],  then y's pairs turned.
+ * q, k         inputs [tokens, heads, dim] of type dtype; each its own head count.
+ * *_gain       device fp32 [rows, dim], rows 1 (shared by the heads) or the
+ *              heads; NULL: no gain.
+ * q_out, k_out outputs of the same shape and type; may be q, k themselves (same
+ *              strides), otherwise they must not overlap the inputs.
+ * dim a multiple of 8 up to 128; fp32 arithmetic, rounded once. The angles are
+ * reduced in 64 bits, so they are as good at large positions as at small ones. */
+int tr_sparseconv_qk_norm_rope(const tr_sc_heads* q, const tr_sc_heads* k, const tr_sc_rotation* rotation,
+                               const float* q_gain, int q_gain_rows, const float* k_gain,
+                               int k_gain_rows, float eps, const tr_sc_heads* q_out,
+                               const tr_sc_heads* k_out, int64_t tokens, int dim, int dtype, void* stream);
+
+/* Its gradient: dq_out, dk_out -> dq, dk (all [tokens, heads, dim] of type
+ * dtype), dq_gain, dk_gain (fp32, as the gains; NULL: not wanted). q, k: the
+ * forward's inputs. dq, dk may be dq_out, dk_out themselves (same strides). The
+ * gains' sums are taken in a fixed order (no atomics: the same bits on every
+ * call). workspace: >= the bytes below, 256-byte aligned. */
+size_t tr_sparseconv_qk_norm_rope_backward_workspace_bytes(int64_t tokens, int q_heads, int kv_heads,
+                                                           int dim);
+int tr_sparseconv_qk_norm_rope_backward(const tr_sc_heads* dq_out, const tr_sc_heads* dk_out,
+                                        const tr_sc_heads* q, const tr_sc_heads* k,
+                                        const tr_sc_rotation* rotation, const float* q_gain,
+                                        int q_gain_rows, const float* k_gain, int k_gain_rows, float eps,
+                                        const tr_sc_heads* dq, const tr_sc_heads* dk, float* dq_gain,
+                                        float* dk_gain, int64_t tokens, int dim, int dtype,
+                                        void* workspace, size_t ws_bytes, void* stream);
+
+/* Sequences and window of an attention call.
+ * batch      number of sequences (objects).
+ * cu_q, cu_k device int32 [batch + 1]: sequence b has the tokens cu_q[b] ..
+ *            cu_q[b + 1] of q and cu_k[b] .. cu_k[b + 1] of k and v. NULL (batch 1
+ *            only): all tokens.
+ * k_len      device int32 [batch] or NULL: sequence b has only the first k_len[b]
+ *            of its tokens of k and v (a cache with room to grow).
+ * left, right, sinks  query i of a sequence with Lq queries and Lk keys stands at
+ *            p = i + Lk - Lq and sees key j when j <= p + right and (j >= p - left
+ *            or j < sinks): a window that moves with the query, and the first
+ *            tokens, which stay visible once they have been seen. -1: no limit on
+ *            that side. Causal: right = 0. sinks in [0, 128].
+ * scale      factor of the scores, > 0.
+ * Offsets and lengths are clamped to the tensors on the device. Rows of outputs
+ * that belong to no sequence have no defined value. */
+typedef struct {
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  const int32_t* k_len;
+  int batch;
+  int64_t left, right;
+  int sinks;
+  float scale;
+} tr_sc_window;
+
+/* out[i] = sum over the keys j that row i sees of softmax(scale q_i . k)_j v_j,
+ * zero for a row that sees none. Query head h reads key-value head
+ * h / (q heads / kv heads). One call for packed objects, prompts and single new
+ * tokens (with few rows the key axis is split over workgroups and joined).
+ * q [tokens_q, q heads, dim], k, v [tokens_k, kv heads, dim], out as q; dtype
+ * bf16, f16 or f32; dim a multiple of 8 up to 128. fp32 scores, statistics and
+ * sums; the weights of a row are rounded to dtype before they multiply v.
+ * What lies in keys and values that a row does not see (NaN, infinities) does
+ * not reach it.
+ * lse        fp32 [q heads, tokens_q] or NULL: log of the sum of the
+ *            exponentials of the scaled scores, -infinity for a row that sees
+ *            none. The backward reads it.
+ * workspace  >= the bytes below, 256-byte aligned (0 bytes: may be NULL). The
+ *            query needs batch, left, right, sinks and scale of the window, not
+ *            its device arrays beyond whether they are NULL.
+ * No atomics: the same bits on every call. out must not overlap q, k, v. */
+size_t tr_sparseconv_window_attention_workspace_bytes(const tr_sc_window* window, int64_t tokens_q,
+                                                      int64_t tokens_k, int q_heads, int kv_heads,
+                                                      int dim, int dtype);
+int tr_sparseconv_window_attention(const tr_sc_heads* q, const tr_sc_heads* k, const tr_sc_heads* v,
+                                   const tr_sc_window* window, const tr_sc_heads* out, float* lse,
+                                   int64_t tokens_q, int64_t tokens_k, int dim, int dtype,
+                                   void* workspace, size_t ws_bytes, void* stream);
+
+/* Its gradients: dout as out; out and lse from the forward; dq [tokens_q, q heads,
+ * dim], dk, dv [tokens_k, kv heads, dim] of type dtype, contiguous. Keys past
+ * k_len get zeros. No atomics: the same bits on every call. */
+size_t tr_sparseconv_window_attention_backward_workspace_bytes(const tr_sc_window* window,
+                                                               int64_t tokens_q, int64_t tokens_k,
+                                                               int q_heads, int kv_heads, int dim,
+                                                               int dtype);
+int tr_sparseconv_window_attention_backward(const tr_sc_heads* dout, const tr_sc_heads* q,
+                                            const tr_sc_heads* k, const tr_sc_heads* v,
+                                            const tr_sc_heads* out, const float* lse,
+                                            const tr_sc_window* window, void* dq, void* dk, void* dv,
+                                            int64_t tokens_q, int64_t tokens_k, int dim, int dtype,
+                                            void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Measured ceilings (for the benchmark's roofline fractions; they compute
  * nothing of the convolution). Both enqueue one kernel on `stream`.
  * ------------------------------------------------------------------------ */

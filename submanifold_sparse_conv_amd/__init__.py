@@ -7,6 +7,9 @@ library; torch only provides device memory and the current stream.
     h = build_hash(coords)          # int32 [N, 4] (b, x, y, z) on the GPU
     m = build_kernel_map(h)         # m.nbr: int32 [N, 27]
     y = forward(m, x, w)            # x [N, C_in], w [27, C_in, C_out] -> [N, C_out]
+
+The transformer layers over the same voxels (norm with position rotation, and
+windowed attention) are in tokens.py and exported here.
 """
 from __future__ import annotations
 
@@ -16,12 +19,16 @@ import torch
 
 from . import _lib
 from ._lib import TrSparseConvError, check  # noqa: F401
+from .tokens import (qk_norm_rope, qk_norm_rope_backward, rope_frequencies, window_attention,  # noqa: F401
+                     window_attention_backward)
 
 __all__ = ["build_hash", "build_kernel_map", "forward", "pack_weights", "forward_packed", "forward_fused",
            "pack_weights_dgrad", "backward_data", "backward_weights", "downsample", "subdivide",
            "channel2spatial", "spatial2channel",
            "status", "hash_lookup", "hash_sorted_rows", "HashTable", "KernelMap", "PackedWeights",
-           "TrSparseConvError", "version", "forward_workspace_bytes", "Workspace", "forward_noalloc"]
+           "TrSparseConvError", "version", "forward_workspace_bytes", "Workspace", "forward_noalloc",
+           "qk_norm_rope", "qk_norm_rope_backward", "rope_frequencies", "window_attention",
+           "window_attention_backward"]
 
 _DTYPES = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16, torch.float16: _lib.F16}
 _ACTS = {"none": _lib.ACT_NONE, "relu": _lib.ACT_RELU, "silu": _lib.ACT_SILU}

@@ -39,6 +39,29 @@ _PP = ctypes.POINTER(ctypes.c_void_p)
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
+
+
+class Heads(ctypes.Structure):
+    """tr_sc_heads: a [tokens, heads, dim] view, strides in elements."""
+    _fields_ = [("data", _P), ("token_stride", _I64), ("head_stride", _I64), ("heads", _I)]
+
+
+class Rotation(ctypes.Structure):
+    """tr_sc_rotation."""
+    _fields_ = [("pos", _P), ("pos_stride", _I64), ("freqs", _P), ("axes", _I), ("pairs", _I * 3),
+                ("interleaved", _I)]
+
+
+class Window(ctypes.Structure):
+    """tr_sc_window."""
+    _fields_ = [("cu_q", _P), ("cu_k", _P), ("k_len", _P), ("batch", _I), ("left", _I64), ("right", _I64),
+                ("sinks", _I), ("scale", _F)]
+
+
+_H = ctypes.POINTER(Heads)
+_R = ctypes.POINTER(Rotation)
+_W = ctypes.POINTER(Window)
 SIGNATURES = [
     ("tr_sparseconv_version", _I, []),
     ("tr_sparseconv_last_error", ctypes.c_char_p, []),
@@ -70,6 +93,15 @@ SIGNATURES = [
     ("tr_sparseconv_subdivide", _I, [_P, _I64, _P, _P, _P, _I64, _P, _SZ, _P, ctypes.POINTER(ctypes.c_int64)]),
     ("tr_sparseconv_channel2spatial", _I, [_P, _I64, _P, _P, _I, _I, _P]),
     ("tr_sparseconv_spatial2channel", _I, [_P, _I64, _P, _P, _I, _I, _P]),
+    ("tr_sparseconv_qk_norm_rope", _I, [_H, _H, _R, _P, _I, _P, _I, _F, _H, _H, _I64, _I, _I, _P]),
+    ("tr_sparseconv_qk_norm_rope_backward_workspace_bytes", _SZ, [_I64, _I, _I, _I]),
+    ("tr_sparseconv_qk_norm_rope_backward", _I,
+     [_H, _H, _H, _H, _R, _P, _I, _P, _I, _F, _H, _H, _P, _P, _I64, _I, _I, _P, _SZ, _P]),
+    ("tr_sparseconv_window_attention_workspace_bytes", _SZ, [_W, _I64, _I64, _I, _I, _I, _I]),
+    ("tr_sparseconv_window_attention", _I, [_H, _H, _H, _W, _H, _P, _I64, _I64, _I, _I, _P, _SZ, _P]),
+    ("tr_sparseconv_window_attention_backward_workspace_bytes", _SZ, [_W, _I64, _I64, _I, _I, _I, _I]),
+    ("tr_sparseconv_window_attention_backward", _I,
+     [_H, _H, _H, _H, _H, _P, _W, _P, _P, _P, _I64, _I64, _I, _I, _P, _SZ, _P]),
     ("tr_sparseconv_ceiling_mfma_flops", _I64, [_I, _I]),
     ("tr_sparseconv_ceiling_mfma", _I, [_P, _I, _I, _P]),
     ("tr_sparseconv_ceiling_copy", _I, [_P, _P, _SZ, _I, _P]),

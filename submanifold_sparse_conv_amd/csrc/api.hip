@@ -9,6 +9,7 @@
 
 #include "common.h"
 #include "launch.h"
+#include "tokens.h"
 #include "tr_sparseconv.h"
 
 using namespace trsc;
@@ -20,6 +21,10 @@ constexpr uint32_t kKmapMagic = 0x4D4B4354u;  // "TCKM"
 constexpr int64_t kMaxN = int64_t(1) << 30;  // table capacity 2^31 slots at most
 
 thread_local std::string g_last_error;
+
+}  // namespace
+
+namespace trsc {
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -34,6 +39,10 @@ int fail(int code, const char* fmt, ...) {
 int hip_fail(hipError_t e, const char* where) {
   return fail(TR_SC_ERR_HIP, "%s: %s", where, hipGetErrorString(e));
 }
+
+}  // namespace trsc
+
+namespace {
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 

@@ -1,0 +1,585 @@
+// Gradients of the windowed attention with sinks.
+//
+// Mathematics. With P_ij = e^{scale q_i.k_j - lse_i} over the keys that row i
+// sees and delta_i = o_i . do_i,
+//     dV_j = sum_i P_ij do_i,   dP_ij = do_i . v_j,   dS_ij = P_ij (dP_ij - delta_i),
+//     dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum_i dS_ij q_i.
+// Two kernels recompute P from q, k and lse: one walks the keys for 128 rows
+// (dq, and delta on the way), one walks the rows for 128 keys (dk, dv). Seven
+// products of the tile sizes instead of the five that one kernel with atomic
+// sums would need, but every sum has one owner and a fixed order: the same bits
+// on every call, and the gradients of a key-value head that several query heads
+// share are summed in the registers.
+//
+// Rows, tiles and products are the forward's (attn_fwd.hip): S^T = K Q^T and
+// dP^T = V dO^T give dS^T in the layout that dQ^T += K^T dS^T takes; in the
+// other kernel S = Q K^T and dP = dO V^T (rows down, keys across) give P and dS
+// as dV^T += dO^T P and dK^T += Q^T dS take them.
+//
+// Sinks. All later rows see the sinks, so the tile that holds them would walk
+// all rows. Its rows past the band go to workgroups of their own, in chunks;
+// their partial sums and the tile's own are joined in a fixed order.
+#include "attn_common.h"
+
+namespace trsc {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kRowsWg = 128, kKeysWg = 128;
+constexpr int kKeyTile = 64;      // keys of a tile of the dq kernel
+constexpr int kRowTile = 32;      // rows of a tile of the dk, dv kernel
+constexpr int kSinkChunk = 1024;  // rows of a sink workgroup
+
+template <class E, int NB>
+__device__ __forceinline__ void store_rows(E* p, const f32x16 (&acc)[NB], float f, int dim, int h) {
+  typedef E out4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+  for (int d = 0; d < NB; ++d)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int at = 32 * d + 8 * g + 4 * h;
+      if (at < dim) {
+        out4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = static_cast<E>(acc[d][4 * g + i] * f);
+        *reinterpret_cast<out4*>(p + at) = v;
+      }
+    }
+}
+
+// dq of one row by a whole wave, touching only the keys it sees.
+template <class E>
+__device__ void careful_dq(const AttnArgs& a, const Seq& q, const KeyTiles& kt, int tok, int head, int kvh,
+                           float lse2, float delta, int lane) {
+  const int64_t q_at = q.q0 + tok;
+  const int p = tok + q.lk - q.lq;
+  const float c = a.scale * kLog2e;
+  const float2 x = pair_of(static_cast<const E*>(a.q.p) + q_at * a.q.ts + head * a.q.hs, a.dim, lane);
+  const float2 g = pair_of(static_cast<const E*>(a.dout.p) + q_at * a.dout.ts + head * a.dout.hs, a.dim, lane);
+  float2 o = make_float2(0.f, 0.f);
+  for (int it = 0; it < kt.n; ++it) {
+    for (int j = kt.at(it) * kKeyTile, je = j + kKeyTile; j < je; ++j) {
+      if (!sees_key(a, p, j, q.lk)) continue;
+      const int64_t at = q.k0 + j;
+      const float2 y = pair_of(static_cast<const E*>(a.k.p) + at * a.k.ts + kvh * a.k.hs, a.dim, lane);
+      const float2 v = pair_of(static_cast<const E*>(a.v.p) + at * a.v.ts + kvh * a.v.hs, a.dim, lane);
+      const float s = wave_sum(x.x * y.x + x.y * y.y), dp = wave_sum(g.x * v.x + g.y * v.y);
+      const float ds = __builtin_amdgcn_exp2f(fmaf(s, c, -lse2)) * (dp - delta);
+      o.x += ds * y.x;
+      o.y += ds * y.y;
+    }
+  }
+  typedef E out2 __attribute__((ext_vector_type(2)));
+  if (2 * lane < a.dim)
+    *reinterpret_cast<out2*>(static_cast<E*>(a.dq) + (q_at * a.hq + head) * a.dim + 2 * lane) =
+        out2{static_cast<E>(o.x * a.scale), static_cast<E>(o.y * a.scale)};
+}
+
+// dk and dv (elements 2 lane, 2 lane + 1) of one key over the rows [r0, r1) by
+// a whole wave, touching only the rows that see it.
+template <class E>
+__device__ void careful_dkv(const AttnArgs& a, const Seq& q, int r0, int r1, int key, int kvh, float2& dk, float2& dv,
+                            int lane) {
+  const int group = a.hq / a.hk;
+  const float c = a.scale * kLog2e;
+  const int64_t at = q.k0 + key;
+  const float2 y = pair_of(static_cast<const E*>(a.k.p) + at * a.k.ts + kvh * a.k.hs, a.dim, lane);
+  const float2 v = pair_of(static_cast<const E*>(a.v.p) + at * a.v.ts + kvh * a.v.hs, a.dim, lane);
+  dk = dv = make_float2(0.f, 0.f);
+  for (int r = r0; r < r1; ++r) {
+    const int tok = r / group, head = kvh * group + r - tok * group;
+    if (!sees_key(a, tok + q.lk - q.lq, key, q.lk)) continue;
+    const int64_t q_at = q.q0 + tok;
+    const float2 x = pair_of(static_cast<const E*>(a.q.p) + q_at * a.q.ts + head * a.q.hs, a.dim, lane);
+    const float2 g = pair_of(static_cast<const E*>(a.dout.p) + q_at * a.dout.ts + head * a.dout.hs, a.dim, lane);
+    const float s = wave_sum(x.x * y.x + x.y * y.y), dp = wave_sum(g.x * v.x + g.y * v.y);
+    const float lse = a.lse[int64_t(head) * a.nq + q_at], delta = a.delta[int64_t(head) * a.nq + q_at];
+    const float p = __builtin_amdgcn_exp2f(fmaf(s, c, lse == -INFINITY ? 0.f : -lse * kLog2e));
+    const float ds = p * (dp - delta) * a.scale;
+    dv.x += p * g.x;
+    dv.y += p * g.y;
+    dk.x += ds * x.x;
+    dk.y += ds * x.y;
+  }
+}
+
+template <class E>
+__device__ __forceinline__ void store_pair(E* p, float2 v, int dim, int lane) {
+  typedef E out2 __attribute__((ext_vector_type(2)));
+  if (2 * lane < dim) *reinterpret_cast<out2*>(p + 2 * lane) = out2{static_cast<E>(v.x), static_cast<E>(v.y)};
+}
+
+// dq and delta: 128 rows a workgroup, 32 a wave.
+template <class E, int NB>
+__global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs a, int tiles) {
+  typedef Tile<E, NB> T;
+  typedef AttnType<E> A;
+  typedef typename A::frag frag;
+  constexpr int KB = kKeyTile / 32, ST = NB * 2;
+  constexpr int kTileBytes = kKeyTile * T::kPitch;
+  __shared__ __attribute__((aligned(1024))) unsigned char s_mem[4 * kTileBytes];
+  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = a.hq / a.hk;
+  const int w = xcd_remap(blockIdx.x, gridDim.x);
+  const int tile = w % tiles, kvh = w / tiles;
+  int inside;
+  const int b = find_sequence(a.cu_q, a.batch, group, kRowsWg, tile, &inside);
+  const Seq q = sequence(a, b);
+  const int rows = q.lq * group;
+  if (inside < 0 || inside > rows / kRowsWg) return;
+  const int r0 = inside * kRowsWg;
+  if (r0 >= rows) return;
+  const int last = min(rows - 1, r0 + kRowsWg - 1) / group;
+  const int shift = q.lk - q.lq;
+  const KeyTiles kt = key_tiles<kKeyTile>(a, r0 / group + shift, last + shift, q.lk);
+  const int wrow = r0 + 32 * wave, row = wrow + l32;
+  const bool on = row < rows, wave_on = wrow < rows;
+  const int tok = on ? row / group : last, head = kvh * group + (on ? row - tok * group : 0);
+  const int p = tok + shift, lo = p - a.left, hi = min(p + a.right, q.lk - 1);
+  const int pw0 = min(wrow, rows - 1) / group + shift, pw1 = min(wrow + 31, rows - 1) / group + shift;
+  const int64_t q_at = q.q0 + tok;
+  frag qf[ST], df[ST];
+  float delta = 0.f;
+  {
+    const E* qp = static_cast<const E*>(a.q.p) + q_at * a.q.ts + head * a.q.hs;
+    const E* dp = static_cast<const E*>(a.dout.p) + q_at * a.dout.ts + head * a.dout.hs;
+    const E* op = static_cast<const E*>(a.o.p) + q_at * a.o.ts + head * a.o.hs;
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+      qf[s] = row_from<E>(qp, on, s, a.dim, lane);
+      df[s] = row_from<E>(dp, on, s, a.dim, lane);
+      const frag of = row_from<E>(op, on, s, a.dim, lane);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) delta = fmaf(float(of[e]), float(df[s][e]), delta);
+    }
+  }
+  delta += __shfl_xor(delta, 32);
+  const int64_t stat = int64_t(head) * a.nq + q_at;
+  if (on && h == 0) a.delta[stat] = delta;
+  const float lse = on ? a.lse[stat] : 0.f;
+  const float lse2 = lse == -INFINITY ? 0.f : lse * kLog2e;
+  const E* kbase = static_cast<const E*>(a.k.p) + int64_t(q.k0) * a.k.ts + kvh * a.k.hs;
+  const E* vbase = static_cast<const E*>(a.v.p) + int64_t(q.k0) * a.v.ts + kvh * a.v.hs;
+  f32x16 acc[NB];
+#pragma unroll
+  for (int d = 0; d < NB; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[d][e] = 0.f;
+  const float c = a.scale * kLog2e;
+
+  auto fetch = [&](int it, int buf) {
+    const int t0 = kt.at(it) * kKeyTile;
+    unsigned char* dst = s_mem + buf * 2 * kTileBytes;
+    T::template copy<kKeyTile, 4>(dst, kbase, a.k.ts, t0, q.lk, a.dim, wave, lane);
+    T::template copy<kKeyTile, 4>(dst + kTileBytes, vbase, a.v.ts, t0, q.lk, a.dim, wave, lane);
+  };
+  auto compute = [&](int it, int buf) {
+    const unsigned char* ks = s_mem + buf * 2 * kTileBytes;
+    const unsigned char* vs = ks + kTileBytes;
+    const int jt = kt.at(it) * kKeyTile;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      const int j0 = jt + 32 * kb, j1 = j0 + 31;
+      if (!wave_on || j0 >= q.lk || j0 > pw1 + a.right || (j1 < pw0 - a.left && j0 >= a.sinks)) continue;
+      const bool all = j1 <= pw0 + a.right && j1 < q.lk && (j0 >= pw1 - a.left || j1 < a.sinks);
+      f32x16 s, dp;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[e] = dp[e] = 0.f;
+#pragma unroll
+      for (int st = 0; st < ST; ++st) s = A::mma(T::row(ks, 32 * kb, st, lane), qf[st], s);
+#pragma unroll
+      for (int st = 0; st < ST; ++st) dp = A::mma(T::row(vs, 32 * kb, st, lane), df[st], dp);
+      if (all) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lse2)) * (dp[e] - delta);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int j = j0 + 4 * h + 8 * (e >> 2) + (e & 3);
+          const bool sees = j <= hi && (j >= lo || j < a.sinks);
+          const float ds = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lse2)) * (dp[e] - delta);
+          s[e] = sees ? ds : 0.f;
+        }
+      }
+#pragma unroll
+      for (int ss = 0; ss < 2; ++ss) {
+        const frag sf = pack_frag8<E>(s, ss);
+#pragma unroll
+        for (int d = 0; d < NB; ++d) acc[d] = A::mma(T::col(ks, 32 * kb, ss, d, lane), sf, acc[d]);
+      }
+    }
+  };
+  if (kt.n > 0) fetch(0, 0);
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  for (int it = 0; it < kt.n; ++it) {
+    if (it + 1 < kt.n) fetch(it + 1, (it & 1) ^ 1);
+    compute(it, it & 1);
+    __builtin_amdgcn_s_waitcnt(0);
+    bare_barrier();
+  }
+  const uint32_t bad = bad_rows(on ? zero_if_finite<NB>(acc) : 0.f);
+  if (on && !((bad >> l32) & 1u))
+    store_rows<E, NB>(static_cast<E*>(a.dq) + (q_at * a.hq + head) * a.dim, acc, a.scale, a.dim, h);
+  if (bad != 0) {
+    for (int i = 0; i < 32; ++i) {
+      if (!((bad >> i) & 1u)) continue;
+      careful_dq<E>(a, q, kt, __shfl(tok, i), __shfl(head, i), kvh, __shfl(lse2, i), __shfl(delta, i), lane);
+    }
+  }
+}
+
+// Token `t` as a bound of a sequence's tokens [0, lq].
+__device__ __forceinline__ int token_at(int64_t t, int lq) { return t < 0 ? 0 : t > lq ? lq : int(t); }
+
+// What a tile's rows need besides their elements.
+struct RowStats {
+  float lse2[kRowTile], delta[kRowTile];
+  int pos[kRowTile];  // position, or far below every window for a row that is not there
+};
+constexpr int kNoRow = -(1 << 30);  // kNoRow + right < 0, and kNoRow - left does not wrap
+
+// dk and dv of 32 keys a wave. SINK = false: 128 keys a workgroup, the four
+// waves take 32 each and share the row tiles. SINK = true: 32 keys (of the
+// sinks) a workgroup, the rows past the band, one chunk; every wave walks row
+// tiles of its own, and the four sums are joined at the end.
+template <class E, int NB, bool SINK>
+__global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs a, int tiles) {
+  typedef Tile<E, NB> T;
+  typedef AttnType<E> A;
+  typedef typename A::frag frag;
+  constexpr int ST = NB * 2;
+  constexpr int kTileBytes = kRowTile * T::kPitch;
+  constexpr int kSets = SINK ? 4 : 1;                       // LDS tile sets: a wave's own, or shared
+  constexpr int kBuffers = SINK && sizeof(E) == 4 ? 1 : 2;
+  constexpr int kLds = kSets * kBuffers * 2 * kTileBytes;
+  constexpr int kJoin = SINK ? 3 * 2 * NB * 16 * 64 * 4 : 0;  // the waves' sums at the end
+  __shared__ __attribute__((aligned(1024))) unsigned char s_mem[kLds > kJoin ? kLds : kJoin];
+  __shared__ RowStats s_stat[kSets * kBuffers];
+  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = a.hq / a.hk;
+  const int sink_blocks = (a.sinks + 31) / 32;
+  const int w = xcd_remap(blockIdx.x, gridDim.x);
+  const int tile = w % tiles, kvh = (w / tiles) % a.hk, sink_block = w / tiles / a.hk;
+  int inside;
+  const int b = SINK ? find_sequence(a.cu_q, a.batch, group, kSinkChunk, tile, &inside)
+                     : find_sequence(a.cu_k, a.batch, 1, kKeysWg, tile, &inside);
+  const Seq q = sequence(a, b);
+  const int shift = q.lk - q.lq, rows = q.lq * group;
+  if (inside < 0) return;
+  int j0, r_begin, r_end, cap = 0;
+  // rows that see a key of the tile [0, kKeysWg) inside the band end here
+  const int band_end = token_at(int64_t(kKeysWg) + a.left - shift, q.lq) * group;
+  if constexpr (SINK) {
+    if (inside > rows / kSinkChunk) return;
+    j0 = 32 * sink_block;
+    r_begin = max(inside * kSinkChunk, band_end);
+    r_end = min((inside + 1) * kSinkChunk, rows);
+    if (r_begin >= r_end) return;  // a chunk that nothing reads
+  } else {
+    cap = a.cu_k ? clamp_to(a.cu_k[b + 1], q.k0, a.nk) - q.k0 : a.nk;
+    if (inside > cap / kKeysWg) return;
+    j0 = inside * kKeysWg;
+    if (j0 >= cap) return;
+    const int last = min(j0 + kKeysWg, q.lk) - 1;
+    r_begin = token_at(int64_t(j0) - a.right - shift, q.lq) * group;
+    r_end = token_at(int64_t(last) + a.left - shift + 1, q.lq) * group;
+    if (j0 == 0 && a.sinks > 0) r_end = band_end;
+    if (j0 >= q.lk) r_end = r_begin;
+  }
+  const int jw = SINK ? j0 : j0 + 32 * wave, key = jw + l32;  // this wave's keys, this lane's
+  const bool key_on = key < q.lk && (!SINK || key < a.sinks);
+  frag kf[ST], vf[ST];
+  {
+    const int64_t at = q.k0 + (key_on ? key : 0);
+    const E* kp = static_cast<const E*>(a.k.p) + at * a.k.ts + kvh * a.k.hs;
+    const E* vp = static_cast<const E*>(a.v.p) + at * a.v.ts + kvh * a.v.hs;
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+      kf[s] = row_from<E>(kp, key_on, s, a.dim, lane);
+      vf[s] = row_from<E>(vp, key_on, s, a.dim, lane);
+    }
+  }
+  f32x16 dk[NB], dv[NB];
+#pragma unroll
+  for (int d = 0; d < NB; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) dk[d][e] = dv[d][e] = 0.f;
+  const float c = a.scale * kLog2e;
+  const int n_tiles = r_end > r_begin ? (r_end - r_begin + kRowTile - 1) / kRowTile : 0;
+  const E* qbase = static_cast<const E*>(a.q.p) + int64_t(q.q0) * a.q.ts + int64_t(kvh) * group * a.q.hs;
+  const E* dbase = static_cast<const E*>(a.dout.p) + int64_t(q.q0) * a.dout.ts + int64_t(kvh) * group * a.dout.hs;
+
+  auto fetch = [&](int it, int set) {
+    unsigned char* dst = s_mem + set * 2 * kTileBytes;
+    const int t0 = r_begin + it * kRowTile;
+#pragma unroll
+    for (int j = 0; j < kRowTile / T::kRowsPerCopy; j += SINK ? 1 : 4) {
+      const int n = SINK ? j : j + wave;
+      if (n >= kRowTile / T::kRowsPerCopy) break;
+      const int rr = n * T::kRowsPerCopy + lane / T::kChunks;
+      const int chunk = (lane % T::kChunks) ^ T::key(rr);
+      const int r = t0 + rr;
+      const bool in = r < r_end && chunk * T::kPer < a.dim;
+      const int tok = in ? r / group : 0, g = in ? r - tok * group : 0;
+      const void* gq = in ? static_cast<const void*>(qbase + tok * a.q.ts + g * a.q.hs + chunk * T::kPer)
+                          : static_cast<const void*>(g_attn_zeros);
+      const void* gd = in ? static_cast<const void*>(dbase + tok * a.dout.ts + g * a.dout.hs + chunk * T::kPer)
+                          : static_cast<const void*>(g_attn_zeros);
+      copy16_to_lds(gq, dst + n * 1024);
+      copy16_to_lds(gd, dst + kTileBytes + n * 1024);
+    }
+    if ((SINK || wave == 3) && lane < kRowTile) {
+      const int r = t0 + lane;
+      const bool in = r < r_end;
+      const int tok = in ? r / group : 0, g = in ? r - tok * group : 0;
+      const int64_t at = int64_t(kvh * group + g) * a.nq + q.q0 + tok;
+      const float lse = in ? a.lse[at] : 0.f;
+      s_stat[set].lse2[lane] = lse == -INFINITY ? 0.f : lse * kLog2e;
+      s_stat[set].delta[lane] = in ? a.delta[at] : 0.f;
+      s_stat[set].pos[lane] = in ? tok + shift : kNoRow;
+    }
+  };
+  auto compute = [&](int it, int set) {
+    const unsigned char* qs = s_mem + set * 2 * kTileBytes;
+    const unsigned char* ds_ = qs + kTileBytes;
+    const int t0 = r_begin + it * kRowTile;
+    const int p0 = t0 / group + shift, p1 = min(t0 + kRowTile - 1, r_end - 1) / group + shift;
+    const int j1 = jw + 31;
+    if (jw >= q.lk || jw > p1 + a.right || (j1 < p0 - a.left && jw >= a.sinks)) return;
+    const bool all = t0 + kRowTile <= r_end && j1 <= p0 + a.right && j1 < q.lk &&
+                     (jw >= p1 - a.left || j1 < a.sinks);
+    f32x16 s, dp;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] = dp[e] = 0.f;
+#pragma unroll
+    for (int st = 0; st < ST; ++st) s = A::mma(T::row(qs, 0, st, lane), kf[st], s);
+#pragma unroll
+    for (int st = 0; st < ST; ++st) dp = A::mma(T::row(ds_, 0, st, lane), vf[st], dp);
+    const RowStats& rs = s_stat[set];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int at = 8 * g + 4 * h;
+      const float4 ls = *reinterpret_cast<const float4*>(&rs.lse2[at]);
+      const float4 de = *reinterpret_cast<const float4*>(&rs.delta[at]);
+      const float lv[4] = {ls.x, ls.y, ls.z, ls.w}, ev[4] = {de.x, de.y, de.z, de.w};
+      if (all) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = 4 * g + i;
+          s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lv[i]));
+          dp[e] = s[e] * (dp[e] - ev[i]);
+        }
+      } else {
+        const int4 po = *reinterpret_cast<const int4*>(&rs.pos[at]);
+        const int pv[4] = {po.x, po.y, po.z, po.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = 4 * g + i;
+          const bool sees = key_on && key <= pv[i] + a.right && (key >= pv[i] - a.left || key < a.sinks);
+          const float pr = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lv[i]));
+          s[e] = sees ? pr : 0.f;
+          dp[e] = sees ? pr * (dp[e] - ev[i]) : 0.f;
+        }
+      }
+    }
+#pragma unroll
+    for (int ss = 0; ss < 2; ++ss) {
+      const frag pf = pack_frag8<E>(s, ss);
+#pragma unroll
+      for (int d = 0; d < NB; ++d) dv[d] = A::mma(T::col(ds_, 0, ss, d, lane), pf, dv[d]);
+    }
+#pragma unroll
+    for (int ss = 0; ss < 2; ++ss) {
+      const frag sf = pack_frag8<E>(dp, ss);
+#pragma unroll
+      for (int d = 0; d < NB; ++d) dk[d] = A::mma(T::col(qs, 0, ss, d, lane), sf, dk[d]);
+    }
+  };
+  if constexpr (!SINK) {
+    if (n_tiles > 0) fetch(0, 0);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    for (int it = 0; it < n_tiles; ++it) {
+      if (it + 1 < n_tiles) fetch(it + 1, (it & 1) ^ 1);
+      compute(it, it & 1);
+      __builtin_amdgcn_s_waitcnt(0);
+      bare_barrier();
+    }
+    const uint32_t bad = bad_rows(key < cap ? zero_if_finite<NB>(dk) + zero_if_finite<NB>(dv) : 0.f);
+    for (uint32_t left = bad; left != 0; left &= left - 1) {
+      const int j = jw + __builtin_ctz(left);
+      float2 gk, gv;
+      careful_dkv<E>(a, q, r_begin, r_end, j, kvh, gk, gv, lane);
+      if (j < a.sinks) {
+        float* dst = a.sink_part + ((int64_t(b) * a.hk + kvh) * a.sinks + j) * 2 * a.dim;
+        store_pair<float>(dst, gk, a.dim, lane);
+        store_pair<float>(dst + a.dim, gv, a.dim, lane);
+      } else {
+        const int64_t at = (int64_t(q.k0 + j) * a.hk + kvh) * a.dim;
+        store_pair<E>(static_cast<E*>(a.dk) + at, gk, a.dim, lane);
+        store_pair<E>(static_cast<E*>(a.dv) + at, gv, a.dim, lane);
+      }
+    }
+    if (key < cap && !((bad >> l32) & 1u)) {
+      // a key of the sinks: its sum is joined with those of the later rows
+      const bool joined = key < a.sinks;
+      if (!joined) {
+        const int64_t at = (int64_t(q.k0 + key) * a.hk + kvh) * a.dim;
+        store_rows<E, NB>(static_cast<E*>(a.dk) + at, dk, a.scale, a.dim, h);
+        store_rows<E, NB>(static_cast<E*>(a.dv) + at, dv, 1.f, a.dim, h);
+      } else {
+        float* dst = a.sink_part + ((int64_t(b) * a.hk + kvh) * a.sinks + key) * 2 * a.dim;
+        store_rows<float, NB>(dst, dk, a.scale, a.dim, h);
+        store_rows<float, NB>(dst + a.dim, dv, 1.f, a.dim, h);
+      }
+    }
+  } else {
+    int it = wave;
+    if constexpr (kBuffers == 2) {
+      int buf = 0;
+      if (it < n_tiles) fetch(it, wave * 2);
+      for (; it < n_tiles; it += 4) {
+        __builtin_amdgcn_s_waitcnt(0);
+        asm volatile("" ::: "memory");
+        if (it + 4 < n_tiles) fetch(it + 4, wave * 2 + (buf ^ 1));
+        compute(it, wave * 2 + buf);
+        buf ^= 1;
+      }
+    } else {
+      for (; it < n_tiles; it += 4) {
+        __builtin_amdgcn_s_waitcnt(0);
+        asm volatile("" ::: "memory");
+        fetch(it, wave);
+        __builtin_amdgcn_s_waitcnt(0);
+        asm volatile("" ::: "memory");
+        compute(it, wave);
+      }
+    }
+    // waves 1 - 3 hand over, wave 0 adds in wave order
+    float* red = reinterpret_cast<float*>(s_mem);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (wave > 0) {
+#pragma unroll
+      for (int d = 0; d < NB; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          red[(((wave - 1) * 2 * NB + d) * 16 + e) * 64 + lane] = dk[d][e];
+          red[(((wave - 1) * 2 * NB + NB + d) * 16 + e) * 64 + lane] = dv[d][e];
+        }
+    }
+    __syncthreads();
+    if (wave == 0) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+#pragma unroll
+        for (int d = 0; d < NB; ++d)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            dk[d][e] += red[((i * 2 * NB + d) * 16 + e) * 64 + lane];
+            dv[d][e] += red[((i * 2 * NB + NB + d) * 16 + e) * 64 + lane];
+          }
+      float* const slot = a.sink_part + (int64_t(a.batch + tile) * a.hk + kvh) * a.sinks * 2 * a.dim;
+      const uint32_t bad = bad_rows(key < a.sinks ? zero_if_finite<NB>(dk) + zero_if_finite<NB>(dv) : 0.f);
+      for (uint32_t left = bad; left != 0; left &= left - 1) {
+        const int j = jw + __builtin_ctz(left);
+        float2 gk, gv;
+        careful_dkv<E>(a, q, r_begin, r_end, j, kvh, gk, gv, lane);
+        store_pair<float>(slot + int64_t(j) * 2 * a.dim, gk, a.dim, lane);
+        store_pair<float>(slot + int64_t(j) * 2 * a.dim + a.dim, gv, a.dim, lane);
+      }
+      if (key < a.sinks && !((bad >> l32) & 1u)) {
+        float* dst = slot + int64_t(key) * 2 * a.dim;
+        store_rows<float, NB>(dst, dk, a.scale, a.dim, h);
+        store_rows<float, NB>(dst + a.dim, dv, 1.f, a.dim, h);
+      }
+    }
+  }
+}
+
+// dk, dv of the sinks: the tile's own sums plus the chunks' in chunk order. One
+// wave a (sequence, kv head, sink).
+template <class E>
+__global__ __launch_bounds__(256) void attn_sinks(AttnArgs a, int chunks) {
+  const int64_t i = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (i >= int64_t(a.batch) * a.hk * a.sinks) return;
+  const int key = int(i % a.sinks), kvh = int(i / a.sinks % a.hk), b = int(i / a.sinks / a.hk);
+  const Seq q = sequence(a, b);
+  const int cap = a.cu_k ? clamp_to(a.cu_k[b + 1], q.k0, a.nk) - q.k0 : a.nk;
+  if (key >= cap) return;
+  const int group = a.hq / a.hk, rows = q.lq * group;
+  const int shift = q.lk - q.lq;
+  const int band_end = token_at(int64_t(kKeysWg) + a.left - shift, q.lq) * group;
+  const int base = a.cu_q ? first_tile(a.cu_q, b, group, kSinkChunk) : 0;
+  const int c0 = band_end / kSinkChunk, c1 = rows > band_end ? (rows + kSinkChunk - 1) / kSinkChunk : c0;
+  const int64_t slot = int64_t(a.hk) * a.sinks * 2 * a.dim;
+  const int64_t in = (int64_t(kvh) * a.sinks + key) * 2 * a.dim;
+  const int64_t out = (int64_t(q.k0 + key) * a.hk + kvh) * a.dim;
+  for (int d = lane; d < 2 * a.dim; d += 64) {
+    float v = a.sink_part[b * slot + in + d];
+    for (int t = c0; t < c1; ++t) v += a.sink_part[(a.batch + clamp_to(base + t, 0, chunks - 1)) * slot + in + d];
+    E* dst = static_cast<E*>(d < a.dim ? a.dk : a.dv);
+    dst[out + (d < a.dim ? d : d - a.dim)] = static_cast<E>(v);
+  }
+}
+
+template <class E, int NB>
+hipError_t launch_shape(const AttnArgs& a, hipStream_t st) {
+  const int group = a.hq / a.hk;
+  if (a.nq > 0) {
+    const int64_t tiles = tiles_of(a.nq, a.batch, group, kRowsWg);
+    if (tiles * a.hk >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+    attn_dq<E, NB><<<unsigned(tiles * a.hk), 256, 0, st>>>(a, int(tiles));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.nk == 0) return hipSuccess;
+  const int64_t tiles = tiles_of(a.nk, a.batch, 1, kKeysWg);
+  if (tiles * a.hk >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+  attn_dkv<E, NB, false><<<unsigned(tiles * a.hk), 256, 0, st>>>(a, int(tiles));
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.sinks == 0) return e;
+  if (a.nq > 0) {
+    const int64_t chunks = tiles_of(a.nq, a.batch, group, kSinkChunk);
+    const int64_t wgs = chunks * a.hk * ((a.sinks + 31) / 32);
+    if (wgs >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+    attn_dkv<E, NB, true><<<unsigned(wgs), 256, 0, st>>>(a, int(chunks));
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const int64_t n = int64_t(a.batch) * a.hk * a.sinks;
+  attn_sinks<E><<<unsigned((n + 3) / 4), 256, 0, st>>>(a, int(tiles_of(a.nq, a.batch, group, kSinkChunk)));
+  return hipGetLastError();
+}
+
+template <class E>
+hipError_t launch_type(const AttnArgs& a, hipStream_t st) {
+  switch ((a.dim + 31) / 32) {
+    case 1: return launch_shape<E, 1>(a, st);
+    case 2: return launch_shape<E, 2>(a, st);
+    case 3: return launch_shape<E, 3>(a, st);
+    default: return launch_shape<E, 4>(a, st);
+  }
+}
+
+}  // namespace
+
+size_t attention_backward_delta_floats(const AttnArgs& a) { return size_t(a.hq) * a.nq; }
+
+size_t attention_backward_sink_floats(const AttnArgs& a) {
+  if (a.sinks == 0) return 0;
+  const int64_t slots = a.batch + tiles_of(a.nq, a.batch, a.hq / a.hk, kSinkChunk);
+  return size_t(slots) * a.hk * a.sinks * 2 * a.dim;
+}
+
+hipError_t launch_attention_backward(const AttnArgs& a, hipStream_t st) {
+  if (a.dtype == TR_SC_BF16) return launch_type<__bf16>(a, st);
+  if (a.dtype == TR_SC_F16) return launch_type<_Float16>(a, st);
+  return launch_type<float>(a, st);
+}
+
+}  // namespace trsc

@@ -1,0 +1,467 @@
+// Windowed attention with sinks, forward: prompts and packed objects, and
+// single tokens against a cache.
+//
+// Mathematics. Row i of a sequence (Lq queries, Lk keys) stands at
+// p = i + Lk - Lq and sees key j when j <= p + right and (j >= p - left or
+// j < sinks). o = sum_j e^{scale q.k_j - lse} v_j over the keys it sees, lse the
+// log of the sum of the exponentials. One pass over the keys with the running
+// maximum m and sum l: e^{scale (s - m)} is taken as 2^{(s - m) c},
+// c = scale log2 e.
+//
+// Rows. The queries of the heads that share a key-value head are one matrix:
+// row r of a sequence is token r / G, head r % G of the group (G = q heads / kv
+// heads). A workgroup takes 128 consecutive rows of one kv head, 32 a wave.
+//
+// Products. S^T = K Q^T (keys down, queries across), so a lane holds scores of
+// one query only: the maximum and the sum need one exchange between the two
+// halves of the wave, the rescaling none. The registers of S^T are, as they
+// are, fragments of P^T for O^T += V^T P^T when V's keys are taken in the same
+// order, which the transposed LDS read of V gives (attn_common.h).
+#include "attn_common.h"
+
+namespace trsc {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// max / sum with the other half of the wave (lane ^ 32)
+__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
+
+// The scores of 32 keys j0 + 8 g + 4 (lane / 32) + i: hidden ones become -inf.
+__device__ __forceinline__ void hide(f32x16& s, int j0, int lo, int hi, int sinks, int lane) {
+  const int base = j0 + 4 * (lane >> 5);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int j = base + 8 * (e >> 2) + (e & 3);
+    const bool sees = j <= hi && (j >= lo || j < sinks);
+    s[e] = sees ? s[e] : -INFINITY;
+  }
+}
+
+// Result of one row: elements 2 lane, 2 lane + 1 (already divided by the sum),
+// and the base-2 log of the sum.
+template <class E>
+__device__ __forceinline__ void store_row(const AttnArgs& a, int splits, int split, int head, int64_t q_at, float2 o,
+                                          float lg, int lane) {
+  typedef E out2 __attribute__((ext_vector_type(2)));
+  const bool in = 2 * lane < a.dim;
+  if (splits == 1) {
+    E* op = static_cast<E*>(const_cast<void*>(a.o.p)) + q_at * a.o.ts + head * a.o.hs + 2 * lane;
+    if (in) *reinterpret_cast<out2*>(op) = out2{static_cast<E>(o.x), static_cast<E>(o.y)};
+    if (a.lse != nullptr && lane == 0) a.lse[int64_t(head) * a.nq + q_at] = lg * 0.6931471805599453f;
+  } else {
+    const int64_t at = (int64_t(split) * a.hq + head) * a.nq + q_at;
+    if (in) *reinterpret_cast<float2*>(a.part + at * a.dim + 2 * lane) = o;
+    if (lane == 0) a.part[int64_t(splits) * a.hq * a.nq * a.dim + at] = lg;
+  }
+}
+
+// One row over the key tiles [first, end), touching only the keys it sees.
+template <class E, int KT>
+__device__ void careful_row(const AttnArgs& a, const Seq& q, const KeyTiles& kt, int first, int end, int splits,
+                            int split, int tok, int head, int kvh, int lane) {
+  const int64_t q_at = q.q0 + tok;
+  const int p = tok + q.lk - q.lq;
+  const float c = a.scale * kLog2e;
+  const float2 x = pair_of(static_cast<const E*>(a.q.p) + q_at * a.q.ts + head * a.q.hs, a.dim, lane);
+  float2 o = make_float2(0.f, 0.f);
+  float m = -INFINITY, l = 0.f;
+  for (int it = first; it < end; ++it) {
+    for (int j = kt.at(it) * KT, je = j + KT; j < je; ++j) {
+      if (!sees_key(a, p, j, q.lk)) continue;
+      const int64_t at = q.k0 + j;
+      const float2 y = pair_of(static_cast<const E*>(a.k.p) + at * a.k.ts + kvh * a.k.hs, a.dim, lane);
+      const float2 v = pair_of(static_cast<const E*>(a.v.p) + at * a.v.ts + kvh * a.v.hs, a.dim, lane);
+      const float s = wave_sum(x.x * y.x + x.y * y.y);
+      const float mx = fmaxf(m, s), ms = mx == -INFINITY ? 0.f : mx;
+      const float f = __builtin_amdgcn_exp2f((m - ms) * c), w = __builtin_amdgcn_exp2f((s - ms) * c);
+      if (f != 1.f) {
+        l *= f;
+        o.x *= f;
+        o.y *= f;
+      }
+      m = mx;
+      l += w;
+      o.x += w * v.x;
+      o.y += w * v.y;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float lg = l == 0.f ? -INFINITY : m * c + __builtin_amdgcn_logf(l);
+  store_row<E>(a, splits, split, head, q_at, make_float2(o.x * inv, o.y * inv), lg, lane);
+}
+
+template <class E, int NB, bool TOKEN>
+struct FwdShape {
+  typedef Tile<E, NB> T;
+  static constexpr int kKeys = TOKEN ? 32 : 64;
+  static constexpr int kTileBytes = kKeys * T::kPitch;
+  // token form: every wave has its own tiles
+  static constexpr int kBuffers = (TOKEN && sizeof(E) == 4 && NB > 2) ? 1 : 2;
+  static constexpr int kWaveSets = TOKEN ? 4 : 1;
+  static constexpr int kLds = kBuffers * 2 * kTileBytes * kWaveSets;
+  static constexpr int kRows = TOKEN ? 32 : 128;
+};
+
+template <class E, int NB, bool TOKEN>
+__global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_fwd(AttnArgs a, int tiles, int splits) {
+  typedef FwdShape<E, NB, TOKEN> F;
+  typedef Tile<E, NB> T;
+  typedef AttnType<E> A;
+  typedef typename A::frag frag;
+  constexpr int KB = F::kKeys / 32, ST = NB * 2;
+  __shared__ __attribute__((aligned(1024))) unsigned char s_mem[F::kLds];
+  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = a.hq / a.hk;
+
+  const int w = xcd_remap(blockIdx.x, gridDim.x);
+  const int tile = w % tiles, kvh = (w / tiles) % a.hk, split = w / tiles / a.hk;
+  int inside;
+  const int b = find_sequence(a.cu_q, a.batch, group, F::kRows, tile, &inside);
+  const Seq q = sequence(a, b);
+  const int rows = q.lq * group;  // < 2^31 - 2^8 (checked by the caller)
+  if (inside < 0 || inside > rows / F::kRows) return;
+  const int r0 = inside * F::kRows;
+  if (r0 >= rows) return;
+  const int last = min(rows - 1, r0 + F::kRows - 1) / group;
+  const int shift = q.lk - q.lq;
+  const KeyTiles kt = key_tiles<F::kKeys>(a, r0 / group + shift, last + shift, q.lk);
+
+  // this lane's row
+  const int wrow = r0 + (TOKEN ? 0 : 32 * wave);  // the wave's first row
+  const int row = wrow + l32;
+  const bool on = row < rows;
+  const int tok = on ? row / group : last, head = kvh * group + (on ? row - tok * group : 0);
+  const int p = tok + shift, lo = p - a.left, hi = min(p + a.right, q.lk - 1);
+  const int pw0 = min(wrow, rows - 1) / group + shift, pw1 = min(wrow + 31, rows - 1) / group + shift;
+  const bool wave_on = wrow < rows;
+  frag qf[ST];
+  {
+    const E* qp = static_cast<const E*>(a.q.p) + int64_t(q.q0 + tok) * a.q.ts + head * a.q.hs;
+#pragma unroll
+    for (int s = 0; s < ST; ++s) qf[s] = row_from<E>(qp, on, s, a.dim, lane);
+  }
+  const E* kbase = static_cast<const E*>(a.k.p) + int64_t(q.k0) * a.k.ts + kvh * a.k.hs;
+  const E* vbase = static_cast<const E*>(a.v.p) + int64_t(q.k0) * a.v.ts + kvh * a.v.hs;
+
+  f32x16 acc[NB];
+#pragma unroll
+  for (int d = 0; d < NB; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[d][e] = 0.f;
+  float m = -INFINITY, l = 0.f;
+  const float c = a.scale * kLog2e;
+
+  const int first = int(int64_t(kt.n) * split / splits), end = int(int64_t(kt.n) * (split + 1) / splits);
+  unsigned char* const mem = s_mem + (TOKEN ? wave * F::kBuffers * 2 * F::kTileBytes : 0);
+  auto fetch = [&](int it, int buf) {
+    const int t0 = kt.at(it) * F::kKeys;
+    unsigned char* dst = mem + buf * 2 * F::kTileBytes;
+    T::template copy<F::kKeys, TOKEN ? 1 : 4>(dst, kbase, a.k.ts, t0, q.lk, a.dim, TOKEN ? 0 : wave, lane);
+    T::template copy<F::kKeys, TOKEN ? 1 : 4>(dst + F::kTileBytes, vbase, a.v.ts, t0, q.lk, a.dim, TOKEN ? 0 : wave,
+                                              lane);
+  };
+  auto compute = [&](int it, int buf) {
+    const unsigned char* ks = mem + buf * 2 * F::kTileBytes;
+    const unsigned char* vs = ks + F::kTileBytes;
+    const int j0 = kt.at(it) * F::kKeys, j1 = j0 + F::kKeys - 1;
+    // nothing of the tile, or all of it, seen by every row of the wave
+    if (!wave_on || j0 > pw1 + a.right || (j1 < pw0 - a.left && j0 >= a.sinks)) return;
+    const bool all = j1 <= pw0 + a.right && j1 < q.lk && (j0 >= pw1 - a.left || j1 < a.sinks);
+    f32x16 s[KB];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[kb][e] = 0.f;
+#pragma unroll
+      for (int st = 0; st < ST; ++st) s[kb] = A::mma(T::row(ks, 32 * kb, st, lane), qf[st], s[kb]);
+    }
+    if (!all) {
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) hide(s[kb], j0 + 32 * kb, lo, hi, a.sinks, lane);
+    }
+    float mx = m;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[kb][e]);
+    mx = fmaxf(mx, other_half(mx));
+    const float ms = mx == -INFINITY ? 0.f : mx;  // a row that has seen nothing yet
+    if (__any(mx != m)) {
+      const float f = __builtin_amdgcn_exp2f((m - ms) * c);
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < NB; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[d][e] *= f;
+      m = mx;
+    }
+    const float mc = ms * c;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        s[kb][e] = __builtin_amdgcn_exp2f(fmaf(s[kb][e], c, -mc));
+        l += s[kb][e];
+      }
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int ss = 0; ss < 2; ++ss) {
+        const frag pf = pack_frag8<E>(s[kb], ss);
+#pragma unroll
+        for (int d = 0; d < NB; ++d) acc[d] = A::mma(T::col(vs, 32 * kb, ss, d, lane), pf, acc[d]);
+      }
+  };
+
+  if constexpr (!TOKEN) {
+    if (first < end) fetch(first, 0);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    for (int it = first; it < end; ++it) {
+      const int buf = (it - first) & 1;
+      if (it + 1 < end) fetch(it + 1, buf ^ 1);
+      compute(it, buf);
+      __builtin_amdgcn_s_waitcnt(0);
+      bare_barrier();
+    }
+  } else {
+    // each wave its own tiles and LDS: no barrier in the loop
+    constexpr int NBUF = F::kBuffers;
+    int it = first + wave, buf = 0;
+    if (NBUF == 2 && it < end) fetch(it, 0);
+    for (; it < end; it += 4) {
+      if constexpr (NBUF == 2) {
+        __builtin_amdgcn_s_waitcnt(0);
+        asm volatile("" ::: "memory");
+        if (it + 4 < end) fetch(it + 4, buf ^ 1);
+        compute(it, buf);
+        buf ^= 1;
+      } else {
+        __builtin_amdgcn_s_waitcnt(0);  // the last tile's reads are done
+        fetch(it, 0);
+        __builtin_amdgcn_s_waitcnt(0);
+        asm volatile("" ::: "memory");
+        compute(it, 0);
+      }
+    }
+  }
+  l += other_half(l);
+  bool writer = true;
+  if constexpr (TOKEN) {
+    // the four waves hold the same rows over different keys: join them in wave
+    // order; wave w sums the blocks d = w, w + 4, ...
+    float* red = reinterpret_cast<float*>(s_mem);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (lane < 32) {
+      red[wave * 64 + lane] = m;
+      red[wave * 64 + 32 + lane] = l;
+    }
+    __syncthreads();
+    float mm = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mm = fmaxf(mm, red[i * 64 + l32]);
+    float f[4], ll = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float mi = red[i * 64 + l32];
+      f[i] = mi == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((mi - mm) * c);
+      ll += f[i] * red[i * 64 + 32 + l32];
+    }
+    const float mine = f[0] * (wave == 0) + f[1] * (wave == 1) + f[2] * (wave == 2) + f[3] * (wave == 3);
+    const bool any = m != -INFINITY;
+    m = mm;
+    l = ll;
+    __syncthreads();
+#pragma unroll
+    for (int d = 0; d < NB; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) red[((wave * NB + d) * 16 + e) * 64 + lane] = any ? acc[d][e] * mine : 0.f;
+    __syncthreads();
+    writer = wave < NB;
+    if (writer) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v += red[((i * NB + wave) * 16 + e) * 64 + lane];
+        acc[0][e] = v;
+      }
+    }
+  }
+  // rows whose sums are not finite, again without what they do not see
+  {
+    float t = 0.f;
+    if (writer && on) {
+      if constexpr (TOKEN) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) t = fmaf(acc[0][e], 0.f, t);
+      } else {
+        t = zero_if_finite<NB>(acc);
+      }
+    }
+    uint32_t bad = bad_rows(t);
+    if constexpr (TOKEN) {  // each wave has seen some of the columns: the rows of all four, shared out
+      uint32_t* flags = reinterpret_cast<uint32_t*>(s_mem);
+      __syncthreads();
+      if (lane == 0) flags[wave] = bad;
+      __syncthreads();
+      bad = flags[0] | flags[1] | flags[2] | flags[3];
+    }
+    if (bad != 0) {
+      const int base = TOKEN ? r0 : wrow;
+      for (int i = 0; i < 32; ++i) {
+        if (!((bad >> i) & 1u) || (TOKEN && (i & 3) != wave)) continue;
+        const int t_i = (base + i) / group;
+        careful_row<E, F::kKeys>(a, q, kt, first, end, splits, split, t_i, kvh * group + base + i - t_i * group, kvh,
+                                 lane);
+      }
+      if ((bad >> l32) & 1u) return;  // its row is written
+    }
+  }
+  if (!on || !writer) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float lg = l == 0.f ? -INFINITY : m * c + __builtin_amdgcn_logf(l);  // base 2
+  const int64_t q_at = q.q0 + tok;
+  const int d_first = TOKEN ? wave : 0, d_count = TOKEN ? 1 : NB;
+  if (splits == 1) {
+    E* op = static_cast<E*>(const_cast<void*>(a.o.p)) + q_at * a.o.ts + head * a.o.hs;
+    typedef E out4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int d = 0; d < NB; ++d) {
+      if (d >= d_count) break;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int at = 32 * (d_first + d) + 8 * g + 4 * h;
+        if (at < a.dim) {
+          out4 v;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = static_cast<E>(acc[d][4 * g + i] * inv);
+          *reinterpret_cast<out4*>(op + at) = v;
+        }
+      }
+    }
+    if (a.lse != nullptr && h == 0 && (!TOKEN || wave == 0))
+      a.lse[int64_t(head) * a.nq + q_at] = lg * 0.6931471805599453f;
+  } else {
+    const int64_t at_row = (int64_t(split) * a.hq + head) * a.nq + q_at;
+    float* op = a.part + at_row * a.dim;
+#pragma unroll
+    for (int d = 0; d < NB; ++d) {
+      if (d >= d_count) break;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int at = 32 * (d_first + d) + 8 * g + 4 * h;
+        if (at < a.dim) {
+          const float4 v = make_float4(acc[d][4 * g] * inv, acc[d][4 * g + 1] * inv, acc[d][4 * g + 2] * inv,
+                                       acc[d][4 * g + 3] * inv);
+          *reinterpret_cast<float4*>(op + at) = v;
+        }
+      }
+    }
+    if (h == 0 && (!TOKEN || wave == 0)) a.part[int64_t(splits) * a.hq * a.nq * a.dim + at_row] = lg;
+  }
+}
+
+// Joins the splits of a row: o = sum_s 2^{l_s - l} o_s, l = log2 sum_s 2^{l_s},
+// in split order. One wave a (token, head); lane: two elements.
+template <class E>
+__global__ __launch_bounds__(256) void attn_join(AttnArgs a, int splits) {
+  const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);  // head * nq + token
+  const int64_t n = int64_t(a.hq) * a.nq;
+  if (row >= n) return;
+  const int lane = threadIdx.x & 63;
+  const float* stat = a.part + int64_t(splits) * n * a.dim + row;
+  float mx = -INFINITY;
+  for (int s = lane; s < splits; s += 64) mx = fmaxf(mx, stat[s * n]);
+  for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
+  const float ms = mx == -INFINITY ? 0.f : mx;
+  float x = 0.f, y = 0.f, sum = 0.f;
+  const bool on = 2 * lane < a.dim;
+  const float* src = a.part + row * a.dim + 2 * lane;
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float w = __builtin_amdgcn_exp2f(stat[s * n] - ms);
+    sum += w;
+    if (on) {
+      const float2 v = *reinterpret_cast<const float2*>(src + int64_t(s) * n * a.dim);
+      x += w * v.x;
+      y += w * v.y;
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int head = int(row / a.nq);
+  const int64_t tok = row % a.nq;
+  if (on) {
+    typedef E out2 __attribute__((ext_vector_type(2)));
+    E* op = static_cast<E*>(const_cast<void*>(a.o.p)) + tok * a.o.ts + head * a.o.hs + 2 * lane;
+    *reinterpret_cast<out2*>(op) = out2{static_cast<E>(x * inv), static_cast<E>(y * inv)};
+  }
+  if (a.lse != nullptr && lane == 0)
+    a.lse[row] = sum == 0.f ? -INFINITY : (ms + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+}
+
+template <class E, int NB, bool TOKEN>
+hipError_t launch_shape(const AttnArgs& a, const AttnPlan& plan, hipStream_t st) {
+  typedef FwdShape<E, NB, TOKEN> F;
+  const int64_t tiles = tiles_of(a.nq, a.batch, a.hq / a.hk, F::kRows);
+  const int64_t wgs = tiles * a.hk * plan.splits;
+  if (wgs >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+  attn_fwd<E, NB, TOKEN><<<unsigned(wgs), 256, 0, st>>>(a, int(tiles), plan.splits);
+  return hipGetLastError();
+}
+
+template <class E>
+hipError_t launch_type(const AttnArgs& a, const AttnPlan& plan, hipStream_t st) {
+  const int nb = (a.dim + 31) / 32;
+  hipError_t e;
+  if (plan.token_form)
+    e = nb == 1   ? launch_shape<E, 1, true>(a, plan, st)
+        : nb == 2 ? launch_shape<E, 2, true>(a, plan, st)
+        : nb == 3 ? launch_shape<E, 3, true>(a, plan, st)
+                  : launch_shape<E, 4, true>(a, plan, st);
+  else
+    e = nb == 1   ? launch_shape<E, 1, false>(a, plan, st)
+        : nb == 2 ? launch_shape<E, 2, false>(a, plan, st)
+        : nb == 3 ? launch_shape<E, 3, false>(a, plan, st)
+                  : launch_shape<E, 4, false>(a, plan, st);
+  if (e != hipSuccess || plan.splits == 1) return e;
+  const int64_t rows = int64_t(a.hq) * a.nq;
+  attn_join<E><<<unsigned((rows + 3) / 4), 256, 0, st>>>(a, plan.splits);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+AttnPlan plan_attention(const AttnArgs& a) {
+  AttnPlan p{};
+  const int group = a.hq / a.hk;
+  p.splits = 1;
+  // up to 32 rows a sequence on average: the token form
+  p.token_form = int64_t(a.nq) * group <= int64_t(32) * a.batch;
+  const int64_t tiles = tiles_of(a.nq, a.batch, group, p.token_form ? 32 : 128) * a.hk;
+  const int keys = p.token_form ? 32 : 64;
+  // keys that one row tile can see at most
+  const int64_t reach = int64_t(a.left) + a.right + 1 + a.sinks + (p.token_form ? 32 : 128) / group;
+  const int64_t span = reach < a.nk ? reach : a.nk;
+  const int64_t per = p.token_form ? 4 : 1;  // tiles that a workgroup takes at once
+  const int64_t key_rounds = (span + keys * per - 1) / (keys * per);
+  const int64_t want = 512;
+  int64_t s = (want + tiles - 1) / tiles;
+  if (s > key_rounds / 2) s = key_rounds / 2;  // at least two rounds each
+  if (s > 256) s = 256;
+  if (s > 1) p.splits = int(s);
+  if (p.splits > 1) p.part_floats = size_t(p.splits) * a.hq * a.nq * (a.dim + 1);
+  return p;
+}
+
+hipError_t launch_attention(const AttnArgs& a, const AttnPlan& plan, hipStream_t st) {
+  if (a.nq == 0) return hipSuccess;
+  if (a.dtype == TR_SC_BF16) return launch_type<__bf16>(a, plan, st);
+  if (a.dtype == TR_SC_F16) return launch_type<_Float16>(a, plan, st);
+  return launch_type<float>(a, plan, st);
+}
+
+}  // namespace trsc
