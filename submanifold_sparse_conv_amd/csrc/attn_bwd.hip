@@ -28,7 +28,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRowsWg = 128, kKeysWg = 128;
 constexpr int kKeyTile = 64;      // keys of a tile of the dq kernel
 constexpr int kRowTile = 32;      // rows of a tile of the dk, dv kernel
-constexpr int kSinkChunk = 1024;  // rows of a sink workgroup
+constexpr int kSinkChunk = 512;   // rows of a sink workgroup
 
 template <class E, int NB>
 __device__ __forceinline__ void store_rows(E* p, const f32x16 (&acc)[NB], float f, int dim, int h) {
@@ -93,9 +93,9 @@ __device__ void careful_dkv(const AttnArgs& a, const Seq& q, int r0, int r1, int
     const float2 x = pair_of(static_cast<const E*>(a.q.p) + q_at * a.q.ts + head * a.q.hs, a.dim, lane);
     const float2 g = pair_of(static_cast<const E*>(a.dout.p) + q_at * a.dout.ts + head * a.dout.hs, a.dim, lane);
     const float s = wave_sum(x.x * y.x + x.y * y.y), dp = wave_sum(g.x * v.x + g.y * v.y);
-    const float lse = a.lse[int64_t(head) * a.nq + q_at], delta = a.delta[int64_t(head) * a.nq + q_at];
-    const float p = __builtin_amdgcn_exp2f(fmaf(s, c, lse == -INFINITY ? 0.f : -lse * kLog2e));
-    const float ds = p * (dp - delta) * a.scale;
+    const float2 st = a.stat[(int64_t(kvh) * a.nq + q.q0) * group + r];
+    const float p = __builtin_amdgcn_exp2f(fmaf(s, c, -st.x));
+    const float ds = p * (dp - st.y) * a.scale;
     dv.x += p * g.x;
     dv.y += p * g.y;
     dk.x += ds * x.x;
@@ -155,12 +155,12 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
     }
   }
   delta += __shfl_xor(delta, 32);
-  const int64_t stat = int64_t(head) * a.nq + q_at;
-  if (on && h == 0) a.delta[stat] = delta;
-  const float lse = on ? a.lse[stat] : 0.f;
+  const float lse = on ? a.lse[int64_t(head) * a.nq + q_at] : 0.f;
   const float lse2 = lse == -INFINITY ? 0.f : lse * kLog2e;
+  if (on && h == 0) a.stat[(int64_t(kvh) * a.nq + q.q0) * group + row] = make_float2(lse2, delta);
   const E* kbase = static_cast<const E*>(a.k.p) + int64_t(q.k0) * a.k.ts + kvh * a.k.hs;
   const E* vbase = static_cast<const E*>(a.v.p) + int64_t(q.k0) * a.v.ts + kvh * a.v.hs;
+  const typename T::Lane at = T::lane_of(lane);
   f32x16 acc[NB];
 #pragma unroll
   for (int d = 0; d < NB; ++d)
@@ -168,11 +168,14 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
     for (int e = 0; e < 16; ++e) acc[d][e] = 0.f;
   const float c = a.scale * kLog2e;
 
+  typename T::template Copy<kKeyTile, 4> kc, vc;
+  kc.start(a.k.ts, a.dim, wave, lane);
+  vc.start(a.v.ts, a.dim, wave, lane);
   auto fetch = [&](int it, int buf) {
     const int t0 = kt.at(it) * kKeyTile;
     unsigned char* dst = s_mem + buf * 2 * kTileBytes;
-    T::template copy<kKeyTile, 4>(dst, kbase, a.k.ts, t0, q.lk, a.dim, wave, lane);
-    T::template copy<kKeyTile, 4>(dst + kTileBytes, vbase, a.v.ts, t0, q.lk, a.dim, wave, lane);
+    kc.run(dst, kbase + t0 * a.k.ts, a.k.ts, q.lk - t0);
+    vc.run(dst + kTileBytes, vbase + t0 * a.v.ts, a.v.ts, q.lk - t0);
   };
   auto compute = [&](int it, int buf) {
     const unsigned char* ks = s_mem + buf * 2 * kTileBytes;
@@ -187,9 +190,10 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[e] = dp[e] = 0.f;
 #pragma unroll
-      for (int st = 0; st < ST; ++st) s = A::mma(T::row(ks, 32 * kb, st, lane), qf[st], s);
+      for (int st = 0; st < ST; ++st) s = A::mma(T::row(ks, 32 * kb, st, at), qf[st], s);
 #pragma unroll
-      for (int st = 0; st < ST; ++st) dp = A::mma(T::row(vs, 32 * kb, st, lane), df[st], dp);
+      for (int st = 0; st < ST; ++st) dp = A::mma(T::row(vs, 32 * kb, st, at), df[st], dp);
+      if constexpr (!A::wide) schedule_reads<2 * ST, 1, 4>();
       if (all) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lse2)) * (dp[e] - delta);
@@ -206,8 +210,9 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
       for (int ss = 0; ss < 2; ++ss) {
         const frag sf = pack_frag8<E>(s, ss);
 #pragma unroll
-        for (int d = 0; d < NB; ++d) acc[d] = A::mma(T::col(ks, 32 * kb, ss, d, lane), sf, acc[d]);
+        for (int d = 0; d < NB; ++d) acc[d] = A::mma(T::col(ks, 32 * kb, ss, d, at), sf, acc[d]);
       }
+      if constexpr (!A::wide) schedule_reads<2 * NB, 2, 4>();
     }
   };
   if (kt.n > 0) fetch(0, 0);
@@ -234,9 +239,9 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
 __device__ __forceinline__ int token_at(int64_t t, int lq) { return t < 0 ? 0 : t > lq ? lq : int(t); }
 
 // What a tile's rows need besides their elements.
-struct RowStats {
-  float lse2[kRowTile], delta[kRowTile];
-  int pos[kRowTile];  // position, or far below every window for a row that is not there
+struct alignas(16) RowStats {
+  float2 stat[kRowTile];  // base-2 lse (0 for a row that sees nothing) and delta
+  int pos[kRowTile];      // position, or far below every window for a row that is not there
 };
 constexpr int kNoRow = -(1 << 30);  // kNoRow + right < 0, and kNoRow - left does not wrap
 
@@ -255,8 +260,12 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
   constexpr int kBuffers = SINK && sizeof(E) == 4 ? 1 : 2;
   constexpr int kLds = kSets * kBuffers * 2 * kTileBytes;
   constexpr int kJoin = SINK ? 3 * 2 * NB * 16 * 64 * 4 : 0;  // the waves' sums at the end
-  __shared__ __attribute__((aligned(1024))) unsigned char s_mem[kLds > kJoin ? kLds : kJoin];
+  // heads of 128: V's fragments stay in LDS (in registers, with K's and the sums, they would spill)
+  constexpr bool kKeepV = NB < 4 || SINK;
+  constexpr int kV = kKeepV ? 0 : kKeysWg * T::kPitch;
+  __shared__ __attribute__((aligned(1024))) unsigned char s_mem[(kLds > kJoin ? kLds : kJoin) + kV];
   __shared__ RowStats s_stat[kSets * kBuffers];
+  unsigned char* const s_v = s_mem + kLds;
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.hq / a.hk;
@@ -291,7 +300,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
   }
   const int jw = SINK ? j0 : j0 + 32 * wave, key = jw + l32;  // this wave's keys, this lane's
   const bool key_on = key < q.lk && (!SINK || key < a.sinks);
-  frag kf[ST], vf[ST];
+  frag kf[ST], vf[kKeepV ? ST : 1];
   {
     const int64_t at = q.k0 + (key_on ? key : 0);
     const E* kp = static_cast<const E*>(a.k.p) + at * a.k.ts + kvh * a.k.hs;
@@ -299,9 +308,15 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
 #pragma unroll
     for (int s = 0; s < ST; ++s) {
       kf[s] = row_from<E>(kp, key_on, s, a.dim, lane);
-      vf[s] = row_from<E>(vp, key_on, s, a.dim, lane);
+      if constexpr (kKeepV) vf[s] = row_from<E>(vp, key_on, s, a.dim, lane);
     }
   }
+  if constexpr (!kKeepV) {
+    typename T::template Copy<kKeysWg, 4> vc;
+    vc.start(a.v.ts, a.dim, wave, lane);
+    vc.run(s_v, static_cast<const E*>(a.v.p) + int64_t(q.k0 + j0) * a.v.ts + kvh * a.v.hs, a.v.ts, q.lk - j0);
+  }
+  const typename T::Lane at = T::lane_of(lane);
   f32x16 dk[NB], dv[NB];
 #pragma unroll
   for (int d = 0; d < NB; ++d)
@@ -312,41 +327,59 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
   const E* qbase = static_cast<const E*>(a.q.p) + int64_t(q.q0) * a.q.ts + int64_t(kvh) * group * a.q.hs;
   const E* dbase = static_cast<const E*>(a.dout.p) + int64_t(q.q0) * a.dout.ts + int64_t(kvh) * group * a.dout.hs;
 
+  const float2* stat = a.stat + (int64_t(kvh) * a.nq + q.q0) * group;
+
+  // The rows of a tile as copies: offsets from the tile's first token, the same
+  // for every tile where the group divides the tile.
+  constexpr int kCopies = kRowTile / T::kRowsPerCopy, kStep = SINK ? 1 : 4, kMine = (kCopies + kStep - 1) / kStep;
+  const bool even = kRowTile % group == 0;
+  const int tok_begin = r_begin / group, tok_step = kRowTile / group;
+  auto first_token = [&](int it) { return even ? tok_begin + it * tok_step : (r_begin + it * kRowTile) / group; };
+  uint32_t oq[kMine], od[kMine];
+  auto offsets = [&](int it) {
+    const int t0 = r_begin + it * kRowTile, tok0 = first_token(it);
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      const int rr = (SINK ? j : j * 4 + wave) * T::kRowsPerCopy + lane / T::kChunks;
+      const int chunk = (lane % T::kChunks) ^ T::key(rr);
+      const int tok = (t0 + rr) / group, g = t0 + rr - tok * group;
+      const bool in = chunk * T::kPer < a.dim;
+      oq[j] = in ? uint32_t(tok - tok0) * uint32_t(a.q.ts * T::kElt) + uint32_t(g) * uint32_t(a.q.hs * T::kElt) +
+                       chunk * 16
+                 : 0x80000000u;
+      od[j] = in ? uint32_t(tok - tok0) * uint32_t(a.dout.ts * T::kElt) +
+                       uint32_t(g) * uint32_t(a.dout.hs * T::kElt) + chunk * 16
+                 : 0x80000000u;
+    }
+  };
+  if (even) offsets(0);
   auto fetch = [&](int it, int set) {
     unsigned char* dst = s_mem + set * 2 * kTileBytes;
-    const int t0 = r_begin + it * kRowTile;
+    const int t0 = r_begin + it * kRowTile, tok0 = first_token(it);
+    const buffer_t bq = buffer_of(qbase + tok0 * a.q.ts, 0x7fffffffu);
+    const buffer_t bd = buffer_of(dbase + tok0 * a.dout.ts, 0x7fffffffu);
+    if (!even) offsets(it);
 #pragma unroll
-    for (int j = 0; j < kRowTile / T::kRowsPerCopy; j += SINK ? 1 : 4) {
-      const int n = SINK ? j : j + wave;
-      if (n >= kRowTile / T::kRowsPerCopy) break;
-      const int rr = n * T::kRowsPerCopy + lane / T::kChunks;
-      const int chunk = (lane % T::kChunks) ^ T::key(rr);
-      const int r = t0 + rr;
-      const bool in = r < r_end && chunk * T::kPer < a.dim;
-      const int tok = in ? r / group : 0, g = in ? r - tok * group : 0;
-      const void* gq = in ? static_cast<const void*>(qbase + tok * a.q.ts + g * a.q.hs + chunk * T::kPer)
-                          : static_cast<const void*>(g_attn_zeros);
-      const void* gd = in ? static_cast<const void*>(dbase + tok * a.dout.ts + g * a.dout.hs + chunk * T::kPer)
-                          : static_cast<const void*>(g_attn_zeros);
-      copy16_to_lds(gq, dst + n * 1024);
-      copy16_to_lds(gd, dst + kTileBytes + n * 1024);
+    for (int j = 0; j < kMine; ++j) {
+      const int n = SINK ? j : j * 4 + wave;
+      if (kCopies % kStep != 0 && n >= kCopies) break;
+      const bool in = t0 + n * T::kRowsPerCopy + lane / T::kChunks < r_end;
+      copy_lds16(bq, in ? oq[j] : 0x80000000u, dst + n * 1024);
+      copy_lds16(bd, in ? od[j] : 0x80000000u, dst + kTileBytes + n * 1024);
     }
-    if ((SINK || wave == 3) && lane < kRowTile) {
-      const int r = t0 + lane;
-      const bool in = r < r_end;
-      const int tok = in ? r / group : 0, g = in ? r - tok * group : 0;
-      const int64_t at = int64_t(kvh * group + g) * a.nq + q.q0 + tok;
-      const float lse = in ? a.lse[at] : 0.f;
-      s_stat[set].lse2[lane] = lse == -INFINITY ? 0.f : lse * kLog2e;
-      s_stat[set].delta[lane] = in ? a.delta[at] : 0.f;
-      s_stat[set].pos[lane] = in ? tok + shift : kNoRow;
+    if (SINK || wave == 3) {
+      const buffer_t bs = buffer_of(stat + t0, uint32_t(min(kRowTile, r_end - t0)) * 8);
+      copy_lds4(bs, lane * 4, reinterpret_cast<unsigned char*>(s_stat[set].stat));
+      if (lane < kRowTile) s_stat[set].pos[lane] = t0 + lane < r_end ? (t0 + lane) / group + shift : kNoRow;
     }
   };
   auto compute = [&](int it, int set) {
     const unsigned char* qs = s_mem + set * 2 * kTileBytes;
     const unsigned char* ds_ = qs + kTileBytes;
     const int t0 = r_begin + it * kRowTile;
-    const int p0 = t0 / group + shift, p1 = min(t0 + kRowTile - 1, r_end - 1) / group + shift;
+    const int p0 = first_token(it) + shift;
+    const int p1 = (even ? min(p0 + max(tok_step, 1) - 1, (r_end - 1) / group + shift)
+                         : min(t0 + kRowTile - 1, r_end - 1) / group + shift);
     const int j1 = jw + 31;
     if (jw >= q.lk || jw > p1 + a.right || (j1 < p0 - a.left && jw >= a.sinks)) return;
     const bool all = t0 + kRowTile <= r_end && j1 <= p0 + a.right && j1 < q.lk &&
@@ -355,16 +388,22 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
 #pragma unroll
     for (int e = 0; e < 16; ++e) s[e] = dp[e] = 0.f;
 #pragma unroll
-    for (int st = 0; st < ST; ++st) s = A::mma(T::row(qs, 0, st, lane), kf[st], s);
+    for (int st = 0; st < ST; ++st) s = A::mma(T::row(qs, 0, st, at), kf[st], s);
 #pragma unroll
-    for (int st = 0; st < ST; ++st) dp = A::mma(T::row(ds_, 0, st, lane), vf[st], dp);
+    for (int st = 0; st < ST; ++st) {
+      if constexpr (kKeepV)
+        dp = A::mma(T::row(ds_, 0, st, at), vf[st], dp);
+      else
+        dp = A::mma(T::row(ds_, 0, st, at), T::row(s_v, 32 * wave, st, at), dp);
+    }
+    if constexpr (!A::wide && kKeepV) schedule_reads<2 * ST, 1, 4>();
     const RowStats& rs = s_stat[set];
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const int at = 8 * g + 4 * h;
-      const float4 ls = *reinterpret_cast<const float4*>(&rs.lse2[at]);
-      const float4 de = *reinterpret_cast<const float4*>(&rs.delta[at]);
-      const float lv[4] = {ls.x, ls.y, ls.z, ls.w}, ev[4] = {de.x, de.y, de.z, de.w};
+      const int row4 = 8 * g + 4 * h;
+      const float4 s0 = *reinterpret_cast<const float4*>(&rs.stat[row4]);
+      const float4 s1 = *reinterpret_cast<const float4*>(&rs.stat[row4 + 2]);
+      const float lv[4] = {s0.x, s0.z, s1.x, s1.z}, ev[4] = {s0.y, s0.w, s1.y, s1.w};
       if (all) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -373,7 +412,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
           dp[e] = s[e] * (dp[e] - ev[i]);
         }
       } else {
-        const int4 po = *reinterpret_cast<const int4*>(&rs.pos[at]);
+        const int4 po = *reinterpret_cast<const int4*>(&rs.pos[row4]);
         const int pv[4] = {po.x, po.y, po.z, po.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -389,14 +428,15 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
     for (int ss = 0; ss < 2; ++ss) {
       const frag pf = pack_frag8<E>(s, ss);
 #pragma unroll
-      for (int d = 0; d < NB; ++d) dv[d] = A::mma(T::col(ds_, 0, ss, d, lane), pf, dv[d]);
+      for (int d = 0; d < NB; ++d) dv[d] = A::mma(T::col(ds_, 0, ss, d, at), pf, dv[d]);
     }
 #pragma unroll
     for (int ss = 0; ss < 2; ++ss) {
       const frag sf = pack_frag8<E>(dp, ss);
 #pragma unroll
-      for (int d = 0; d < NB; ++d) dk[d] = A::mma(T::col(qs, 0, ss, d, lane), sf, dk[d]);
+      for (int d = 0; d < NB; ++d) dk[d] = A::mma(T::col(qs, 0, ss, d, at), sf, dk[d]);
     }
+    if constexpr (!A::wide) schedule_reads<4 * NB, 2, 4>();
   };
   if constexpr (!SINK) {
     if (n_tiles > 0) fetch(0, 0);
@@ -501,30 +541,26 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
 }
 
 // dk, dv of the sinks: the tile's own sums plus the chunks' in chunk order. One
-// wave a (sequence, kv head, sink).
+// workgroup a (sequence, kv head, sink), one thread an element of dk or dv.
 template <class E>
 __global__ __launch_bounds__(256) void attn_sinks(AttnArgs a, int chunks) {
-  const int64_t i = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (i >= int64_t(a.batch) * a.hk * a.sinks) return;
-  const int key = int(i % a.sinks), kvh = int(i / a.sinks % a.hk), b = int(i / a.sinks / a.hk);
+  const int64_t i = blockIdx.x;
+  const int key = int(i % a.sinks), kvh = int(i / a.sinks % a.hk), b = int(i / a.sinks / a.hk), d = threadIdx.x;
   const Seq q = sequence(a, b);
   const int cap = a.cu_k ? clamp_to(a.cu_k[b + 1], q.k0, a.nk) - q.k0 : a.nk;
-  if (key >= cap) return;
+  if (key >= cap || d >= 2 * a.dim) return;
   const int group = a.hq / a.hk, rows = q.lq * group;
   const int shift = q.lk - q.lq;
   const int band_end = token_at(int64_t(kKeysWg) + a.left - shift, q.lq) * group;
   const int base = a.cu_q ? first_tile(a.cu_q, b, group, kSinkChunk) : 0;
   const int c0 = band_end / kSinkChunk, c1 = rows > band_end ? (rows + kSinkChunk - 1) / kSinkChunk : c0;
   const int64_t slot = int64_t(a.hk) * a.sinks * 2 * a.dim;
-  const int64_t in = (int64_t(kvh) * a.sinks + key) * 2 * a.dim;
-  const int64_t out = (int64_t(q.k0 + key) * a.hk + kvh) * a.dim;
-  for (int d = lane; d < 2 * a.dim; d += 64) {
-    float v = a.sink_part[b * slot + in + d];
-    for (int t = c0; t < c1; ++t) v += a.sink_part[(a.batch + clamp_to(base + t, 0, chunks - 1)) * slot + in + d];
-    E* dst = static_cast<E*>(d < a.dim ? a.dk : a.dv);
-    dst[out + (d < a.dim ? d : d - a.dim)] = static_cast<E>(v);
-  }
+  const float* src = a.sink_part + (int64_t(kvh) * a.sinks + key) * 2 * a.dim + d;
+  float v = src[b * slot];
+#pragma unroll 8
+  for (int t = c0; t < c1; ++t) v += src[(a.batch + clamp_to(base + t, 0, chunks - 1)) * slot];
+  E* dst = static_cast<E*>(d < a.dim ? a.dk : a.dv);
+  dst[(int64_t(q.k0 + key) * a.hk + kvh) * a.dim + (d < a.dim ? d : d - a.dim)] = static_cast<E>(v);
 }
 
 template <class E, int NB>
@@ -551,8 +587,8 @@ hipError_t launch_shape(const AttnArgs& a, hipStream_t st) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const int64_t n = int64_t(a.batch) * a.hk * a.sinks;
-  attn_sinks<E><<<unsigned((n + 3) / 4), 256, 0, st>>>(a, int(tiles_of(a.nq, a.batch, group, kSinkChunk)));
+  const int64_t n = int64_t(a.batch) * a.hk * a.sinks;  // < 2^31: see the caller
+  attn_sinks<E><<<unsigned(n), 256, 0, st>>>(a, int(tiles_of(a.nq, a.batch, group, kSinkChunk)));
   return hipGetLastError();
 }
 
@@ -568,7 +604,7 @@ hipError_t launch_type(const AttnArgs& a, hipStream_t st) {
 
 }  // namespace
 
-size_t attention_backward_delta_floats(const AttnArgs& a) { return size_t(a.hq) * a.nq; }
+size_t attention_backward_stat_floats(const AttnArgs& a) { return size_t(a.hq) * a.nq * 2; }
 
 size_t attention_backward_sink_floats(const AttnArgs& a) {
   if (a.sinks == 0) return 0;

@@ -16,6 +16,13 @@ namespace trsc {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+// Transposing LDS read: of 16 lanes, lane i gets element i % 4 of the 8 bytes
+// that lanes i / 4, i / 4 + 4, i / 4 + 8 and i / 4 + 12 name. The restrict
+// gives the read an alias scope of its own: without one the compiler waits for
+// every copy to LDS in flight before it, the next tile's too.
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+__device__ __forceinline__ s16x4 read_tr(lds_s16x4* __restrict p) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p); }
+
 template <class E>
 struct AttnType;
 template <>
@@ -48,9 +55,18 @@ struct AttnType<float> {
   }
 };
 
-// 16 bytes that stand for what lies past a sequence's end or a head's width.
-__device__ __attribute__((aligned(16))) const uint32_t g_attn_zeros[4] = {0, 0, 0, 0};
-
+// Memory as a bounded buffer (wave-uniform; offsets from `bytes` on read as
+// zero), and its direct copy to LDS: lane l of the wave fills lds + 16 l.
+typedef __amdgpu_buffer_rsrc_t buffer_t;
+__device__ __forceinline__ buffer_t buffer_of(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, int(bytes), 0x00027000);
+}
+__device__ __forceinline__ void copy_lds16(buffer_t b, uint32_t off, unsigned char* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)(lds), 16, int(off), 0, 0, 0);
+}
+__device__ __forceinline__ void copy_lds4(buffer_t b, uint32_t off, unsigned char* lds) {  // lds + 4 l
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)(lds), 4, int(off), 0, 0, 0);
+}
 // LDS tile of token rows, NB * 32 elements wide: rows of kPitch bytes in
 // 16-byte chunks; chunk c of row r sits at chunk position c ^ key(r). The keys
 // spread both reads over the banks: one chunk of 16 consecutive rows (row
@@ -71,60 +87,88 @@ struct Tile {
   }
   static __device__ __forceinline__ int at(int r, int chunk) { return r * kPitch + ((chunk ^ key(r)) << 4); }
 
-  // Rows [0, ROWS) of the tile from tokens t0 + row (zeros from token `end`
-  // on, and past `dim`): copies first, first + step, ... of ROWS / kRowsPerCopy.
+  // Copies rows [0, ROWS) of a tile from memory to LDS, this wave's part of it:
+  // copies first, first + STEP, ... of ROWS / kRowsPerCopy, 64 lanes x 16 bytes
+  // each. A lane's offsets from the tile's first row stay the same from tile to
+  // tile; what lies past the tensor's end or a head's width reads as zero (the
+  // buffer's bound). Buffer loads, not global ones: with a flat-encoded copy in
+  // flight the compiler waits for all LDS reads where it needs one.
   template <int ROWS, int STEP>
-  static __device__ __forceinline__ void copy(unsigned char* lds, const E* base, int64_t stride, int t0, int end,
-                                              int dim, int first, int lane) {
+  struct Copy {
+    static constexpr int kN = (ROWS / kRowsPerCopy + STEP - 1) / STEP;
+    uint32_t off[kN], row_bytes;
+    int first;
+    __device__ __forceinline__ void start(int64_t stride, int dim, int first_, int lane) {
+      first = first_;
+      row_bytes = uint32_t(dim * kElt);
 #pragma unroll
-    for (int j = 0; j < ROWS / kRowsPerCopy; j += STEP) {
-      const int n = j + first;
-      const int row = n * kRowsPerCopy + lane / kChunks;
-      const int chunk = (lane % kChunks) ^ key(row);
-      const int t = t0 + row;
-      const bool in = t < end && chunk * kPer < dim;
-      const void* g = in ? static_cast<const void*>(base + int64_t(t) * stride + chunk * kPer)
-                         : static_cast<const void*>(g_attn_zeros);
-      copy16_to_lds(g, lds + n * 1024);
+      for (int j = 0; j < kN; ++j) {
+        const int row = (first + j * STEP) * kRowsPerCopy + lane / kChunks;
+        const int chunk = (lane % kChunks) ^ key(row);
+        off[j] = chunk * kPer < dim ? uint32_t(row) * uint32_t(stride * kElt) + chunk * 16 : 0x80000000u;
+      }
     }
-  }
-  // Row fragment: rows r0 + lane % 32, elements 16 s + 8 (lane / 32) + 0..7.
-  static __device__ __forceinline__ frag row(const unsigned char* lds, int r0, int s, int lane) {
-    const int r = r0 + (lane & 31), h = lane >> 5;
+    // base: the tile's first row (wave-uniform); left: rows from there to the end
+    __device__ __forceinline__ void run(unsigned char* lds, const E* base, int64_t stride, int left) const {
+      const int rows = left < 0 ? 0 : left > ROWS ? ROWS : left;
+      const buffer_t b = buffer_of(base, rows == 0 ? 0 : uint32_t(rows - 1) * uint32_t(stride * kElt) + row_bytes);
+#pragma unroll
+      for (int j = 0; j < kN; ++j)
+        if ((j + 1) * STEP <= ROWS / kRowsPerCopy || first + j * STEP < ROWS / kRowsPerCopy)
+          copy_lds16(b, off[j], lds + (first + j * STEP) * 1024);
+    }
+  };
+  // A lane's byte offsets in a tile. key(r) is the same for rows 16 apart, and
+  // the chunk's higher bits are the caller's constants, so a fragment's address
+  // is one of these, the constants in by XOR and the tile's rows by addition.
+  static constexpr int kCols = kElt == 2 ? 2 : 8;
+  struct Lane {
+    int row, col[kCols];
+  };
+  static __device__ __forceinline__ Lane lane_of(int lane) {
+    Lane o;
+    const int h = lane >> 5;
     if constexpr (kElt == 2) {
-      return *reinterpret_cast<const frag*>(lds + at(r, 2 * s + h));
+      o.row = at(lane & 31, h);
+      const int i = lane & 15, chunk = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
+      o.col[0] = at(4 * h + (i >> 2), chunk) + 8 * (i & 1);
+      o.col[1] = at(4 * h + (i >> 2) + 8, chunk) + 8 * (i & 1);
+    } else {
+      o.row = at(lane & 31, 2 * h);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        o.col[e] = at(4 * h + (e & 3) + 8 * (e >> 2), (lane & 31) / kPer) + (lane % kPer) * 4;
+    }
+    return o;
+  }
+  // Row fragment: rows r0 + lane % 32 (r0 a multiple of 32), elements 16 s + 8 (lane / 32) + 0..7.
+  static __device__ __forceinline__ frag row(const unsigned char* lds, int r0, int s, const Lane& o) {
+    if constexpr (kElt == 2) {
+      return *reinterpret_cast<const frag*>(lds + r0 * kPitch + (o.row ^ (s << 5)));
     } else {
       typedef float f4 __attribute__((ext_vector_type(4)));
-      const f4 a = *reinterpret_cast<const f4*>(lds + at(r, 4 * s + 2 * h));
-      const f4 b = *reinterpret_cast<const f4*>(lds + at(r, 4 * s + 2 * h + 1));
+      const f4 a = *reinterpret_cast<const f4*>(lds + r0 * kPitch + (o.row ^ (s << 6)));
+      const f4 b = *reinterpret_cast<const f4*>(lds + r0 * kPitch + (o.row ^ (s << 6) ^ 16));
       return frag{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
     }
   }
   // Transposed fragment: column 32 b + lane % 32, at the rows that the
   // accumulator registers 8 s .. 8 s + 7 of a 32-row block stand for:
   // r0 + 16 s + 4 (lane / 32) + 0..3 and those + 8.
-  static __device__ __forceinline__ frag col(const unsigned char* lds, int r0, int s, int b, int lane) {
-    const int h = lane >> 5;
+  static __device__ __forceinline__ frag col(const unsigned char* lds, int r0, int s, int b, const Lane& o) {
+    const unsigned char* const from = lds + (r0 + 16 * s) * kPitch;
     if constexpr (kElt == 2) {
-      const int i = lane & 15;
-      const int r = r0 + 16 * s + 4 * h + (i >> 2);
-      const int chunk = 4 * b + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
-      typedef __attribute__((address_space(3))) s16x4* lptr;
       union {
         s16x4 half[2];
         frag f;
       } u;
-      u.half[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lptr)(lds + at(r, chunk) + 8 * (i & 1)));
-      u.half[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lptr)(lds + at(r + 8, chunk) + 8 * (i & 1)));
+      u.half[0] = read_tr((lds_s16x4*)(from + (o.col[0] ^ (b << 6))));
+      u.half[1] = read_tr((lds_s16x4*)(from + (o.col[1] ^ (b << 6))));
       return u.f;
     } else {
-      const int d = 32 * b + (lane & 31);
       frag f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int r = r0 + 16 * s + 4 * h + (e & 3) + (e >> 2) * 8;
-        f[e] = *reinterpret_cast<const float*>(lds + at(r, d / kPer) + (d % kPer) * 4);
-      }
+      for (int e = 0; e < 8; ++e) f[e] = *reinterpret_cast<const float*>(from + (o.col[e] ^ (b << 7)));
       return f;
     }
   }
@@ -149,6 +193,26 @@ __device__ __forceinline__ typename AttnType<E>::frag pack_frag8(const f32x16& a
 #pragma unroll
   for (int e = 0; e < 8; ++e) f[e] = static_cast<E>(a[8 * s + e]);
   return f;
+}
+
+// The value of lane ^ 32 and its own, as (lower half's, upper half's).
+__device__ __forceinline__ float2 both_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// Order of the matrix products' block before it: the LDS reads (READS for each
+// of the N products) run AHEAD products in front of the products that take them.
+template <int N, int READS, int AHEAD>
+__device__ __forceinline__ void schedule_reads() {
+  constexpr int kFirst = AHEAD < N ? AHEAD : N;
+  __builtin_amdgcn_sched_group_barrier(0x100, kFirst * READS, 0);  // LDS reads
+#pragma unroll
+  for (int i = 0; i < N - kFirst; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix
+    __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, kFirst, 0);
 }
 
 // A sequence of the packed batch. Offsets and lengths from the device are

@@ -24,16 +24,20 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// max / sum with the other half of the wave (lane ^ 32)
-__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
+// The running maximum need not be the true one: the weights only have to stay
+// representable. A tile is weighed with the maximum so far, and only where its
+// sum leaves [0, kMostSum) is the maximum taken again, the sums rescaled and the
+// tile weighed anew. (fp16 holds weights up to 65504.)
+constexpr float kMostSum = 16384.f;
 
 // The scores of 32 keys j0 + 8 g + 4 (lane / 32) + i: hidden ones become -inf.
 __device__ __forceinline__ void hide(f32x16& s, int j0, int lo, int hi, int sinks, int lane) {
   const int base = j0 + 4 * (lane >> 5);
+  const int a0 = lo - base, a1 = hi - base, a2 = sinks - base;
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
-    const int j = base + 8 * (e >> 2) + (e & 3);
-    const bool sees = j <= hi && (j >= lo || j < sinks);
+    const int j = 8 * (e >> 2) + (e & 3);
+    const bool sees = j <= a1 && (j >= a0 || j < a2);
     s[e] = sees ? s[e] : -INFINITY;
   }
 }
@@ -91,6 +95,175 @@ __device__ void careful_row(const AttnArgs& a, const Seq& q, const KeyTiles& kt,
   store_row<E>(a, splits, split, head, q_at, make_float2(o.x * inv, o.y * inv), lg, lane);
 }
 
+// A wave's 32 rows on their way over the keys: lane l and l + 32 hold row l.
+template <class E, int NB, int KB>
+struct RowState {
+  typedef Tile<E, NB> T;
+  typedef AttnType<E> A;
+  typedef typename A::frag frag;
+  static constexpr int ST = NB * 2;
+  frag qf[ST];     // the queries
+  f32x16 acc[NB];  // O^T
+  float mc, l;     // scaled maximum (base 2) and sum of the weights
+  f32x16 s[KB];    // scores of a tile of 32 KB keys
+  frag pf[KB][2];  // its weights
+
+  __device__ __forceinline__ void start(const E* qp, bool on, int dim, int lane) {
+#pragma unroll
+    for (int st = 0; st < ST; ++st) qf[st] = row_from<E>(qp, on, st, dim, lane);
+#pragma unroll
+    for (int d = 0; d < NB; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[d][e] = 0.f;
+    mc = -INFINITY;
+    l = 0.f;
+  }
+  __device__ __forceinline__ void scores(const unsigned char* ks, const typename T::Lane& at) {
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[kb][e] = 0.f;
+#pragma unroll
+      for (int st = 0; st < ST; ++st) s[kb] = A::mma(T::row(ks, 32 * kb, st, at), qf[st], s[kb]);
+    }
+    if constexpr (!A::wide) schedule_reads<KB * ST, 1, 4>();
+  }
+  // weights 2^(s c - m), their sum, and the fragments that multiply V
+  __device__ __forceinline__ float weigh_by(float c, float m) {
+    float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int ss = 0; ss < 2; ++ss)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float w = __builtin_amdgcn_exp2f(fmaf(s[kb][8 * ss + e], c, -m));
+          sum[e & 1] += w;
+          pf[kb][ss][e] = static_cast<E>(w);
+        }
+    return sum[0] + sum[1];
+  }
+  __device__ __forceinline__ void weigh(float c) {
+    float sum = weigh_by(c, mc);
+    if (__any(!(sum < kMostSum))) {  // also where the row has seen nothing before (mc = -inf)
+      float mx = -INFINITY;
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[kb][e]);
+      const float2 mh = both_halves(mx);
+      mx = fmaxf(fmaxf(mh.x, mh.y) * c, mc);
+      const float f = mx == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mc - mx);
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < NB; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[d][e] *= f;
+      mc = mx;
+      sum = weigh_by(c, mx == -INFINITY ? 0.f : mx);
+    }
+    l += sum;
+  }
+  __device__ __forceinline__ void multiply(const unsigned char* vs, const typename T::Lane& at) {
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int ss = 0; ss < 2; ++ss)
+#pragma unroll
+        for (int d = 0; d < NB; ++d) acc[d] = A::mma(T::col(vs, 32 * kb, ss, d, at), pf[kb][ss], acc[d]);
+    if constexpr (!A::wide) schedule_reads<KB * 2 * NB, 2, 4>();
+  }
+  __device__ __forceinline__ void join_halves() {
+    const float2 lh = both_halves(l);
+    l = lh.x + lh.y;
+  }
+};
+
+// A lane's row of the output: `count` blocks of 32 columns from block `first`.
+template <class E, int NB>
+__device__ __forceinline__ void store_tile_row(const AttnArgs& a, int splits, int split, int head, int64_t q_at,
+                                               const f32x16 (&acc)[NB], float mc, float l, int first, int count,
+                                               bool with_sum, int h) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float lg = l == 0.f ? -INFINITY : mc + __builtin_amdgcn_logf(l);  // base 2
+  const int64_t at_row = (int64_t(split) * a.hq + head) * a.nq + q_at;
+  typedef E out4 __attribute__((ext_vector_type(4)));
+  E* const op = static_cast<E*>(const_cast<void*>(a.o.p)) + q_at * a.o.ts + head * a.o.hs;
+  float* const pp = a.part + at_row * a.dim;
+#pragma unroll
+  for (int d = 0; d < NB; ++d) {
+    if (d >= count) break;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int col = 32 * (first + d) + 8 * g + 4 * h;
+      if (col >= a.dim) continue;
+      if (splits == 1) {
+        out4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = static_cast<E>(acc[d][4 * g + i] * inv);
+        *reinterpret_cast<out4*>(op + col) = v;
+      } else {
+        *reinterpret_cast<float4*>(pp + col) = make_float4(acc[d][4 * g] * inv, acc[d][4 * g + 1] * inv,
+                                                           acc[d][4 * g + 2] * inv, acc[d][4 * g + 3] * inv);
+      }
+    }
+  }
+  if (!with_sum) return;
+  if (splits > 1)
+    a.part[int64_t(splits) * a.hq * a.nq * a.dim + at_row] = lg;
+  else if (a.lse != nullptr)
+    a.lse[int64_t(head) * a.nq + q_at] = lg * 0.6931471805599453f;
+}
+
+// Where a workgroup of `rows_wg` rows and each of its waves' rows lie.
+struct RowTile {
+  Seq q;
+  int rows, r0, last, shift;  // rows of the sequence; first row; last token; position of token 0
+};
+__device__ __forceinline__ bool row_tile(const AttnArgs& a, int tile, int rows_wg, RowTile* t) {
+  const int group = a.hq / a.hk;
+  int inside;
+  const int b = find_sequence(a.cu_q, a.batch, group, rows_wg, tile, &inside);
+  t->q = sequence(a, b);
+  t->rows = t->q.lq * group;  // < 2^31 - 2^10 (checked by the caller)
+  if (inside < 0 || inside > t->rows / rows_wg) return false;
+  t->r0 = inside * rows_wg;
+  if (t->r0 >= t->rows) return false;
+  t->last = min(t->rows - 1, t->r0 + rows_wg - 1) / group;
+  t->shift = t->q.lk - t->q.lq;
+  return true;
+}
+struct WaveRows {
+  bool any, on;       // the wave has rows; this lane has one
+  int first;          // the wave's first row
+  int tok, head;      // this lane's
+  int lo, hi;         // keys that it sees: [lo, hi] (and the sinks up to hi)
+  int p0, p1;         // positions of the wave's rows
+};
+__device__ __forceinline__ WaveRows wave_rows(const AttnArgs& a, const RowTile& t, int first, int kvh, int l32) {
+  const int group = a.hq / a.hk;
+  WaveRows w;
+  w.first = first;
+  const int row = first + l32;
+  w.any = first < t.rows;
+  w.on = row < t.rows;
+  w.tok = w.on ? row / group : t.last;
+  w.head = kvh * group + (w.on ? row - w.tok * group : 0);
+  const int p = w.tok + t.shift;
+  w.lo = p - a.left;
+  w.hi = min(p + a.right, t.q.lk - 1);
+  w.p0 = min(first, t.rows - 1) / group + t.shift;
+  w.p1 = min(first + 31, t.rows - 1) / group + t.shift;
+  return w;
+}
+// A tile of keys j0 .. j1 as the wave's rows see it.
+__device__ __forceinline__ bool tile_seen(const AttnArgs& a, const WaveRows& w, int j0, int j1) {
+  return w.any && j0 <= w.p1 + a.right && (j1 >= w.p0 - a.left || j0 < a.sinks);
+}
+__device__ __forceinline__ bool tile_whole(const AttnArgs& a, const WaveRows& w, int j0, int j1, int lk) {
+  return j1 <= w.p0 + a.right && j1 < lk && (j0 >= w.p1 - a.left || j1 < a.sinks);
+}
+
 template <class E, int NB, bool TOKEN>
 struct FwdShape {
   typedef Tile<E, NB> T;
@@ -107,124 +280,62 @@ template <class E, int NB, bool TOKEN>
 __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_fwd(AttnArgs a, int tiles, int splits) {
   typedef FwdShape<E, NB, TOKEN> F;
   typedef Tile<E, NB> T;
-  typedef AttnType<E> A;
-  typedef typename A::frag frag;
-  constexpr int KB = F::kKeys / 32, ST = NB * 2;
+  constexpr int KB = F::kKeys / 32;
   __shared__ __attribute__((aligned(1024))) unsigned char s_mem[F::kLds];
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.hq / a.hk;
-
   const int w = xcd_remap(blockIdx.x, gridDim.x);
   const int tile = w % tiles, kvh = (w / tiles) % a.hk, split = w / tiles / a.hk;
-  int inside;
-  const int b = find_sequence(a.cu_q, a.batch, group, F::kRows, tile, &inside);
-  const Seq q = sequence(a, b);
-  const int rows = q.lq * group;  // < 2^31 - 2^8 (checked by the caller)
-  if (inside < 0 || inside > rows / F::kRows) return;
-  const int r0 = inside * F::kRows;
-  if (r0 >= rows) return;
-  const int last = min(rows - 1, r0 + F::kRows - 1) / group;
-  const int shift = q.lk - q.lq;
-  const KeyTiles kt = key_tiles<F::kKeys>(a, r0 / group + shift, last + shift, q.lk);
-
-  // this lane's row
-  const int wrow = r0 + (TOKEN ? 0 : 32 * wave);  // the wave's first row
-  const int row = wrow + l32;
-  const bool on = row < rows;
-  const int tok = on ? row / group : last, head = kvh * group + (on ? row - tok * group : 0);
-  const int p = tok + shift, lo = p - a.left, hi = min(p + a.right, q.lk - 1);
-  const int pw0 = min(wrow, rows - 1) / group + shift, pw1 = min(wrow + 31, rows - 1) / group + shift;
-  const bool wave_on = wrow < rows;
-  frag qf[ST];
-  {
-    const E* qp = static_cast<const E*>(a.q.p) + int64_t(q.q0 + tok) * a.q.ts + head * a.q.hs;
-#pragma unroll
-    for (int s = 0; s < ST; ++s) qf[s] = row_from<E>(qp, on, s, a.dim, lane);
-  }
+  RowTile t;
+  if (!row_tile(a, tile, F::kRows, &t)) return;
+  const Seq& q = t.q;
+  const KeyTiles kt = key_tiles<F::kKeys>(a, t.r0 / group + t.shift, t.last + t.shift, q.lk);
+  const WaveRows wr = wave_rows(a, t, t.r0 + (TOKEN ? 0 : 32 * wave), kvh, l32);
+  const typename T::Lane at = T::lane_of(lane);
+  RowState<E, NB, KB> st;
+  st.start(static_cast<const E*>(a.q.p) + int64_t(q.q0 + wr.tok) * a.q.ts + wr.head * a.q.hs, wr.on, a.dim, lane);
   const E* kbase = static_cast<const E*>(a.k.p) + int64_t(q.k0) * a.k.ts + kvh * a.k.hs;
   const E* vbase = static_cast<const E*>(a.v.p) + int64_t(q.k0) * a.v.ts + kvh * a.v.hs;
-
-  f32x16 acc[NB];
-#pragma unroll
-  for (int d = 0; d < NB; ++d)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) acc[d][e] = 0.f;
-  float m = -INFINITY, l = 0.f;
   const float c = a.scale * kLog2e;
 
   const int first = int(int64_t(kt.n) * split / splits), end = int(int64_t(kt.n) * (split + 1) / splits);
   unsigned char* const mem = s_mem + (TOKEN ? wave * F::kBuffers * 2 * F::kTileBytes : 0);
+  typename T::template Copy<F::kKeys, TOKEN ? 1 : 4> kc, vc;
+  kc.start(a.k.ts, a.dim, TOKEN ? 0 : wave, lane);
+  vc.start(a.v.ts, a.dim, TOKEN ? 0 : wave, lane);
   auto fetch = [&](int it, int buf) {
     const int t0 = kt.at(it) * F::kKeys;
     unsigned char* dst = mem + buf * 2 * F::kTileBytes;
-    T::template copy<F::kKeys, TOKEN ? 1 : 4>(dst, kbase, a.k.ts, t0, q.lk, a.dim, TOKEN ? 0 : wave, lane);
-    T::template copy<F::kKeys, TOKEN ? 1 : 4>(dst + F::kTileBytes, vbase, a.v.ts, t0, q.lk, a.dim, TOKEN ? 0 : wave,
-                                              lane);
+    kc.run(dst, kbase + t0 * a.k.ts, a.k.ts, q.lk - t0);
+    vc.run(dst + F::kTileBytes, vbase + t0 * a.v.ts, a.v.ts, q.lk - t0);
   };
   auto compute = [&](int it, int buf) {
     const unsigned char* ks = mem + buf * 2 * F::kTileBytes;
-    const unsigned char* vs = ks + F::kTileBytes;
     const int j0 = kt.at(it) * F::kKeys, j1 = j0 + F::kKeys - 1;
-    // nothing of the tile, or all of it, seen by every row of the wave
-    if (!wave_on || j0 > pw1 + a.right || (j1 < pw0 - a.left && j0 >= a.sinks)) return;
-    const bool all = j1 <= pw0 + a.right && j1 < q.lk && (j0 >= pw1 - a.left || j1 < a.sinks);
-    f32x16 s[KB];
+    if (!tile_seen(a, wr, j0, j1)) return;
+    st.scores(ks, at);
+    if (!tile_whole(a, wr, j0, j1, q.lk)) {
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) s[kb][e] = 0.f;
-#pragma unroll
-      for (int st = 0; st < ST; ++st) s[kb] = A::mma(T::row(ks, 32 * kb, st, lane), qf[st], s[kb]);
+      for (int kb = 0; kb < KB; ++kb) hide(st.s[kb], j0 + 32 * kb, wr.lo, wr.hi, a.sinks, lane);
     }
-    if (!all) {
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) hide(s[kb], j0 + 32 * kb, lo, hi, a.sinks, lane);
-    }
-    float mx = m;
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[kb][e]);
-    mx = fmaxf(mx, other_half(mx));
-    const float ms = mx == -INFINITY ? 0.f : mx;  // a row that has seen nothing yet
-    if (__any(mx != m)) {
-      const float f = __builtin_amdgcn_exp2f((m - ms) * c);
-      l *= f;
-#pragma unroll
-      for (int d = 0; d < NB; ++d)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[d][e] *= f;
-      m = mx;
-    }
-    const float mc = ms * c;
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        s[kb][e] = __builtin_amdgcn_exp2f(fmaf(s[kb][e], c, -mc));
-        l += s[kb][e];
-      }
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-      for (int ss = 0; ss < 2; ++ss) {
-        const frag pf = pack_frag8<E>(s[kb], ss);
-#pragma unroll
-        for (int d = 0; d < NB; ++d) acc[d] = A::mma(T::col(vs, 32 * kb, ss, d, lane), pf, acc[d]);
-      }
+    st.weigh(c);
+    st.multiply(ks + F::kTileBytes, at);
   };
 
   if constexpr (!TOKEN) {
     if (first < end) fetch(first, 0);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    for (int it = first; it < end; ++it) {
-      const int buf = (it - first) & 1;
-      if (it + 1 < end) fetch(it + 1, buf ^ 1);
-      compute(it, buf);
-      __builtin_amdgcn_s_waitcnt(0);
-      bare_barrier();
+    for (int it = first; it < end; it += 2) {  // two tiles a round: the buffers' addresses are constants
+#pragma unroll
+      for (int buf = 0; buf < 2; ++buf) {
+        if (it + buf >= end) break;
+        if (it + buf + 1 < end) fetch(it + buf + 1, buf ^ 1);
+        compute(it + buf, buf);
+        __builtin_amdgcn_s_waitcnt(0);
+        bare_barrier();
+      }
     }
   } else {
     // each wave its own tiles and LDS: no barrier in the loop
@@ -247,7 +358,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_fwd(AttnArgs
       }
     }
   }
-  l += other_half(l);
+  st.join_halves();
+  float mc = st.mc, l = st.l;
   bool writer = true;
   if constexpr (TOKEN) {
     // the four waves hold the same rows over different keys: join them in wave
@@ -256,7 +368,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_fwd(AttnArgs
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
     if (lane < 32) {
-      red[wave * 64 + lane] = m;
+      red[wave * 64 + lane] = mc;
       red[wave * 64 + 32 + lane] = l;
     }
     __syncthreads();
@@ -267,18 +379,18 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_fwd(AttnArgs
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float mi = red[i * 64 + l32];
-      f[i] = mi == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((mi - mm) * c);
+      f[i] = mi == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mi - mm);
       ll += f[i] * red[i * 64 + 32 + l32];
     }
     const float mine = f[0] * (wave == 0) + f[1] * (wave == 1) + f[2] * (wave == 2) + f[3] * (wave == 3);
-    const bool any = m != -INFINITY;
-    m = mm;
+    const bool any = mc != -INFINITY;
+    mc = mm;
     l = ll;
     __syncthreads();
 #pragma unroll
     for (int d = 0; d < NB; ++d)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) red[((wave * NB + d) * 16 + e) * 64 + lane] = any ? acc[d][e] * mine : 0.f;
+      for (int e = 0; e < 16; ++e) red[((wave * NB + d) * 16 + e) * 64 + lane] = any ? st.acc[d][e] * mine : 0.f;
     __syncthreads();
     writer = wave < NB;
     if (writer) {
@@ -287,19 +399,19 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_fwd(AttnArgs
         float v = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v += red[((i * NB + wave) * 16 + e) * 64 + lane];
-        acc[0][e] = v;
+        st.acc[0][e] = v;
       }
     }
   }
   // rows whose sums are not finite, again without what they do not see
   {
     float t = 0.f;
-    if (writer && on) {
+    if (writer && wr.on) {
       if constexpr (TOKEN) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) t = fmaf(acc[0][e], 0.f, t);
+        for (int e = 0; e < 16; ++e) t = fmaf(st.acc[0][e], 0.f, t);
       } else {
-        t = zero_if_finite<NB>(acc);
+        t = zero_if_finite<NB>(st.acc);
       }
     }
     uint32_t bad = bad_rows(t);
@@ -311,7 +423,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_fwd(AttnArgs
       bad = flags[0] | flags[1] | flags[2] | flags[3];
     }
     if (bad != 0) {
-      const int base = TOKEN ? r0 : wrow;
+      const int base = wr.first;
       for (int i = 0; i < 32; ++i) {
         if (!((bad >> i) & 1u) || (TOKEN && (i & 3) != wave)) continue;
         const int t_i = (base + i) / group;
@@ -321,48 +433,9 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_fwd(AttnArgs
       if ((bad >> l32) & 1u) return;  // its row is written
     }
   }
-  if (!on || !writer) return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const float lg = l == 0.f ? -INFINITY : m * c + __builtin_amdgcn_logf(l);  // base 2
-  const int64_t q_at = q.q0 + tok;
-  const int d_first = TOKEN ? wave : 0, d_count = TOKEN ? 1 : NB;
-  if (splits == 1) {
-    E* op = static_cast<E*>(const_cast<void*>(a.o.p)) + q_at * a.o.ts + head * a.o.hs;
-    typedef E out4 __attribute__((ext_vector_type(4)));
-#pragma unroll
-    for (int d = 0; d < NB; ++d) {
-      if (d >= d_count) break;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int at = 32 * (d_first + d) + 8 * g + 4 * h;
-        if (at < a.dim) {
-          out4 v;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = static_cast<E>(acc[d][4 * g + i] * inv);
-          *reinterpret_cast<out4*>(op + at) = v;
-        }
-      }
-    }
-    if (a.lse != nullptr && h == 0 && (!TOKEN || wave == 0))
-      a.lse[int64_t(head) * a.nq + q_at] = lg * 0.6931471805599453f;
-  } else {
-    const int64_t at_row = (int64_t(split) * a.hq + head) * a.nq + q_at;
-    float* op = a.part + at_row * a.dim;
-#pragma unroll
-    for (int d = 0; d < NB; ++d) {
-      if (d >= d_count) break;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int at = 32 * (d_first + d) + 8 * g + 4 * h;
-        if (at < a.dim) {
-          const float4 v = make_float4(acc[d][4 * g] * inv, acc[d][4 * g + 1] * inv, acc[d][4 * g + 2] * inv,
-                                       acc[d][4 * g + 3] * inv);
-          *reinterpret_cast<float4*>(op + at) = v;
-        }
-      }
-    }
-    if (h == 0 && (!TOKEN || wave == 0)) a.part[int64_t(splits) * a.hq * a.nq * a.dim + at_row] = lg;
-  }
+  if (!wr.on || !writer) return;
+  store_tile_row<E, NB>(a, splits, split, wr.head, q.q0 + wr.tok, st.acc, mc, l, TOKEN ? wave : 0, TOKEN ? 1 : NB,
+                        h == 0 && (!TOKEN || wave == 0), h);
 }
 
 // Joins the splits of a row: o = sum_s 2^{l_s - l} o_s, l = log2 sum_s 2^{l_s},

@@ -57,7 +57,8 @@ struct AttnArgs {
   HeadsRef q, k, v, o, dout;  // o: output of the forward, input of the backward
   void *dq, *dk, *dv;         // contiguous [tokens, heads, dim]
   float* lse;                 // [q_heads, tokens_q]
-  float* delta;               // [q_heads, tokens_q], backward workspace
+  float2* stat;               // backward workspace: (base-2 lse, delta) of row r = token, head of the group of
+                              // each kv head, [kv_heads, tokens_q * group]
   float* part;                // forward splits: partial outputs, then their statistics
   float* sink_part;           // backward workspace: the sinks' partial gradients
   const int32_t *cu_q, *cu_k, *k_len;
@@ -76,8 +77,8 @@ struct AttnPlan {
 };
 AttnPlan plan_attention(const AttnArgs& a);
 hipError_t launch_attention(const AttnArgs& a, const AttnPlan& plan, hipStream_t st);
-// Workspace of the backward, in floats: delta, then the sinks' partials.
-size_t attention_backward_delta_floats(const AttnArgs& a);
+// Workspace of the backward, in floats: the rows' statistics, then the sinks' partials.
+size_t attention_backward_stat_floats(const AttnArgs& a);
 size_t attention_backward_sink_floats(const AttnArgs& a);
 hipError_t launch_attention_backward(const AttnArgs& a, hipStream_t st);
 

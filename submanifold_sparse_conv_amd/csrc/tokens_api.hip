@@ -122,6 +122,15 @@ void set_grad(NormSide* s, const tr_sc_heads* t) {
 
 HeadsRef ref(const tr_sc_heads* t) { return HeadsRef{t->data, t->token_stride, t->head_stride}; }
 
+// Whether 32 rows of a query-like tensor (rows: token by token, in a token the
+// heads that share a key-value head) lie within 2^30 bytes of the first.
+bool rows_reach(const tr_sc_heads* t, const tr_sc_heads* k, int bytes) {
+  const int64_t group = t->heads / k->heads, tokens = 32 / group + 2;
+  const int64_t most = int64_t(1) << 30;
+  return t->token_stride * bytes < most / tokens && t->head_stride * bytes < most / group &&
+         tokens * t->token_stride * bytes + group * t->head_stride * bytes < most;
+}
+
 // Everything of an attention call but its outputs.
 int fill_attn(const char* who, const tr_sc_heads* q, const tr_sc_heads* k, const tr_sc_heads* v,
               const tr_sc_window* win, int64_t nq, int64_t nk, int dim, int dtype, AttnArgs* a) {
@@ -148,9 +157,15 @@ int fill_attn(const char* who, const tr_sc_heads* q, const tr_sc_heads* k, const
     return fail(TR_SC_ERR_INVALID_ARG, "%s: sinks = %d out of [0, %d]", who, win->sinks, kMaxSinks);
   if (!(win->scale > 0.f) || std::isinf(win->scale))
     return fail(TR_SC_ERR_INVALID_ARG, "%s: scale = %g, a positive number is needed", who, double(win->scale));
-  if (nq * (q->heads / k->heads) + int64_t(1024) * (win->batch + 1) >= (int64_t(1) << 31) ||
+  if (int64_t(win->batch) * k->heads * (win->sinks + 1) >= (int64_t(1) << 31) ||
+      nq * (q->heads / k->heads) + int64_t(1024) * (win->batch + 1) >= (int64_t(1) << 31) ||
       nq * q->heads >= (int64_t(1) << 33) || nk + int64_t(128) * (win->batch + 1) >= (int64_t(1) << 31))
     return fail(TR_SC_ERR_UNSUPPORTED, "%s: too many rows", who);
+  // a tile's rows lie within 32-bit offsets of its first
+  const int64_t reach = int64_t(1) << 30;
+  const int bytes = elem_bytes(dtype);
+  if (k->token_stride * bytes >= reach / 64 || v->token_stride * bytes >= reach / 64 || !rows_reach(q, k, bytes))
+    return fail(TR_SC_ERR_UNSUPPORTED, "%s: strides too large", who);
   *a = AttnArgs{};
   a->q = ref(q);
   a->k = ref(k);
@@ -180,12 +195,12 @@ bool sizes_only(const tr_sc_window* win, int64_t nq, int64_t nk, int q_heads, in
 }
 
 struct BackwardLayout {
-  size_t delta, sinks, total;
+  size_t stat, sinks, total;
 };
 BackwardLayout backward_layout(const AttnArgs& a) {
   BackwardLayout l{};
-  l.delta = 0;
-  l.sinks = align_up(attention_backward_delta_floats(a) * 4, 256);
+  l.stat = 0;
+  l.sinks = align_up(attention_backward_stat_floats(a) * 4, 256);
   l.total = l.sinks + align_up(attention_backward_sink_floats(a) * 4, 256);
   return l;
 }
@@ -292,6 +307,7 @@ int tr_sparseconv_window_attention_backward(const tr_sc_heads* dout, const tr_sc
   if (c == TR_SC_OK) c = check_heads(who, "dout", dout, tokens_q, q->heads, dim, dtype, false);
   if (c == TR_SC_OK) c = check_heads(who, "out", out, tokens_q, q->heads, dim, dtype, false);
   if (c != TR_SC_OK) return c;
+  if (!rows_reach(dout, k, elem_bytes(dtype))) return fail(TR_SC_ERR_UNSUPPORTED, "%s: strides too large", who);
   if ((tokens_q > 0 && (lse == nullptr || dq == nullptr)) || (tokens_k > 0 && (dk == nullptr || dv == nullptr)))
     return fail(TR_SC_ERR_INVALID_ARG, "%s: NULL tensor", who);
   if (reinterpret_cast<uintptr_t>(dq) % 16 != 0 || reinterpret_cast<uintptr_t>(dk) % 16 != 0 ||
@@ -306,7 +322,7 @@ int tr_sparseconv_window_attention_backward(const tr_sc_heads* dout, const tr_sc
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
-  a.delta = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.delta);
+  a.stat = reinterpret_cast<float2*>(static_cast<char*>(workspace) + l.stat);
   a.sink_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.sinks);
   const hipError_t e = launch_attention_backward(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? TR_SC_OK : hip_fail(e, who);
