@@ -29,6 +29,7 @@ constexpr int kRowsWg = 128, kKeysWg = 128;
 constexpr int kKeyTile = 64;      // keys of a tile of the dq kernel
 constexpr int kRowTile = 32;      // rows of a tile of the dk, dv kernel
 constexpr int kSinkChunk = 512;   // rows of a sink workgroup
+constexpr int kWantWgs = 512;     // workgroups that fill the chip: two on each of 256 CUs
 
 template <class E, int NB>
 __device__ __forceinline__ void store_rows(E* p, const f32x16 (&acc)[NB], float f, int dim, int h) {
@@ -250,28 +251,29 @@ constexpr int kNoRow = -(1 << 30);  // kNoRow + right < 0, and kNoRow - left doe
 // sinks) a workgroup, the rows past the band, one chunk; every wave walks row
 // tiles of its own, and the four sums are joined at the end.
 template <class E, int NB, bool SINK>
-__global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs a, int tiles) {
+__global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs a, int tiles, int parts) {
   typedef Tile<E, NB> T;
   typedef AttnType<E> A;
   typedef typename A::frag frag;
   constexpr int ST = NB * 2;
   constexpr int kTileBytes = kRowTile * T::kPitch;
   constexpr int kSets = SINK ? 4 : 1;                       // LDS tile sets: a wave's own, or shared
-  constexpr int kBuffers = SINK && sizeof(E) == 4 ? 1 : 2;
+  constexpr int kBuffers = SINK ? 1 : 2;                    // a sink workgroup's other half waits on the CU instead
   constexpr int kLds = kSets * kBuffers * 2 * kTileBytes;
-  constexpr int kJoin = SINK ? 3 * 2 * NB * 16 * 64 * 4 : 0;  // the waves' sums at the end
+  constexpr int kJoin = SINK ? 3 * NB * 16 * 64 * 4 : 0;  // the waves' sums at the end
   // heads of 128: V's fragments stay in LDS (in registers, with K's and the sums, they would spill)
-  constexpr bool kKeepV = NB < 4 || SINK;
-  constexpr int kV = kKeepV ? 0 : kKeysWg * T::kPitch;
+  constexpr bool kKeepV = NB < 4;
+  constexpr int kV = kKeepV ? 0 : (SINK ? 32 : kKeysWg) * T::kPitch;
   __shared__ __attribute__((aligned(1024))) unsigned char s_mem[(kLds > kJoin ? kLds : kJoin) + kV];
   __shared__ RowStats s_stat[kSets * kBuffers];
-  unsigned char* const s_v = s_mem + kLds;
+  unsigned char* const s_v = s_mem + (kLds > kJoin ? kLds : kJoin);
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.hq / a.hk;
   const int sink_blocks = (a.sinks + 31) / 32;
   const int w = xcd_remap(blockIdx.x, gridDim.x);
-  const int tile = w % tiles, kvh = (w / tiles) % a.hk, sink_block = w / tiles / a.hk;
+  const int tile = w % tiles, kvh = (w / tiles) % a.hk;
+  const int sink_block = SINK ? w / tiles / a.hk : 0, part = SINK ? 0 : w / tiles / a.hk;
   int inside;
   const int b = SINK ? find_sequence(a.cu_q, a.batch, group, kSinkChunk, tile, &inside)
                      : find_sequence(a.cu_k, a.batch, 1, kKeysWg, tile, &inside);
@@ -297,6 +299,12 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
     r_end = token_at(int64_t(last) + a.left - shift + 1, q.lq) * group;
     if (j0 == 0 && a.sinks > 0) r_end = band_end;
     if (j0 >= q.lk) r_end = r_begin;
+    if (parts > 1 && r_end > r_begin) {  // this workgroup's part of the row tiles
+      const int n = (r_end - r_begin + kRowTile * group - 1) / (kRowTile * group);  // whole tokens
+      const int from = r_begin, unit = kRowTile * group;
+      r_begin = from + int(int64_t(n) * part / parts) * unit;
+      r_end = min(r_end, from + int(int64_t(n) * (part + 1) / parts) * unit);
+    }
   }
   const int jw = SINK ? j0 : j0 + 32 * wave, key = jw + l32;  // this wave's keys, this lane's
   const bool key_on = key < q.lk && (!SINK || key < a.sinks);
@@ -312,11 +320,11 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
     }
   }
   if constexpr (!kKeepV) {
-    typename T::template Copy<kKeysWg, 4> vc;
+    typename T::template Copy<SINK ? 32 : kKeysWg, 4> vc;
     vc.start(a.v.ts, a.dim, wave, lane);
     vc.run(s_v, static_cast<const E*>(a.v.p) + int64_t(q.k0 + j0) * a.v.ts + kvh * a.v.hs, a.v.ts, q.lk - j0);
   }
-  const typename T::Lane at = T::lane_of(lane);
+  const typename T::Lane lanes = T::lane_of(lane);
   f32x16 dk[NB], dv[NB];
 #pragma unroll
   for (int d = 0; d < NB; ++d)
@@ -374,6 +382,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
     }
   };
   auto compute = [&](int it, int set) {
+    typename T::Lane at = lanes;
+    if constexpr (!kKeepV) at.fresh();
     const unsigned char* qs = s_mem + set * 2 * kTileBytes;
     const unsigned char* ds_ = qs + kTileBytes;
     const int t0 = r_begin + it * kRowTile;
@@ -394,7 +404,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
       if constexpr (kKeepV)
         dp = A::mma(T::row(ds_, 0, st, at), vf[st], dp);
       else
-        dp = A::mma(T::row(ds_, 0, st, at), T::row(s_v, 32 * wave, st, at), dp);
+        dp = A::mma(T::row(ds_, 0, st, at), T::row(s_v, SINK ? 0 : 32 * wave, st, at), dp);
     }
     if constexpr (!A::wide && kKeepV) schedule_reads<2 * ST, 1, 4>();
     const RowStats& rs = s_stat[set];
@@ -449,12 +459,18 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
       bare_barrier();
     }
     const uint32_t bad = bad_rows(key < cap ? zero_if_finite<NB>(dk) + zero_if_finite<NB>(dv) : 0.f);
+    // where a key's sums go: to the sinks' slots (joined with the later rows'),
+    // to this part's (joined with the other parts'), or out
+    auto slot = [&](int j) -> float* {
+      if (j < a.sinks) return a.sink_part + (((int64_t(b) * parts + part) * a.hk + kvh) * a.sinks + j) * 2 * a.dim;
+      if (parts > 1) return a.dkv_part + ((int64_t(part) * a.nk + q.k0 + j) * a.hk + kvh) * 2 * a.dim;
+      return nullptr;
+    };
     for (uint32_t left = bad; left != 0; left &= left - 1) {
       const int j = jw + __builtin_ctz(left);
       float2 gk, gv;
       careful_dkv<E>(a, q, r_begin, r_end, j, kvh, gk, gv, lane);
-      if (j < a.sinks) {
-        float* dst = a.sink_part + ((int64_t(b) * a.hk + kvh) * a.sinks + j) * 2 * a.dim;
+      if (float* dst = slot(j)) {
         store_pair<float>(dst, gk, a.dim, lane);
         store_pair<float>(dst + a.dim, gv, a.dim, lane);
       } else {
@@ -464,65 +480,52 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
       }
     }
     if (key < cap && !((bad >> l32) & 1u)) {
-      // a key of the sinks: its sum is joined with those of the later rows
-      const bool joined = key < a.sinks;
-      if (!joined) {
+      if (float* dst = slot(key)) {
+        store_rows<float, NB>(dst, dk, a.scale, a.dim, h);
+        store_rows<float, NB>(dst + a.dim, dv, 1.f, a.dim, h);
+      } else {
         const int64_t at = (int64_t(q.k0 + key) * a.hk + kvh) * a.dim;
         store_rows<E, NB>(static_cast<E*>(a.dk) + at, dk, a.scale, a.dim, h);
         store_rows<E, NB>(static_cast<E*>(a.dv) + at, dv, 1.f, a.dim, h);
-      } else {
-        float* dst = a.sink_part + ((int64_t(b) * a.hk + kvh) * a.sinks + key) * 2 * a.dim;
-        store_rows<float, NB>(dst, dk, a.scale, a.dim, h);
-        store_rows<float, NB>(dst + a.dim, dv, 1.f, a.dim, h);
       }
     }
   } else {
-    int it = wave;
-    if constexpr (kBuffers == 2) {
-      int buf = 0;
-      if (it < n_tiles) fetch(it, wave * 2);
-      for (; it < n_tiles; it += 4) {
-        __builtin_amdgcn_s_waitcnt(0);
-        asm volatile("" ::: "memory");
-        if (it + 4 < n_tiles) fetch(it + 4, wave * 2 + (buf ^ 1));
-        compute(it, wave * 2 + buf);
-        buf ^= 1;
-      }
-    } else {
-      for (; it < n_tiles; it += 4) {
-        __builtin_amdgcn_s_waitcnt(0);
-        asm volatile("" ::: "memory");
-        fetch(it, wave);
-        __builtin_amdgcn_s_waitcnt(0);
-        asm volatile("" ::: "memory");
-        compute(it, wave);
-      }
-    }
-    // waves 1 - 3 hand over, wave 0 adds in wave order
-    float* red = reinterpret_cast<float*>(s_mem);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    if (wave > 0) {
-#pragma unroll
-      for (int d = 0; d < NB; ++d)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          red[(((wave - 1) * 2 * NB + d) * 16 + e) * 64 + lane] = dk[d][e];
-          red[(((wave - 1) * 2 * NB + NB + d) * 16 + e) * 64 + lane] = dv[d][e];
-        }
+    for (int it = wave; it < n_tiles; it += 4) {
+      __builtin_amdgcn_s_waitcnt(0);  // the last tile's reads are done
+      asm volatile("" ::: "memory");
+      fetch(it, wave);
+      __builtin_amdgcn_s_waitcnt(0);
+      asm volatile("" ::: "memory");
+      compute(it, wave);
     }
-    __syncthreads();
-    if (wave == 0) {
-#pragma unroll
-      for (int i = 0; i < 3; ++i)
+    // waves 1 - 3 hand over, first dk, then dv; wave 0 adds in wave order
+    float* red = reinterpret_cast<float*>(s_mem);
+    auto join = [&](f32x16 (&x)[NB]) {
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      if (wave > 0) {
 #pragma unroll
         for (int d = 0; d < NB; ++d)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            dk[d][e] += red[((i * 2 * NB + d) * 16 + e) * 64 + lane];
-            dv[d][e] += red[((i * 2 * NB + NB + d) * 16 + e) * 64 + lane];
-          }
-      float* const slot = a.sink_part + (int64_t(a.batch + tile) * a.hk + kvh) * a.sinks * 2 * a.dim;
+          for (int e = 0; e < 16; ++e) red[(((wave - 1) * NB + d) * 16 + e) * 64 + lane] = x[d][e];
+      }
+      __syncthreads();
+      if (wave == 0) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+#pragma unroll
+          for (int d = 0; d < NB; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[d][e] += red[((i * NB + d) * 16 + e) * 64 + lane];
+      }
+    };
+    join(dk);
+    join(dv);
+    if (wave == 0) {
+      float* const slot = a.sink_part + (int64_t(a.batch) * parts + tile) * a.hk * a.sinks * 2 * a.dim +
+                          int64_t(kvh) * a.sinks * 2 * a.dim;
       const uint32_t bad = bad_rows(key < a.sinks ? zero_if_finite<NB>(dk) + zero_if_finite<NB>(dv) : 0.f);
       for (uint32_t left = bad; left != 0; left &= left - 1) {
         const int j = jw + __builtin_ctz(left);
@@ -543,7 +546,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
 // dk, dv of the sinks: the tile's own sums plus the chunks' in chunk order. One
 // workgroup a (sequence, kv head, sink), one thread an element of dk or dv.
 template <class E>
-__global__ __launch_bounds__(256) void attn_sinks(AttnArgs a, int chunks) {
+__global__ __launch_bounds__(256) void attn_sinks(AttnArgs a, int chunks, int parts) {
   const int64_t i = blockIdx.x;
   const int key = int(i % a.sinks), kvh = int(i / a.sinks % a.hk), b = int(i / a.sinks / a.hk), d = threadIdx.x;
   const Seq q = sequence(a, b);
@@ -556,11 +559,49 @@ __global__ __launch_bounds__(256) void attn_sinks(AttnArgs a, int chunks) {
   const int c0 = band_end / kSinkChunk, c1 = rows > band_end ? (rows + kSinkChunk - 1) / kSinkChunk : c0;
   const int64_t slot = int64_t(a.hk) * a.sinks * 2 * a.dim;
   const float* src = a.sink_part + (int64_t(kvh) * a.sinks + key) * 2 * a.dim + d;
-  float v = src[b * slot];
+  float v = 0.f;
+  for (int t = 0; t < parts; ++t) v += src[(int64_t(b) * parts + t) * slot];
+  src += int64_t(a.batch) * parts * slot;
 #pragma unroll 8
-  for (int t = c0; t < c1; ++t) v += src[(a.batch + clamp_to(base + t, 0, chunks - 1)) * slot];
+  for (int t = c0; t < c1; ++t) v += src[clamp_to(base + t, 0, chunks - 1) * slot];
   E* dst = static_cast<E*>(d < a.dim ? a.dk : a.dv);
   dst[(int64_t(q.k0 + key) * a.hk + kvh) * a.dim + (d < a.dim ? d : d - a.dim)] = static_cast<E>(v);
+}
+
+// dk, dv of every (key, kv head) from the parts of the row walk, in part order:
+// one thread four elements.
+template <class E>
+__global__ __launch_bounds__(256) void attn_parts(AttnArgs a, int parts) {
+  const int64_t per = a.dim / 2, n = int64_t(a.nk) * a.hk * per;  // float4s of a part
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= n) return;
+  const float4* src = reinterpret_cast<const float4*>(a.dkv_part) + i;
+  float4 v = src[0];
+  for (int t = 1; t < parts; ++t) {
+    const float4 x = src[t * n];
+    v.x += x.x;
+    v.y += x.y;
+    v.z += x.z;
+    v.w += x.w;
+  }
+  const int64_t row = i / per;
+  const int d = int(i - row * per) * 4;
+  typedef E out4 __attribute__((ext_vector_type(4)));
+  E* dst = static_cast<E*>(d < a.dim ? a.dk : a.dv) + row * a.dim + (d < a.dim ? d : d - a.dim);
+  *reinterpret_cast<out4*>(dst) = out4{static_cast<E>(v.x), static_cast<E>(v.y), static_cast<E>(v.z),
+                                       static_cast<E>(v.w)};
+}
+
+// Parts of the row walk of a key tile: few key tiles with many rows each (short
+// sequences, many query heads to a kv head) would leave most of the chip idle.
+int row_parts(const AttnArgs& a) {
+  const int64_t wgs = tiles_of(a.nk, a.batch, 1, kKeysWg) * a.hk, group = a.hq / a.hk;
+  const int64_t reach = int64_t(a.left) + a.right + 1 + kKeysWg;
+  const int64_t units = (reach < a.nq ? reach : a.nq) / kRowTile;  // tiles of a part are a multiple of the group
+  int64_t p = kWantWgs / wgs;
+  if (p > units * group / 16) p = units * group / 16;  // 16 row tiles a part at least
+  if (p > units) p = units;
+  return p < 2 ? 1 : p > 8 ? 8 : int(p);
 }
 
 template <class E, int NB>
@@ -576,19 +617,27 @@ hipError_t launch_shape(const AttnArgs& a, hipStream_t st) {
   if (a.nk == 0) return hipSuccess;
   const int64_t tiles = tiles_of(a.nk, a.batch, 1, kKeysWg);
   if (tiles * a.hk >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-  attn_dkv<E, NB, false><<<unsigned(tiles * a.hk), 256, 0, st>>>(a, int(tiles));
+  const int parts = row_parts(a);
+  attn_dkv<E, NB, false><<<unsigned(tiles * a.hk * parts), 256, 0, st>>>(a, int(tiles), parts);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.sinks == 0) return e;
+  if (e != hipSuccess) return e;
+  if (parts > 1) {
+    const int64_t n = int64_t(a.nk) * a.hk * (a.dim / 2);
+    attn_parts<E><<<unsigned((n + 255) / 256), 256, 0, st>>>(a, parts);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.sinks == 0) return hipSuccess;
   if (a.nq > 0) {
     const int64_t chunks = tiles_of(a.nq, a.batch, group, kSinkChunk);
     const int64_t wgs = chunks * a.hk * ((a.sinks + 31) / 32);
     if (wgs >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-    attn_dkv<E, NB, true><<<unsigned(wgs), 256, 0, st>>>(a, int(chunks));
+    attn_dkv<E, NB, true><<<unsigned(wgs), 256, 0, st>>>(a, int(chunks), parts);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   const int64_t n = int64_t(a.batch) * a.hk * a.sinks;  // < 2^31: see the caller
-  attn_sinks<E><<<unsigned(n), 256, 0, st>>>(a, int(tiles_of(a.nq, a.batch, group, kSinkChunk)));
+  attn_sinks<E><<<unsigned(n), 256, 0, st>>>(a, int(tiles_of(a.nq, a.batch, group, kSinkChunk)), parts);
   return hipGetLastError();
 }
 
@@ -608,8 +657,13 @@ size_t attention_backward_stat_floats(const AttnArgs& a) { return size_t(a.hq) *
 
 size_t attention_backward_sink_floats(const AttnArgs& a) {
   if (a.sinks == 0) return 0;
-  const int64_t slots = a.batch + tiles_of(a.nq, a.batch, a.hq / a.hk, kSinkChunk);
+  const int64_t slots = int64_t(a.batch) * row_parts(a) + tiles_of(a.nq, a.batch, a.hq / a.hk, kSinkChunk);
   return size_t(slots) * a.hk * a.sinks * 2 * a.dim;
+}
+
+size_t attention_backward_part_floats(const AttnArgs& a) {
+  const int parts = row_parts(a);
+  return parts > 1 ? size_t(parts) * a.nk * a.hk * 2 * a.dim : 0;
 }
 
 hipError_t launch_attention_backward(const AttnArgs& a, hipStream_t st) {

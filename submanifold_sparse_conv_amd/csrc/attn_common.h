@@ -124,6 +124,13 @@ struct Tile {
   static constexpr int kCols = kElt == 2 ? 2 : 8;
   struct Lane {
     int row, col[kCols];
+    // Addresses made from these are made again, not kept in registers (which
+    // would be spilled) from before a loop.
+    __device__ __forceinline__ void fresh() {
+      asm volatile("" : "+v"(row));
+#pragma unroll
+      for (int e = 0; e < kCols; ++e) asm volatile("" : "+v"(col[e]));
+    }
   };
   static __device__ __forceinline__ Lane lane_of(int lane) {
     Lane o;

@@ -61,6 +61,7 @@ struct AttnArgs {
                               // each kv head, [kv_heads, tokens_q * group]
   float* part;                // forward splits: partial outputs, then their statistics
   float* sink_part;           // backward workspace: the sinks' partial gradients
+  float* dkv_part;            // backward workspace: dk, dv of the parts of the row walk
   const int32_t *cu_q, *cu_k, *k_len;
   int batch;
   int32_t nq, nk;  // tokens of q and of k, v
@@ -77,9 +78,10 @@ struct AttnPlan {
 };
 AttnPlan plan_attention(const AttnArgs& a);
 hipError_t launch_attention(const AttnArgs& a, const AttnPlan& plan, hipStream_t st);
-// Workspace of the backward, in floats: the rows' statistics, then the sinks' partials.
+// Workspace of the backward, in floats: the rows' statistics, the sinks' partials, the parts'.
 size_t attention_backward_stat_floats(const AttnArgs& a);
 size_t attention_backward_sink_floats(const AttnArgs& a);
+size_t attention_backward_part_floats(const AttnArgs& a);
 hipError_t launch_attention_backward(const AttnArgs& a, hipStream_t st);
 
 }  // namespace trsc
