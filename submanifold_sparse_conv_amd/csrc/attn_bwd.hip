@@ -116,7 +116,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
   typedef Tile<E, NB> T;
   typedef AttnType<E> A;
   typedef typename A::frag frag;
-  constexpr int KB = kKeyTile / 32, ST = NB * 2;
+  constexpr int KB = kKeyTile / 32, ST = NB * 2, kAhead = A::wide ? 1 : 4;
   constexpr int kTileBytes = kKeyTile * T::kPitch;
   __shared__ __attribute__((aligned(1024))) unsigned char s_mem[4 * kTileBytes];
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
@@ -190,11 +190,14 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
       f32x16 s, dp;
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[e] = dp[e] = 0.f;
-#pragma unroll
-      for (int st = 0; st < ST; ++st) s = A::mma(T::row(ks, 32 * kb, st, at), qf[st], s);
-#pragma unroll
-      for (int st = 0; st < ST; ++st) dp = A::mma(T::row(vs, 32 * kb, st, at), df[st], dp);
-      if constexpr (!A::wide) schedule_reads<2 * ST, 1, 4>();
+      products<2 * ST, kAhead, frag>(
+          [&](int i, frag& f) { f = T::row(i < ST ? ks : vs, 32 * kb, i % ST, at); },
+          [&](int i, const frag& f) {
+            if (i < ST)
+              s = A::mma(f, qf[i], s);
+            else
+              dp = A::mma(f, df[i - ST], dp);
+          });
       if (all) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lse2)) * (dp[e] - delta);
@@ -207,13 +210,10 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
           s[e] = sees ? ds : 0.f;
         }
       }
-#pragma unroll
-      for (int ss = 0; ss < 2; ++ss) {
-        const frag sf = pack_frag8<E>(s, ss);
-#pragma unroll
-        for (int d = 0; d < NB; ++d) acc[d] = A::mma(T::col(ks, 32 * kb, ss, d, at), sf, acc[d]);
-      }
-      if constexpr (!A::wide) schedule_reads<2 * NB, 2, 4>();
+      const frag sf[2] = {pack_frag8<E>(s, 0), pack_frag8<E>(s, 1)};
+      products<2 * NB, kAhead, frag>(
+          [&](int i, frag& f) { f = T::col(ks, 32 * kb, i / NB, i % NB, at); },
+          [&](int i, const frag& f) { acc[i % NB] = A::mma(f, sf[i / NB], acc[i % NB]); });
     }
   };
   if (kt.n > 0) fetch(0, 0);
@@ -255,7 +255,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
   typedef Tile<E, NB> T;
   typedef AttnType<E> A;
   typedef typename A::frag frag;
-  constexpr int ST = NB * 2;
+  constexpr int ST = NB * 2, kAhead = A::wide ? 1 : SINK ? 2 : 4;
   constexpr int kTileBytes = kRowTile * T::kPitch;
   constexpr int kSets = SINK ? 4 : 1;                       // LDS tile sets: a wave's own, or shared
   constexpr int kBuffers = SINK ? 1 : 2;                    // a sink workgroup's other half waits on the CU instead
@@ -264,9 +264,12 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
   // heads of 128: V's fragments stay in LDS (in registers, with K's and the sums, they would spill)
   constexpr bool kKeepV = NB < 4;
   constexpr int kV = kKeepV ? 0 : (SINK ? 32 : kKeysWg) * T::kPitch;
-  __shared__ __attribute__((aligned(1024))) unsigned char s_mem[(kLds > kJoin ? kLds : kJoin) + kV];
-  __shared__ RowStats s_stat[kSets * kBuffers];
-  unsigned char* const s_v = s_mem + (kLds > kJoin ? kLds : kJoin);
+  // one array: with two, every copy to LDS is tracked by the array it goes to,
+  // and a tile's reads wait for the next tile's copies
+  constexpr int kTiles = kLds > kJoin ? kLds : kJoin;
+  __shared__ __attribute__((aligned(1024))) unsigned char s_mem[kTiles + kV + kSets * kBuffers * sizeof(RowStats)];
+  unsigned char* const s_v = s_mem + kTiles;
+  RowStats* const s_stat = reinterpret_cast<RowStats*>(s_mem + kTiles + kV);
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.hq / a.hk;
@@ -367,13 +370,22 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
     const buffer_t bq = buffer_of(qbase + tok0 * a.q.ts, 0x7fffffffu);
     const buffer_t bd = buffer_of(dbase + tok0 * a.dout.ts, 0x7fffffffu);
     if (!even) offsets(it);
+    // Past the rows: out of the buffer. (In place, in the last tile: a register
+    // that a copy's offset was in is not reused before the copy has landed.)
+    if (t0 + kRowTile > r_end) {
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        const bool in = t0 + (SINK ? j : j * 4 + wave) * T::kRowsPerCopy + lane / T::kChunks < r_end;
+        oq[j] = in ? oq[j] : 0x80000000u;
+        od[j] = in ? od[j] : 0x80000000u;
+      }
+    }
 #pragma unroll
     for (int j = 0; j < kMine; ++j) {
       const int n = SINK ? j : j * 4 + wave;
       if (kCopies % kStep != 0 && n >= kCopies) break;
-      const bool in = t0 + n * T::kRowsPerCopy + lane / T::kChunks < r_end;
-      copy_lds16(bq, in ? oq[j] : 0x80000000u, dst + n * 1024);
-      copy_lds16(bd, in ? od[j] : 0x80000000u, dst + kTileBytes + n * 1024);
+      copy_lds16(bq, oq[j], dst + n * 1024);
+      copy_lds16(bd, od[j], dst + kTileBytes + n * 1024);
     }
     if (SINK || wave == 3) {
       const buffer_t bs = buffer_of(stat + t0, uint32_t(min(kRowTile, r_end - t0)) * 8);
@@ -397,56 +409,73 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
     f32x16 s, dp;
 #pragma unroll
     for (int e = 0; e < 16; ++e) s[e] = dp[e] = 0.f;
-#pragma unroll
-    for (int st = 0; st < ST; ++st) s = A::mma(T::row(qs, 0, st, at), kf[st], s);
-#pragma unroll
-    for (int st = 0; st < ST; ++st) {
-      if constexpr (kKeepV)
-        dp = A::mma(T::row(ds_, 0, st, at), vf[st], dp);
-      else
-        dp = A::mma(T::row(ds_, 0, st, at), T::row(s_v, SINK ? 0 : 32 * wave, st, at), dp);
-    }
-    if constexpr (!A::wide && kKeepV) schedule_reads<2 * ST, 1, 4>();
+    struct Pair {
+      frag row, v;
+    };
+    products<ST, kAhead, frag>([&](int i, frag& f) { f = T::row(qs, 0, i, at); },
+                               [&](int i, const frag& f) { s = A::mma(f, kf[i], s); });
+    if constexpr (kKeepV)
+      products<ST, kAhead, frag>([&](int i, frag& f) { f = T::row(ds_, 0, i, at); },
+                                 [&](int i, const frag& f) { dp = A::mma(f, vf[i], dp); });
+    else
+      products<ST, (kAhead + 1) / 2, Pair>(
+          [&](int i, Pair& f) {
+            f.row = T::row(ds_, 0, i, at);
+            f.v = T::row(s_v, SINK ? 0 : 32 * wave, i, at);
+          },
+          [&](int i, const Pair& f) { dp = A::mma(f.row, f.v, dp); });
     const RowStats& rs = s_stat[set];
+    // weights into s, score gradients into dp; of what a row does not see, zero.
+    // Both branches end with their fragments, so that the products are a block
+    // of their own and their reads can be put in order.
+    frag pf[2], sf[2];
+    auto pack = [&]() {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int row4 = 8 * g + 4 * h;
-      const float4 s0 = *reinterpret_cast<const float4*>(&rs.stat[row4]);
-      const float4 s1 = *reinterpret_cast<const float4*>(&rs.stat[row4 + 2]);
-      const float lv[4] = {s0.x, s0.z, s1.x, s1.z}, ev[4] = {s0.y, s0.w, s1.y, s1.w};
-      if (all) {
+      for (int ss = 0; ss < 2; ++ss) {
+        pf[ss] = pack_frag8<E>(s, ss);
+        sf[ss] = pack_frag8<E>(dp, ss);
+      }
+    };
+    if (all) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float4 s0 = read_lds<float4>(&rs.stat[8 * g + 4 * h]), s1 = read_lds<float4>(&rs.stat[8 * g + 4 * h + 2]);
+        const float lv[4] = {s0.x, s0.z, s1.x, s1.z}, ev[4] = {s0.y, s0.w, s1.y, s1.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int e = 4 * g + i;
           s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lv[i]));
           dp[e] = s[e] * (dp[e] - ev[i]);
         }
-      } else {
-        const int4 po = *reinterpret_cast<const int4*>(&rs.pos[row4]);
+      }
+      pack();
+    } else {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float4 s0 = read_lds<float4>(&rs.stat[8 * g + 4 * h]), s1 = read_lds<float4>(&rs.stat[8 * g + 4 * h + 2]);
+        const int4 po = read_lds<int4>(&rs.pos[8 * g + 4 * h]);
+        const float lv[4] = {s0.x, s0.z, s1.x, s1.z}, ev[4] = {s0.y, s0.w, s1.y, s1.w};
         const int pv[4] = {po.x, po.y, po.z, po.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int e = 4 * g + i;
-          const bool sees = key_on && key <= pv[i] + a.right && (key >= pv[i] - a.left || key < a.sinks);
+          const int from = key < a.sinks ? 0 : pv[i] - a.left, to = key_on ? pv[i] + a.right : -1;
+          const bool sees = (key <= to) & (key >= from);
           const float pr = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lv[i]));
           s[e] = sees ? pr : 0.f;
           dp[e] = sees ? pr * (dp[e] - ev[i]) : 0.f;
         }
       }
+      pack();
     }
-#pragma unroll
-    for (int ss = 0; ss < 2; ++ss) {
-      const frag pf = pack_frag8<E>(s, ss);
-#pragma unroll
-      for (int d = 0; d < NB; ++d) dv[d] = A::mma(T::col(ds_, 0, ss, d, at), pf, dv[d]);
-    }
-#pragma unroll
-    for (int ss = 0; ss < 2; ++ss) {
-      const frag sf = pack_frag8<E>(dp, ss);
-#pragma unroll
-      for (int d = 0; d < NB; ++d) dk[d] = A::mma(T::col(qs, 0, ss, d, at), sf, dk[d]);
-    }
-    if constexpr (!A::wide) schedule_reads<4 * NB, 2, 4>();
+    products<4 * NB, kAhead, frag>(
+        [&](int i, frag& f) { f = T::col(i < 2 * NB ? ds_ : qs, 0, i / NB % 2, i % NB, at); },
+        [&](int i, const frag& f) {
+          if (i < 2 * NB)
+            dv[i % NB] = A::mma(f, pf[i / NB], dv[i % NB]);
+          else
+            dk[i % NB] = A::mma(f, sf[i / NB - 2], dk[i % NB]);
+        });
   };
   if constexpr (!SINK) {
     if (n_tiles > 0) fetch(0, 0);

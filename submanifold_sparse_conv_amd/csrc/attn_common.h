@@ -16,11 +16,13 @@ namespace trsc {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// Transposing LDS read: of 16 lanes, lane i gets element i % 4 of the 8 bytes
-// that lanes i / 4, i / 4 + 4, i / 4 + 8 and i / 4 + 12 name. The restrict
-// gives the read an alias scope of its own: without one the compiler waits for
-// every copy to LDS in flight before it, the next tile's too.
+// LDS reads. The restrict gives each an alias scope of its own: without one the
+// compiler waits for every copy to LDS in flight before it, the next tile's too.
+// Transposing: of 16 lanes, lane i gets element i % 4 of the 8 bytes that lanes
+// i / 4, i / 4 + 4, i / 4 + 8 and i / 4 + 12 name.
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+template <class V>
+__device__ __forceinline__ V read_lds(const void* __restrict p) { return *static_cast<const V*>(p); }
 __device__ __forceinline__ s16x4 read_tr(lds_s16x4* __restrict p) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p); }
 
 template <class E>
@@ -151,11 +153,11 @@ struct Tile {
   // Row fragment: rows r0 + lane % 32 (r0 a multiple of 32), elements 16 s + 8 (lane / 32) + 0..7.
   static __device__ __forceinline__ frag row(const unsigned char* lds, int r0, int s, const Lane& o) {
     if constexpr (kElt == 2) {
-      return *reinterpret_cast<const frag*>(lds + r0 * kPitch + (o.row ^ (s << 5)));
+      return read_lds<frag>(lds + r0 * kPitch + (o.row ^ (s << 5)));
     } else {
       typedef float f4 __attribute__((ext_vector_type(4)));
-      const f4 a = *reinterpret_cast<const f4*>(lds + r0 * kPitch + (o.row ^ (s << 6)));
-      const f4 b = *reinterpret_cast<const f4*>(lds + r0 * kPitch + (o.row ^ (s << 6) ^ 16));
+      const f4 a = read_lds<f4>(lds + r0 * kPitch + (o.row ^ (s << 6)));
+      const f4 b = read_lds<f4>(lds + r0 * kPitch + (o.row ^ (s << 6) ^ 16));
       return frag{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
     }
   }
@@ -175,7 +177,7 @@ struct Tile {
     } else {
       frag f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = *reinterpret_cast<const float*>(from + (o.col[e] ^ (b << 7)));
+      for (int e = 0; e < 8; ++e) f[e] = read_lds<float>(from + (o.col[e] ^ (b << 7)));
       return f;
     }
   }
@@ -208,18 +210,23 @@ __device__ __forceinline__ float2 both_halves(float v) {
   return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-// Order of the matrix products' block before it: the LDS reads (READS for each
-// of the N products) run AHEAD products in front of the products that take them.
-template <int N, int READS, int AHEAD>
-__device__ __forceinline__ void schedule_reads() {
-  constexpr int kFirst = AHEAD < N ? AHEAD : N;
-  __builtin_amdgcn_sched_group_barrier(0x100, kFirst * READS, 0);  // LDS reads
+// N products in order, the fragments of each read from LDS `AHEAD` products
+// before it: load(i, f) and use(i, f). The scheduling barriers hold the order,
+// which the compiler's own schedule gives up for fewer registers (every product
+// then waits for its own reads).
+template <int N, int AHEAD, class Frags, class Load, class Use>
+__device__ __forceinline__ void products(const Load& load, const Use& use) {
+  constexpr int kSlots = AHEAD < N ? AHEAD : N;
+  Frags f[kSlots];
 #pragma unroll
-  for (int i = 0; i < N - kFirst; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix
-    __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+  for (int i = 0; i < kSlots; ++i) load(i, f[i]);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    use(i, f[i % kSlots]);
+    if (i + kSlots < N) load(i + kSlots, f[i % kSlots]);
+    __builtin_amdgcn_sched_barrier(0);
   }
-  __builtin_amdgcn_sched_group_barrier(0x008, kFirst, 0);
 }
 
 // A sequence of the packed batch. Offsets and lengths from the device are

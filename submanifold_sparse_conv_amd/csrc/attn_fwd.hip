@@ -101,7 +101,7 @@ struct RowState {
   typedef Tile<E, NB> T;
   typedef AttnType<E> A;
   typedef typename A::frag frag;
-  static constexpr int ST = NB * 2;
+  static constexpr int ST = NB * 2, kAhead = A::wide ? 1 : 4;
   frag qf[ST];     // the queries
   f32x16 acc[NB];  // O^T
   float mc, l;     // scaled maximum (base 2) and sum of the weights
@@ -120,13 +120,11 @@ struct RowState {
   }
   __device__ __forceinline__ void scores(const unsigned char* ks, const typename T::Lane& at) {
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[kb][e] = 0.f;
-#pragma unroll
-      for (int st = 0; st < ST; ++st) s[kb] = A::mma(T::row(ks, 32 * kb, st, at), qf[st], s[kb]);
-    }
-    if constexpr (!A::wide) schedule_reads<KB * ST, 1, 4>();
+    products<KB * ST, kAhead, frag>([&](int i, frag& f) { f = T::row(ks, 32 * (i / ST), i % ST, at); },
+                                    [&](int i, const frag& f) { s[i / ST] = A::mma(f, qf[i % ST], s[i / ST]); });
   }
   // weights 2^(s c - m), their sum, and the fragments that multiply V
   __device__ __forceinline__ float weigh_by(float c, float m) {
@@ -165,13 +163,9 @@ struct RowState {
     l += sum;
   }
   __device__ __forceinline__ void multiply(const unsigned char* vs, const typename T::Lane& at) {
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-      for (int ss = 0; ss < 2; ++ss)
-#pragma unroll
-        for (int d = 0; d < NB; ++d) acc[d] = A::mma(T::col(vs, 32 * kb, ss, d, at), pf[kb][ss], acc[d]);
-    if constexpr (!A::wide) schedule_reads<KB * 2 * NB, 2, 4>();
+    products<KB * 2 * NB, kAhead, frag>(
+        [&](int i, frag& f) { f = T::col(vs, 32 * (i / (2 * NB)), i / NB % 2, i % NB, at); },
+        [&](int i, const frag& f) { acc[i % NB] = A::mma(f, pf[i / (2 * NB)][i / NB % 2], acc[i % NB]); });
   }
   __device__ __forceinline__ void join_halves() {
     const float2 lh = both_halves(l);
