@@ -379,8 +379,8 @@ int tr_sparseconv_qk_norm_rope(const tr_sc_heads* q, const tr_sc_heads* k, const
                                const tr_sc_heads* k_out, int64_t tokens, int dim, int dtype, void* stream);
 
 /* Its gradient: dq_out, dk_out -> dq, dk (all [tokens, heads, dim] of type
- * dtype), dq_gain, dk_gain (fp32, as the gains; NULL: not wanted). q, k: the
- * forward's inputs. dq, dk may be dq_out, dk_out themselves (same strides). The
+ * dtype), dq_gain, dk_gain (fp32, as the gains, 16-byte aligned; NULL: not
+ * wanted). q, k: the forward's inputs. dq, dk may be dq_out, dk_out themselves (same strides). The
  * gains' sums are taken in a fixed order (no atomics: the same bits on every
  * call). workspace: >= the bytes below, 256-byte aligned. */
 size_t tr_sparseconv_qk_norm_rope_backward_workspace_bytes(int64_t tokens, int q_heads, int kv_heads,

@@ -261,7 +261,8 @@ __device__ __forceinline__ bool tile_whole(const AttnArgs& a, const WaveRows& w,
 template <class E, int NB, bool TOKEN>
 struct FwdShape {
   typedef Tile<E, NB> T;
-  static constexpr int kKeys = TOKEN ? 32 : 64;
+  // fp32 products are sixteen times the half types' time: smaller tiles waste less of them at the window's edges
+  static constexpr int kKeys = TOKEN || sizeof(E) == 4 ? 32 : 64;
   static constexpr int kTileBytes = kKeys * T::kPitch;
   // token form: every wave has its own tiles
   static constexpr int kBuffers = (TOKEN && sizeof(E) == 4 && NB > 2) ? 1 : 2;
@@ -271,7 +272,7 @@ struct FwdShape {
 };
 
 template <class E, int NB, bool TOKEN>
-__global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_fwd(AttnArgs a, int tiles, int splits) {
+__global__ __launch_bounds__(256, sizeof(E) == 4 && NB == 4 ? 1 : 2) void attn_fwd(AttnArgs a, int tiles, int splits) {
   typedef FwdShape<E, NB, TOKEN> F;
   typedef Tile<E, NB> T;
   constexpr int KB = F::kKeys / 32;
@@ -549,7 +550,7 @@ AttnPlan plan_attention(const AttnArgs& a) {
   // up to 32 rows a sequence on average: the token form
   p.token_form = int64_t(a.nq) * group <= int64_t(32) * a.batch;
   const int64_t tiles = tiles_of(a.nq, a.batch, group, p.token_form ? 32 : 128) * a.hk;
-  const int keys = p.token_form ? 32 : 64;
+  const int keys = p.token_form || a.dtype == TR_SC_F32 ? 32 : 64;
   // keys that one row tile can see at most
   const int64_t reach = int64_t(a.left) + a.right + 1 + a.sinks + (p.token_form ? 32 : 128) / group;
   const int64_t span = reach < a.nk ? reach : a.nk;

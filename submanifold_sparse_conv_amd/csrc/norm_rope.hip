@@ -230,29 +230,44 @@ __global__ __launch_bounds__(kNormThreads) void norm_rope_kernel(NormArgs a, int
 
 // dgain[row, d] = the sum, in a fixed order, of the workgroups' partials
 // [splits][heads][dim] over the splits and, for a shared gain, the heads of
-// that side. blockIdx.y: side. 32 columns x 8 row slices a workgroup.
+// that side. blockIdx.y: side. L lanes of four columns by 256 / L slices of the
+// splits: few columns (a shared gain) take few lanes and many slices.
+template <int L>
 __global__ __launch_bounds__(256) void gain_sum(NormArgs a, int splits) {
+  constexpr int kSlices = 256 / L;
   const NormSide& s = blockIdx.y == 0 ? a.q : a.k;
   if (s.dgain == nullptr) return;
   const int h0 = blockIdx.y == 0 ? 0 : a.q.heads, heads = a.q.heads + a.k.heads;
-  const int cols = s.gain_rows * a.dim;
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
-  __shared__ float s_part[8][32];
-  const int inner = s.gain_rows == 1 ? s.heads : 1;  // rows of one split that add to this column
-  const int64_t rows = int64_t(splits) * inner;
-  float v = 0.f;
+  const int cols = s.gain_rows * a.dim, inner = s.gain_rows == 1 ? s.heads : 1;
+  const int lane = threadIdx.x % L, slice = threadIdx.x / L;
+  const int col = (blockIdx.x * L + lane) * 4;
+  __shared__ float4 s_part[256];
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float4& x) {
+    v.x += x.x;
+    v.y += x.y;
+    v.z += x.z;
+    v.w += x.w;
+  };
   if (col < cols) {
     const float* src = a.partials + int64_t(h0) * a.dim + col;
-    for (int64_t i = slice; i < rows; i += 8)
-      v += src[(i / inner) * heads * a.dim + (i % inner) * a.dim];
+    for (int i = slice; i < splits; i += kSlices) {
+      const float* p = src + int64_t(i) * heads * a.dim;
+#pragma unroll 4
+      for (int h = 0; h < inner; ++h) add(*reinterpret_cast<const float4*>(p + h * a.dim));
+    }
   }
-  s_part[slice][threadIdx.x & 31] = v;
+  s_part[threadIdx.x] = v;
   __syncthreads();
-  if (slice == 0 && col < cols) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) v += s_part[i][threadIdx.x];
-    s.dgain[col] = v;
+  for (int n = kSlices / 2; n > 0; n >>= 1) {
+    if (slice < n) {
+      add(s_part[(slice + n) * L + lane]);
+      s_part[threadIdx.x] = v;
+    }
+    __syncthreads();
   }
+  if (slice == 0 && col < cols) *reinterpret_cast<float4*>(s.dgain + col) = v;
 }
 
 int chunk_elems(int dim) { return dim % 16 == 0 ? 8 : 4; }
@@ -323,8 +338,11 @@ hipError_t launch_norm_rope_backward(const NormArgs& a, hipStream_t st) {
     if (e != hipSuccess) return e;
   }
   if (a.q.dgain || a.k.dgain) {
-    const int rows = a.q.gain_rows > a.k.gain_rows ? a.q.gain_rows : a.k.gain_rows;
-    gain_sum<<<dim3((rows * a.dim + 31) / 32, 2), 256, 0, st>>>(a, splits);
+    const int cols = (a.q.gain_rows > a.k.gain_rows ? a.q.gain_rows : a.k.gain_rows) * a.dim;
+    if (cols >= 1024)
+      gain_sum<8><<<dim3((cols + 31) / 32, 2), 256, 0, st>>>(a, splits);
+    else
+      gain_sum<2><<<dim3((cols + 7) / 8, 2), 256, 0, st>>>(a, splits);
   }
   return hipGetLastError();
 }

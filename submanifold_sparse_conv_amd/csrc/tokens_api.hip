@@ -252,6 +252,8 @@ int tr_sparseconv_qk_norm_rope_backward(const tr_sc_heads* dq_out, const tr_sc_h
   if (c != TR_SC_OK) return c;
   if ((dq_gain != nullptr && q_gain == nullptr) || (dk_gain != nullptr && k_gain == nullptr))
     return fail(TR_SC_ERR_INVALID_ARG, "%s: the gradient of a gain that is not there", who);
+  if (reinterpret_cast<uintptr_t>(dq_gain) % 16 != 0 || reinterpret_cast<uintptr_t>(dk_gain) % 16 != 0)
+    return fail(TR_SC_ERR_INVALID_ARG, "%s: dq_gain and dk_gain must be 16-byte aligned", who);
   set_grad(&a.q, dq_out);
   set_grad(&a.k, dk_out);
   set_out(&a.q, dq);

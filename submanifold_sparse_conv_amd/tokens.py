@@ -24,17 +24,20 @@ _byref = ctypes.byref
 def _heads(t, name: str, tokens=None, heads=None, dim=None, like: torch.Tensor | None = None) -> Heads:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, dim], got {tuple(t.shape)}")
-    n, h, d = t.shape
-    if (tokens is not None and n != tokens) or (heads is not None and h != heads) or (dim is not None and d != dim):
-        want = ["*" if w is None else w for w in (tokens, heads, dim)]
-        raise ValueError(f"{name} must be [{want[0]}, {want[1]}, {want[2]}], got {tuple(t.shape)}")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, dim], got {tuple(shape)}")
+    n, h, d = shape
+    if like is not None:
+        if d != dim or (tokens is not None and n != tokens) or (heads is not None and h != heads):
+            want = ["*" if w is None else w for w in (tokens, heads, dim)]
+            raise ValueError(f"{name} must be [{want[0]}, {want[1]}, {want[2]}], got {tuple(shape)}")
+        if t.dtype is not like.dtype or t.device != like.device:
+            raise ValueError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
     st, sh, sd = t.stride()
     if sd != 1 and d > 1:
         raise ValueError(f"the elements of a row of {name} must be adjacent")
+    # a stride that is never taken may be anything
     return Heads(t.data_ptr() if n else None, st if n > 1 else 0, sh if h > 1 else 0, h)
 
 
@@ -56,16 +59,40 @@ def _ints(t, name: str, n: int, device):
 
 
 def _scratch(nbytes: int, device, given):
-    """(pointer, bytes, owner) of a workspace, from the package's Workspace."""
-    if nbytes == 0 and given is None:
+    """(pointer, bytes, owner) of a workspace; torch's own blocks are aligned to 256 bytes and more."""
+    if given is not None:
+        if given.nbytes < nbytes:
+            raise ValueError(f"workspace of {given.nbytes} bytes, {nbytes} needed")
+        return given.ptr, given.nbytes, given
+    if nbytes == 0:
         return None, 0, None
-    from . import _workspace
-    ws = _workspace(nbytes, device, given)
-    return ws.ptr, ws.nbytes, ws
+    buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return buf.data_ptr(), nbytes, buf
 
 
-def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+def _out(out, name: str, tokens: int, heads: int, dim: int, like: torch.Tensor):
+    """An output of the caller's, or a new contiguous one, with its view."""
+    if out is not None:
+        return out, _heads(out, name, tokens, heads, dim, like)
+    out = like.new_empty((tokens, heads, dim))
+    return out, Heads(out.data_ptr() if tokens else None, heads * dim if tokens > 1 else 0, dim if heads > 1 else 0,
+                      heads)
+
+
+# The stream's address without a Stream object around it, where torch has the call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(fn, device, *args) -> None:
+    """fn(*args, stream) on the device's current stream. (A call of a few
+    microseconds: the context manager is entered only for another device.)"""
+    stream = _raw_stream(device.index)
+    if torch.cuda.current_device() == device.index:
+        check(fn(*args, stream))
+    else:
+        with torch.cuda.device(device):
+            check(fn(*args, stream))
 
 
 def rope_frequencies(dim: int, axes: int = 1, theta: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -133,14 +160,10 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, freqs: tor
     rot = _rotation(pos, freqs, sections, interleaved, n, dim, dev)
     qg, qr = _gain(q_gain, "q_gain", hq.heads, dim, dev)
     kg, kr = _gain(k_gain, "k_gain", hk.heads, dim, dev)
-    if q_out is None:
-        q_out = torch.empty((n, hq.heads, dim), dtype=q.dtype, device=dev)
-    if k_out is None:
-        k_out = torch.empty((n, hk.heads, dim), dtype=q.dtype, device=dev)
-    ho, hp = _heads(q_out, "q_out", n, hq.heads, dim, q), _heads(k_out, "k_out", n, hk.heads, dim, q)
-    with torch.cuda.device(dev):
-        check(_lib.lib().tr_sparseconv_qk_norm_rope(_byref(hq), _byref(hk), _byref(rot), qg, qr, kg, kr, eps,
-                                                    _byref(ho), _byref(hp), n, dim, dt, _stream(dev)))
+    q_out, ho = _out(q_out, "q_out", n, hq.heads, dim, q)
+    k_out, hp = _out(k_out, "k_out", n, hk.heads, dim, q)
+    _call(_lib.lib().tr_sparseconv_qk_norm_rope, dev, _byref(hq), _byref(hk), _byref(rot), qg, qr, kg, kr, eps,
+          _byref(ho), _byref(hp), n, dim, dt)
     return q_out, k_out
 
 
@@ -161,21 +184,16 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
     rot = _rotation(pos, freqs, sections, interleaved, n, dim, dev)
     qg, qr = _gain(q_gain, "q_gain", hq.heads, dim, dev)
     kg, kr = _gain(k_gain, "k_gain", hk.heads, dim, dev)
-    if dq is None:
-        dq = torch.empty((n, hq.heads, dim), dtype=q.dtype, device=dev)
-    if dk is None:
-        dk = torch.empty((n, hk.heads, dim), dtype=q.dtype, device=dev)
-    oq, ok = _heads(dq, "dq", n, hq.heads, dim, q), _heads(dk, "dk", n, hk.heads, dim, q)
+    dq, oq = _out(dq, "dq", n, hq.heads, dim, q)
+    dk, ok = _out(dk, "dk", n, hk.heads, dim, q)
     dqg = None if q_gain is None else torch.empty_like(q_gain)
     dkg = None if k_gain is None else torch.empty_like(k_gain)
     L = _lib.lib()
     ptr, nbytes, _keep = _scratch(
         L.tr_sparseconv_qk_norm_rope_backward_workspace_bytes(n, hq.heads, hk.heads, dim), dev, workspace)
-    with torch.cuda.device(dev):
-        check(L.tr_sparseconv_qk_norm_rope_backward(
-            _byref(gq), _byref(gk), _byref(hq), _byref(hk), _byref(rot), qg, qr, kg, kr, eps, _byref(oq), _byref(ok),
-            None if dqg is None else dqg.data_ptr(), None if dkg is None else dkg.data_ptr(), n, dim, dt, ptr, nbytes,
-            _stream(dev)))
+    _call(L.tr_sparseconv_qk_norm_rope_backward, dev, _byref(gq), _byref(gk), _byref(hq), _byref(hk), _byref(rot), qg,
+          qr, kg, kr, eps, _byref(oq), _byref(ok), None if dqg is None else dqg.data_ptr(),
+          None if dkg is None else dkg.data_ptr(), n, dim, dt, ptr, nbytes)
     return dq, dk, dqg, dkg
 
 
@@ -213,18 +231,14 @@ def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     hv = _heads(v, "v", m, hk.heads, dim, q)
     dev = q.device
     win = _window(cu_q, cu_k, k_len, left, right, sinks, scale, dim, dev)
-    if out is None:
-        out = torch.empty((n, hq.heads, dim), dtype=q.dtype, device=dev)
-    ho = _heads(out, "out", n, hq.heads, dim, q)
+    out, ho = _out(out, "out", n, hq.heads, dim, q)
     lse = torch.empty((hq.heads, n), dtype=torch.float32, device=dev) if return_lse else None
     L = _lib.lib()
     ptr, nbytes, _keep = _scratch(
         L.tr_sparseconv_window_attention_workspace_bytes(_byref(win), n, m, hq.heads, hk.heads, dim, dt), dev,
         workspace)
-    with torch.cuda.device(dev):
-        check(L.tr_sparseconv_window_attention(
-            _byref(hq), _byref(hk), _byref(hv), _byref(win), _byref(ho), None if lse is None else lse.data_ptr(), n,
-            m, dim, dt, ptr, nbytes, _stream(dev)))
+    _call(L.tr_sparseconv_window_attention, dev, _byref(hq), _byref(hk), _byref(hv), _byref(win), _byref(ho),
+          None if lse is None else lse.data_ptr(), n, m, dim, dt, ptr, nbytes)
     return (out, lse) if return_lse else out
 
 
@@ -253,8 +267,6 @@ def window_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tens
     ptr, nbytes, _keep = _scratch(
         L.tr_sparseconv_window_attention_backward_workspace_bytes(_byref(win), n, m, hq.heads, hk.heads, dim, dt),
         dev, workspace)
-    with torch.cuda.device(dev):
-        check(L.tr_sparseconv_window_attention_backward(
-            _byref(hd), _byref(hq), _byref(hk), _byref(hv), _byref(ho), lse.data_ptr(), _byref(win), dq.data_ptr(),
-            dk.data_ptr(), dv.data_ptr(), n, m, dim, dt, ptr, nbytes, _stream(dev)))
+    _call(L.tr_sparseconv_window_attention_backward, dev, _byref(hd), _byref(hq), _byref(hk), _byref(hv), _byref(ho),
+          lse.data_ptr(), _byref(win), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), n, m, dim, dt, ptr, nbytes)
     return dq, dk, dv
