@@ -272,10 +272,12 @@ struct FwdShape {
 };
 
 template <class E, int NB, bool TOKEN>
-__global__ __launch_bounds__(256, sizeof(E) == 4 && NB == 4 ? 1 : 2) void attn_fwd(AttnArgs a, int tiles, int splits) {
+__global__ __launch_bounds__(256, sizeof(E) == 4 && NB == 4 ? 1 : sizeof(E) == 2 && NB <= 2 && !TOKEN ? 4 : 2) void attn_fwd(AttnArgs a, int tiles, int splits) {
   typedef FwdShape<E, NB, TOKEN> F;
   typedef Tile<E, NB> T;
-  constexpr int KB = F::kKeys / 32;
+  // 32-key blocks whose scores are held at once: heads of 64 and less do best with four waves a SIMD and
+  // one block (four objects of 74 k tokens x 16: 426 us, with two blocks 455), wider ones with two (27 us of 1010 less)
+  constexpr int KB = NB <= 2 ? 1 : F::kKeys / 32;
   __shared__ __attribute__((aligned(1024))) unsigned char s_mem[F::kLds];
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -307,15 +309,18 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 && NB == 4 ? 1 : 2) void attn_f
   };
   auto compute = [&](int it, int buf) {
     const unsigned char* ks = mem + buf * 2 * F::kTileBytes;
-    const int j0 = kt.at(it) * F::kKeys, j1 = j0 + F::kKeys - 1;
-    if (!tile_seen(a, wr, j0, j1)) return;
-    st.scores(ks, at);
-    if (!tile_whole(a, wr, j0, j1, q.lk)) {
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) hide(st.s[kb], j0 + 32 * kb, wr.lo, wr.hi, a.sinks, lane);
+    for (int part = 0; part < F::kKeys / (32 * KB); ++part) {
+      const int j0 = kt.at(it) * F::kKeys + part * 32 * KB, j1 = j0 + 32 * KB - 1;
+      if (!tile_seen(a, wr, j0, j1)) continue;
+      st.scores(ks + part * 32 * KB * T::kPitch, at);
+      if (!tile_whole(a, wr, j0, j1, q.lk)) {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) hide(st.s[kb], j0 + 32 * kb, wr.lo, wr.hi, a.sinks, lane);
+      }
+      st.weigh(c);
+      st.multiply(ks + F::kTileBytes + part * 32 * KB * T::kPitch, at);
     }
-    st.weigh(c);
-    st.multiply(ks + F::kTileBytes, at);
   };
 
   if constexpr (!TOKEN) {
