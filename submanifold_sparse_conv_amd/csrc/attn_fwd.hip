@@ -561,7 +561,8 @@ AttnPlan plan_attention(const AttnArgs& a) {
   const int64_t span = reach < a.nk ? reach : a.nk;
   const int64_t per = p.token_form ? 4 : 1;  // tiles that a workgroup takes at once
   const int64_t key_rounds = (span + keys * per - 1) / (keys * per);
-  const int64_t want = 512;
+  // workgroups that the chip holds at once (by LDS: one a CU in the token form of wide heads, else two)
+  const int64_t want = p.token_form && (a.dim > 64 || a.dtype == TR_SC_F32) ? 256 : 512;
   int64_t s = (want + tiles - 1) / tiles;
   if (s > key_rounds / 2) s = key_rounds / 2;  // at least two rounds each
   if (s > 256) s = 256;
