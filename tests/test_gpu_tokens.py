@@ -482,3 +482,29 @@ def test_graph_replay():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("dim", [32, 64, 96, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_attention_gradient_of_short_windows_keeps_its_precision(dtype, dim):
+    """Two independent roundings of the type on the way to every sum of dq, dk and
+    dv (the weights' or dS's, and the last): sqrt(2) times the rms error of
+    rounding the exact gradient once, with a sixth for what they share. The
+    rounding of the forward's result, a share of every dS of a row, must not add
+    to them."""
+    n, hk, g = 1000, 2, gen(23)
+    q, k, v, dout = (randn(g, n, hk, dim, dtype=TD[dtype], scale=s) for s in (1.3, 1.3, 1.0, 1.0))
+    how = dict(left=16, right=0, sinks=4)
+    on = [x.to(DEV) for x in (q, k, v, dout)]
+    out, lse = sc.window_attention(*on[:3], return_lse=True, **how)
+    grads = sc.window_attention_backward(on[3], *on[:3], out, lse, **how)
+    i = torch.arange(n)
+    sees = (i[None] <= i[:, None]) & ((i[None] >= i[:, None] - 16) | (i[None] < 4))
+    x = [t.double().transpose(0, 1).contiguous().requires_grad_() for t in (q, k, v)]
+    z = (x[0] @ x[1].transpose(1, 2).contiguous() * dim ** -0.5).masked_fill(~sees, -math.inf)
+    exact = torch.autograd.grad((torch.softmax(z, -1) @ x[2] * dout.double().transpose(0, 1)).sum(), x)
+    for name, a, b in zip(("dq", "dk", "dv"), grads, exact):
+        b = b.transpose(0, 1)
+        once = (b.to(TD[dtype]).double() - b).norm()
+        err = (a.cpu().double() - b).norm()
+        assert err < math.sqrt(2) * 7 / 6 * once, (name, float(err / once))
