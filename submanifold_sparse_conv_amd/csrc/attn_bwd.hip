@@ -286,9 +286,10 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
 __device__ __forceinline__ int token_at(int64_t t, int lq) { return t < 0 ? 0 : t > lq ? lq : int(t); }
 
 // What a tile's rows need besides their elements.
+template <int ROWS>
 struct alignas(16) RowStats {
-  float2 stat[kRowTile];  // base-2 lse (0 for a row that sees nothing) and delta
-  int pos[kRowTile];      // position, or far below every window for a row that is not there
+  float2 stat[ROWS];  // base-2 lse (0 for a row that sees nothing) and delta
+  int pos[ROWS];      // position, or far below every window for a row that is not there
 };
 constexpr int kNoRow = -(1 << 30);  // kNoRow + right < 0, and kNoRow - left does not wrap
 
@@ -302,7 +303,9 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
   typedef AttnType<E> A;
   typedef typename A::frag frag;
   constexpr int ST = NB * 2, kAhead = A::wide ? 1 : SINK ? 2 : 4;
-  constexpr int kTileBytes = kRowTile * T::kPitch;
+  constexpr int kRows = SINK || A::wide || NB > 2 ? kRowTile : 2 * kRowTile;  // rows between two barriers
+  typedef RowStats<kRows> Stats;
+  constexpr int kTileBytes = kRows * T::kPitch;
   constexpr int kSets = SINK ? 4 : 1;                       // LDS tile sets: a wave's own, or shared
   constexpr int kBuffers = SINK ? 1 : 2;                    // a sink workgroup's other half waits on the CU instead
   constexpr int kLds = kSets * kBuffers * 2 * kTileBytes;
@@ -313,9 +316,9 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
   // one array: with two, every copy to LDS is tracked by the array it goes to,
   // and a tile's reads wait for the next tile's copies
   constexpr int kTiles = kLds > kJoin ? kLds : kJoin;
-  __shared__ __attribute__((aligned(1024))) unsigned char s_mem[kTiles + kV + kSets * kBuffers * sizeof(RowStats)];
+  __shared__ __attribute__((aligned(1024))) unsigned char s_mem[kTiles + kV + kSets * kBuffers * sizeof(Stats)];
   unsigned char* const s_v = s_mem + kTiles;
-  RowStats* const s_stat = reinterpret_cast<RowStats*>(s_mem + kTiles + kV);
+  Stats* const s_stat = reinterpret_cast<Stats*>(s_mem + kTiles + kV);
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.hq / a.hk;
@@ -380,7 +383,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
 #pragma unroll
     for (int e = 0; e < 16; ++e) dk[d][e] = dv[d][e] = 0.f;
   const float c = a.scale * kLog2e;
-  const int n_tiles = r_end > r_begin ? (r_end - r_begin + kRowTile - 1) / kRowTile : 0;
+  const int n_tiles = r_end > r_begin ? (r_end - r_begin + kRows - 1) / kRows : 0;
   const E* qbase = static_cast<const E*>(a.q.p) + int64_t(q.q0) * a.q.ts + int64_t(kvh) * group * a.q.hs;
   const E* dbase = static_cast<const E*>(a.dout.p) + int64_t(q.q0) * a.dout.ts + int64_t(kvh) * group * a.dout.hs;
 
@@ -388,13 +391,14 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
 
   // The rows of a tile as copies: offsets from the tile's first token, the same
   // for every tile where the group divides the tile.
-  constexpr int kCopies = kRowTile / T::kRowsPerCopy, kStep = SINK ? 1 : 4, kMine = (kCopies + kStep - 1) / kStep;
+  constexpr int kCopies = kRows / T::kRowsPerCopy, kStep = SINK ? 1 : 4, kMine = (kCopies + kStep - 1) / kStep;
   const bool even = kRowTile % group == 0;
   const int tok_begin = r_begin / group, tok_step = kRowTile / group;
-  auto first_token = [&](int it) { return even ? tok_begin + it * tok_step : (r_begin + it * kRowTile) / group; };
+  // of the block of kRowTile rows n
+  auto first_token = [&](int n) { return even ? tok_begin + n * tok_step : (r_begin + n * kRowTile) / group; };
   uint32_t oq[kMine], od[kMine];
   auto offsets = [&](int it) {
-    const int t0 = r_begin + it * kRowTile, tok0 = first_token(it);
+    const int t0 = r_begin + it * kRows, tok0 = first_token(it * (kRows / kRowTile));
 #pragma unroll
     for (int j = 0; j < kMine; ++j) {
       const int rr = (SINK ? j : j * 4 + wave) * T::kRowsPerCopy + lane / T::kChunks;
@@ -412,13 +416,13 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
   if (even) offsets(0);
   auto fetch = [&](int it, int set) {
     unsigned char* dst = s_mem + set * 2 * kTileBytes;
-    const int t0 = r_begin + it * kRowTile, tok0 = first_token(it);
+    const int t0 = r_begin + it * kRows, tok0 = first_token(it * (kRows / kRowTile));
     const buffer_t bq = buffer_of(qbase + tok0 * a.q.ts, 0x7fffffffu);
     const buffer_t bd = buffer_of(dbase + tok0 * a.dout.ts, 0x7fffffffu);
     if (!even) offsets(it);
     // Past the rows: out of the buffer. (In place, in the last tile: a register
     // that a copy's offset was in is not reused before the copy has landed.)
-    if (t0 + kRowTile > r_end) {
+    if (t0 + kRows > r_end) {
 #pragma unroll
       for (int j = 0; j < kMine; ++j) {
         const bool in = t0 + (SINK ? j : j * 4 + wave) * T::kRowsPerCopy + lane / T::kChunks < r_end;
@@ -434,18 +438,21 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
       copy_lds16(bd, od[j], dst + kTileBytes + n * 1024);
     }
     if (SINK || wave == 3) {
-      const buffer_t bs = buffer_of(stat + t0, uint32_t(min(kRowTile, r_end - t0)) * 8);
-      copy_lds4(bs, lane * 4, reinterpret_cast<unsigned char*>(s_stat[set].stat));
-      if (lane < kRowTile) s_stat[set].pos[lane] = t0 + lane < r_end ? (t0 + lane) / group + shift : kNoRow;
+      const buffer_t bs = buffer_of(stat + t0, uint32_t(min(kRows, r_end - t0)) * 8);
+#pragma unroll
+      for (int i = 0; i < kRows / 32; ++i)
+        copy_lds4(bs, 256 * i + lane * 4, reinterpret_cast<unsigned char*>(s_stat[set].stat) + 256 * i);
+      if (lane < kRows) s_stat[set].pos[lane] = t0 + lane < r_end ? (t0 + lane) / group + shift : kNoRow;
     }
   };
-  auto compute = [&](int it, int set) {
+  auto block = [&](int it, int set, int rb) {  // rows 32 rb .. of tile `it`
     typename T::Lane at = lanes;
     if constexpr (!kKeepV) at.fresh();
-    const unsigned char* qs = s_mem + set * 2 * kTileBytes;
+    const unsigned char* qs = s_mem + set * 2 * kTileBytes + rb * kRowTile * T::kPitch;
     const unsigned char* ds_ = qs + kTileBytes;
-    const int t0 = r_begin + it * kRowTile;
-    const int p0 = first_token(it) + shift;
+    const int t0 = r_begin + it * kRows + rb * kRowTile;
+    if (kRows > kRowTile && t0 >= r_end) return;
+    const int p0 = first_token(it * (kRows / kRowTile) + rb) + shift;
     const int p1 = (even ? min(p0 + max(tok_step, 1) - 1, (r_end - 1) / group + shift)
                          : min(t0 + kRowTile - 1, r_end - 1) / group + shift);
     const int j1 = jw + 31;
@@ -470,7 +477,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
             f.v = T::row(s_v, SINK ? 0 : 32 * wave, i, at);
           },
           [&](int i, const Pair& f) { dp = A::mma(f.row, f.v, dp); });
-    const RowStats& rs = s_stat[set];
+    const float2* const stats = s_stat[set].stat + rb * kRowTile;
+    const int* const at_pos = s_stat[set].pos + rb * kRowTile;
     // weights into s, score gradients into dp; of what a row does not see, zero.
     // Both branches end with their fragments, so that the products are a block
     // of their own and their reads can be put in order.
@@ -485,7 +493,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
     if (all) {
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const float4 s0 = read_lds<float4>(&rs.stat[8 * g + 4 * h]), s1 = read_lds<float4>(&rs.stat[8 * g + 4 * h + 2]);
+        const float4 s0 = read_lds<float4>(&stats[8 * g + 4 * h]), s1 = read_lds<float4>(&stats[8 * g + 4 * h + 2]);
         const float lv[4] = {s0.x, s0.z, s1.x, s1.z}, ev[4] = {s0.y, s0.w, s1.y, s1.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -498,8 +506,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
     } else {
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const float4 s0 = read_lds<float4>(&rs.stat[8 * g + 4 * h]), s1 = read_lds<float4>(&rs.stat[8 * g + 4 * h + 2]);
-        const int4 po = read_lds<int4>(&rs.pos[8 * g + 4 * h]);
+        const float4 s0 = read_lds<float4>(&stats[8 * g + 4 * h]), s1 = read_lds<float4>(&stats[8 * g + 4 * h + 2]);
+        const int4 po = read_lds<int4>(&at_pos[8 * g + 4 * h]);
         const float lv[4] = {s0.x, s0.z, s1.x, s1.z}, ev[4] = {s0.y, s0.w, s1.y, s1.w};
         const int pv[4] = {po.x, po.y, po.z, po.w};
 #pragma unroll
@@ -522,6 +530,10 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
           else
             dk[i % NB] = A::mma(f, sf[i / NB - 2], dk[i % NB]);
         });
+  };
+  auto compute = [&](int it, int set) {
+#pragma unroll
+    for (int rb = 0; rb < kRows / kRowTile; ++rb) block(it, set, rb);
   };
   if constexpr (!SINK) {
     if (n_tiles > 0) fetch(0, 0);
