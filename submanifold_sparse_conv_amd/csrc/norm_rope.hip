@@ -14,13 +14,21 @@
 // has no error that grows with the position.
 //
 // Layout. A row (token, head) of dim elements is held by dim / (2 E) lanes (the
-// group; E = 8 elements, or 4 where dim is no multiple of 16): lane c holds
-// elements [c E, c E + E) of either half of the row, so both pairings have
-// their pairs inside one lane. A wave holds 64 / group rows: the same token's
+// group; E = 4 elements): lane c holds elements [c E, c E + E) of either half of
+// the row, so both pairings have their pairs inside one lane. (E = 8 halves the
+// lanes' instructions but holds five waves a SIMD, backward three, instead of
+// eight and five: forward 128 us for 122 at the first size below, backward the
+// same.) A wave holds 64 / group rows: the same token's
 // consecutive heads. Its heads stay the same over the tokens that it walks, so
 // a lane's gains (and the backward's sums of their gradients) live in
 // registers. The sines and cosines of a token are computed once a wave, one
 // pair a lane, and handed out through LDS that only this wave uses.
+//
+// What bounds it: memory, each element read and written once (backward: two
+// read). bf16, 73,881 tokens x 32 heads of 64: 605 MB in 122 us, 4.96 TB/s, the
+// rate of a large copy (5.03 TB/s). fp32, 16,219 x 16 heads of 72: 149 MB in
+// 26.6 us (in part from the caches). Backward, bf16, 15,800 x 24 heads of 128:
+// 291 MB in 58 us with the gains' sums, 5.0 TB/s. 32 tokens: 4.3 us, one launch.
 #include "common.h"
 #include "token_types.h"
 #include "tokens.h"
@@ -29,6 +37,7 @@ namespace trsc {
 namespace {
 
 constexpr int kWaves = 4;
+constexpr int E = 4;  // elements of either half of a row in a lane
 constexpr int kNormThreads = kWaves * 64;
 
 template <class T>
@@ -69,13 +78,12 @@ __device__ __forceinline__ void turn_table(const NormArgs& a, int32_t p, double 
   table[lane] = cs;
 }
 
-template <int E>
 __device__ __forceinline__ float group_sum(float v, int group) {
   for (int o = group >> 1; o > 0; o >>= 1) v += __shfl_xor(v, o);
   return v;
 }
 
-template <class T, int E, bool IL, bool BWD>
+template <class T, bool IL, bool BWD>
 __global__ __launch_bounds__(kNormThreads) void norm_rope_kernel(NormArgs a, int group) {
   typedef typename T::elt elt;
   __shared__ float2 s_turn[kWaves][64];
@@ -136,7 +144,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_rope_kernel(NormArgs a, int
 #pragma unroll
     for (int e = 0; e < E; ++e) ss += x[0][e] * x[0][e] + x[1][e] * x[1][e];
     if (!on) ss = 0.f;
-    ss = group_sum<E>(ss, group);
+    ss = group_sum(ss, group);
     const float r = rsqrtf(ss * inv_dim + a.eps);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the table is the wave's own
     float2 cs[E];  // IL: E / 2 pairs of the first chunk, then E / 2 of the second; else pair e
@@ -183,7 +191,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_rope_kernel(NormArgs a, int
         dot += o[0][e] * x[0][e] + o[1][e] * x[1][e];
       }
       if (!on) dot = 0.f;
-      dot = group_sum<E>(dot, group) * inv_dim;
+      dot = group_sum(dot, group) * inv_dim;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         o[0][e] = r * (o[0][e] - x[0][e] * dot);
@@ -230,11 +238,11 @@ __global__ __launch_bounds__(kNormThreads) void norm_rope_kernel(NormArgs a, int
 
 // dgain[row, d] = the sum, in a fixed order, of the workgroups' partials
 // [splits][heads][dim] over the splits and, for a shared gain, the heads of
-// that side. blockIdx.y: side. L lanes of four columns by 256 / L slices of the
-// splits: few columns (a shared gain) take few lanes and many slices.
-template <int L>
+// that side. blockIdx.y: side. Two lanes of four columns each by 128 slices of
+// the splits, joined in a tree (15,800 tokens x 24 heads of 128, 208 splits: 5 us;
+// one thread a column walked all of them in 19).
 __global__ __launch_bounds__(256) void gain_sum(NormArgs a, int splits) {
-  constexpr int kSlices = 256 / L;
+  constexpr int L = 2, kSlices = 256 / L;
   const NormSide& s = blockIdx.y == 0 ? a.q : a.k;
   if (s.dgain == nullptr) return;
   const int h0 = blockIdx.y == 0 ? 0 : a.q.heads, heads = a.q.heads + a.k.heads;
@@ -270,41 +278,41 @@ __global__ __launch_bounds__(256) void gain_sum(NormArgs a, int splits) {
   if (slice == 0 && col < cols) *reinterpret_cast<float4*>(s.dgain + col) = v;
 }
 
-int chunk_elems(int dim) { return dim % 16 == 0 ? 8 : 4; }
 int group_lanes(int dim) {
-  const int lanes = dim / (2 * chunk_elems(dim));
+  const int lanes = dim / (2 * E);
   int g = 1;
   while (g < lanes) g <<= 1;
   return g;
 }
 
-// Workgroups over the tokens. Forward: each wave walks at least one token and
-// the launch holds up to `want` workgroups.
-int token_blocks(int64_t tokens, int head_blocks, int want) {
-  const int64_t most = (tokens + kWaves - 1) / kWaves;
-  const int64_t n = want / head_blocks > 1 ? want / head_blocks : 1;
-  return int(most < n ? most : n);
+// Workgroups over the tokens: `fill` in all, fewer where a wave would have no
+// token, and evened out so that every wave walks as many. Forward: four a CU
+// (eight fit; 132 us for 122 with them at the first size above). Backward: the
+// five a CU that fit (three: 62 us for 58).
+constexpr int kForwardFill = 1024, kBackwardFill = 1280;
+int token_blocks(int64_t tokens, int head_blocks, int fill) {
+  const int64_t n = fill / head_blocks > 1 ? fill / head_blocks : 1;
+  const int64_t walk = (tokens + n * kWaves - 1) / (n * kWaves);
+  return walk == 0 ? 0 : int((tokens + walk * kWaves - 1) / (walk * kWaves));
 }
-constexpr int kForwardBlocks = 2048, kBackwardBlocks = 1024;
 
-template <class T, int E, bool BWD>
-void launch_il(const NormArgs& a, dim3 grid, int group, hipStream_t st) {
+template <class T, bool BWD>
+void launch_pairs(const NormArgs& a, dim3 grid, hipStream_t st) {
+  const int group = group_lanes(a.dim);
   if (a.interleaved)
-    norm_rope_kernel<T, E, true, BWD><<<grid, kNormThreads, 0, st>>>(a, group);
+    norm_rope_kernel<T, true, BWD><<<grid, kNormThreads, 0, st>>>(a, group);
   else
-    norm_rope_kernel<T, E, false, BWD><<<grid, kNormThreads, 0, st>>>(a, group);
+    norm_rope_kernel<T, false, BWD><<<grid, kNormThreads, 0, st>>>(a, group);
 }
 
 template <bool BWD>
 void launch_typed(const NormArgs& a, dim3 grid, hipStream_t st) {
-  const int group = group_lanes(a.dim);
-  const bool wide = chunk_elems(a.dim) == 8;
   if (a.dtype == TR_SC_BF16)
-    wide ? launch_il<TBF16, 8, BWD>(a, grid, group, st) : launch_il<TBF16, 4, BWD>(a, grid, group, st);
+    launch_pairs<TBF16, BWD>(a, grid, st);
   else if (a.dtype == TR_SC_F16)
-    wide ? launch_il<TF16, 8, BWD>(a, grid, group, st) : launch_il<TF16, 4, BWD>(a, grid, group, st);
+    launch_pairs<TF16, BWD>(a, grid, st);
   else
-    wide ? launch_il<TF32, 8, BWD>(a, grid, group, st) : launch_il<TF32, 4, BWD>(a, grid, group, st);
+    launch_pairs<TF32, BWD>(a, grid, st);
 }
 
 int head_blocks(int heads, int dim) {
@@ -317,12 +325,12 @@ int head_blocks(int heads, int dim) {
 hipError_t launch_norm_rope(const NormArgs& a, hipStream_t st) {
   if (a.tokens == 0) return hipSuccess;
   const int hb = head_blocks(a.q.heads + a.k.heads, a.dim);
-  launch_typed<false>(a, dim3(token_blocks(a.tokens, hb, kForwardBlocks), hb), st);
+  launch_typed<false>(a, dim3(token_blocks(a.tokens, hb, kForwardFill), hb), st);
   return hipGetLastError();
 }
 
 static int backward_blocks(int64_t tokens, int heads, int dim) {
-  return token_blocks(tokens, head_blocks(heads, dim), kBackwardBlocks);
+  return token_blocks(tokens, head_blocks(heads, dim), kBackwardFill);
 }
 
 int64_t norm_rope_partials(int64_t tokens, int heads, int dim) {
@@ -339,10 +347,7 @@ hipError_t launch_norm_rope_backward(const NormArgs& a, hipStream_t st) {
   }
   if (a.q.dgain || a.k.dgain) {
     const int cols = (a.q.gain_rows > a.k.gain_rows ? a.q.gain_rows : a.k.gain_rows) * a.dim;
-    if (cols >= 1024)
-      gain_sum<8><<<dim3((cols + 31) / 32, 2), 256, 0, st>>>(a, splits);
-    else
-      gain_sum<2><<<dim3((cols + 7) / 8, 2), 256, 0, st>>>(a, splits);
+    gain_sum<<<dim3((cols + 7) / 8, 2), 256, 0, st>>>(a, splits);
   }
   return hipGetLastError();
 }
