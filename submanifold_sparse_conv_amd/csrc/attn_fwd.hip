@@ -118,13 +118,17 @@ struct RowState {
     mc = -INFINITY;
     l = 0.f;
   }
-  __device__ __forceinline__ void scores(const unsigned char* ks, const typename T::Lane& at) {
+  __device__ __forceinline__ void scores(const unsigned char* ks, int steps, const typename T::Lane& at) {
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[kb][e] = 0.f;
     products<KB * ST, kAhead, frag>([&](int i, frag& f) { f = T::row(ks, 32 * (i / ST), i % ST, at); },
-                                    [&](int i, const frag& f) { s[i / ST] = A::mma(f, qf[i % ST], s[i / ST]); });
+                                    [&](int i, const frag& f) {
+                                      // fp32: a last step of zeros (heads of 16 past 32's multiples) costs a branch less
+                                      if (!A::wide || i % ST < ST - 1 || steps == ST)
+                                        s[i / ST] = A::mma(f, qf[i % ST], s[i / ST]);
+                                    });
   }
   // weights 2^(s c - m), their sum, and the fragments that multiply V
   __device__ __forceinline__ float weigh_by(float c, float m) {
@@ -313,7 +317,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 && NB == 4 ? 1 : sizeof(E) == 2
     for (int part = 0; part < F::kKeys / (32 * KB); ++part) {
       const int j0 = kt.at(it) * F::kKeys + part * 32 * KB, j1 = j0 + 32 * KB - 1;
       if (!tile_seen(a, wr, j0, j1)) continue;
-      st.scores(ks + part * 32 * KB * T::kPitch, at);
+      st.scores(ks + part * 32 * KB * T::kPitch, (a.dim + 15) / 16, at);
       if (!tile_whole(a, wr, j0, j1, q.lk)) {
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) hide(st.s[kb], j0 + 32 * kb, wr.lo, wr.hi, a.sinks, lane);
