@@ -17,6 +17,22 @@
 // halves of the wave, the rescaling none. The registers of S^T are, as they
 // are, fragments of P^T for O^T += V^T P^T when V's keys are taken in the same
 // order, which the transposed LDS read of V gives (attn_common.h).
+//
+// Rounding. Scores, maxima, sums and the result's sums are fp32. The weights are
+// rounded to the tensors' type for the product with V (the matrix units take
+// half types; for fp32 tensors nothing is rounded), their sum takes them
+// unrounded: the result is off by that rounding's average and its own last one.
+//
+// What bounds it. bf16, 32,768 tokens, 16 query and 4 kv heads of 128, 4096 keys
+// back: 1.03 TFLOP in 1.00 ms, 1.03 PFLOP/s, of 1.19 that a large library product
+// reaches (both on clocks that power lowers): matrix units, one LDS fragment a
+// product. bf16, 73,881 tokens, 16 heads of 64, 512 keys either way: 0.31 TFLOP in
+// 426 us, 735 TFLOP/s: the 16 exponentials, sums and packings of every 8
+// products. fp32, 2,877 tokens in four sequences, 6 heads of 80 over 2, 255 either
+// way: 57 us, four splits a row tile to reach the chip, the products' padding (80
+// of 96) and the join. Token form: bytes; 32 caches of up to 4100 keys, 4 kv heads of
+// 128: 257 MB in 48 us, 5.3 TB/s; one cache of 65,540 keys: 134 MB in 31 us,
+// 4.3 TB/s, the join's launch included.
 #include "attn_common.h"
 
 namespace trsc {
@@ -27,7 +43,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // The running maximum need not be the true one: the weights only have to stay
 // representable. A tile is weighed with the maximum so far, and only where its
 // sum leaves [0, kMostSum) is the maximum taken again, the sums rescaled and the
-// tile weighed anew. (fp16 holds weights up to 65504.)
+// tile weighed anew. (fp16 holds weights up to 65504.) With the maximum of every
+// tile taken the two bf16 sizes above took 1.24 ms and 622 us.
 constexpr float kMostSum = 16384.f;
 
 // The scores of 32 keys j0 + 8 g + 4 (lane / 32) + i: hidden ones become -inf.
@@ -266,6 +283,7 @@ template <class E, int NB, bool TOKEN>
 struct FwdShape {
   typedef Tile<E, NB> T;
   // fp32 products are sixteen times the half types' time: smaller tiles waste less of them at the window's edges
+  // (the fp32 size above: 85 us with tiles of 64 keys, 60 with 32)
   static constexpr int kKeys = TOKEN || sizeof(E) == 4 ? 32 : 64;
   static constexpr int kTileBytes = kKeys * T::kPitch;
   // token form: every wave has its own tiles
@@ -276,11 +294,14 @@ struct FwdShape {
 };
 
 template <class E, int NB, bool TOKEN>
-__global__ __launch_bounds__(256, sizeof(E) == 4 && NB == 4 ? 1 : sizeof(E) == 2 && NB <= 2 && !TOKEN ? 4 : 2) void attn_fwd(AttnArgs a, int tiles, int splits) {
+__global__ __launch_bounds__(256, sizeof(E) == 4 && NB == 4                ? 1
+                                  : sizeof(E) == 2 && NB <= 2 && !TOKEN ? 4
+                                                                        : 2) void attn_fwd(AttnArgs a, int tiles,
+                                                                                           int splits) {
   typedef FwdShape<E, NB, TOKEN> F;
   typedef Tile<E, NB> T;
-  // 32-key blocks whose scores are held at once: heads of 64 and less do best with four waves a SIMD and
-  // one block (four objects of 74 k tokens x 16: 426 us, with two blocks 455), wider ones with two (27 us of 1010 less)
+  // 32-key blocks whose scores are held at once. Heads of 64 and less: one block, and four waves a SIMD (the size
+  // above 426 us, with two blocks and fewer waves 455). Wider heads: two blocks (1.00 ms, with one 1.03).
   constexpr int KB = NB <= 2 ? 1 : F::kKeys / 32;
   __shared__ __attribute__((aligned(1024))) unsigned char s_mem[F::kLds];
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
@@ -543,7 +564,9 @@ hipError_t launch_type(const AttnArgs& a, const AttnPlan& plan, hipStream_t st) 
                   : launch_shape<E, 4, false>(a, plan, st);
   if (e != hipSuccess || plan.splits == 1) return e;
   const int64_t rows = int64_t(a.hq) * a.nq;
-  if (plan.splits > 8)  // 128 splits of 16 rows: 53 us with a wave a row
+  // many splits of few rows (one cache: 128 of 16 rows): four waves a row, the call 31 us for 33; few splits of many
+  // rows (the fp32 size: 4 of 17 k): one, 57 us for 68
+  if (plan.splits > 8)
     attn_join<E, 4><<<unsigned(rows), 256, 0, st>>>(a, plan.splits);
   else
     attn_join<E, 1><<<unsigned((rows + 3) / 4), 256, 0, st>>>(a, plan.splits);
@@ -565,7 +588,8 @@ AttnPlan plan_attention(const AttnArgs& a) {
   const int64_t span = reach < a.nk ? reach : a.nk;
   const int64_t per = p.token_form ? 4 : 1;  // tiles that a workgroup takes at once
   const int64_t key_rounds = (span + keys * per - 1) / (keys * per);
-  // workgroups that the chip holds at once (by LDS: one a CU in the token form of wide heads, else two)
+  // workgroups that the chip holds at once (by LDS: one a CU in the token form of wide heads, else two). Twice that
+  // in the token form: 53 us for 48 and 37 for 31; half or more than that of the others was no faster.
   const int64_t want = p.token_form && (a.dim > 64 || a.dtype == TR_SC_F32) ? 256 : 512;
   int64_t s = (want + tiles - 1) / tiles;
   if (s > key_rounds / 2) s = key_rounds / 2;  // at least two rounds each
