@@ -592,7 +592,11 @@ AttnPlan plan_attention(const AttnArgs& a) {
   // in the token form: 53 us for 48 and 37 for 31; half or more than that of the others was no faster.
   const int64_t want = p.token_form && (a.dim > 64 || a.dtype == TR_SC_F32) ? 256 : 512;
   int64_t s = (want + tiles - 1) / tiles;
-  if (s > key_rounds / 2) s = key_rounds / 2;  // at least two rounds each
+  // Rounds that a split has at least. The join and its launch are worth 5 us: eight rounds (512 keys) of the half
+  // types (450 tokens, 8 heads of 64, 64 keys either way: 17.4 us in two splits, 13.5 in one; all 450 keys: 17.3 and
+  // 13.3), two of fp32 (700 tokens, 6 heads of 80: 21 us for 36) or of a workgroup whose waves take four tiles.
+  const int64_t least = p.token_form || a.dtype == TR_SC_F32 ? 2 : 8;
+  if (s > key_rounds / least) s = key_rounds / least;
   if (s > 256) s = 256;
   if (s > 1) p.splits = int(s);
   if (p.splits > 1) p.part_floats = size_t(p.splits) * a.hq * a.nq * (a.dim + 1);

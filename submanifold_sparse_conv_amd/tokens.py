@@ -19,6 +19,7 @@ from ._lib import Heads, Rotation, Window, check
 
 _DTYPES = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16, torch.float16: _lib.F16}
 _byref = ctypes.byref
+_Pairs = ctypes.c_int * 3
 
 
 def _heads(t, name: str, tokens=None, heads=None, dim=None, like: torch.Tensor | None = None) -> Heads:
@@ -111,21 +112,21 @@ def _rotation(pos, freqs, sections, interleaved, tokens, dim, device) -> Rotatio
         raise ValueError(f"pos must be an int32 tensor on {device}")
     if pos.dim() == 1:
         pos = pos[:, None]
-    if pos.dim() != 2 or pos.shape[0] != tokens or not 1 <= pos.shape[1] <= 3:
-        raise ValueError(f"pos must be [{tokens}, 1 .. 3 axes], got {tuple(pos.shape)}")
-    axes = pos.shape[1]
+    shape = pos.shape
+    if len(shape) != 2 or shape[0] != tokens or not 1 <= shape[1] <= 3:
+        raise ValueError(f"pos must be [{tokens}, 1 .. 3 axes], got {tuple(shape)}")
+    axes = shape[1]
     if axes > 1 and pos.stride(1) != 1:
         raise ValueError("the axes of a position must be adjacent")
     if not isinstance(freqs, torch.Tensor) or freqs.device != device or freqs.dtype != torch.float32 \
-            or tuple(freqs.shape) != (dim // 2,) or not freqs.is_contiguous():
+            or freqs.shape != (dim // 2,) or not freqs.is_contiguous():
         raise ValueError(f"freqs must be fp32 [{dim // 2}] on {device}")
     if sections is None:
         sections = [dim // 2 // axes] * axes
     if len(sections) != axes:
         raise ValueError(f"{axes} axes need {axes} sections, got {list(sections)}")
-    pairs = (ctypes.c_int * 3)(*sections)
     return Rotation(pos.data_ptr() if tokens else None, pos.stride(0) if tokens > 1 else 0, freqs.data_ptr(), axes,
-                    pairs, bool(interleaved))
+                    _Pairs(*sections), bool(interleaved))
 
 
 def _gain(g, name: str, heads: int, dim: int, device):
@@ -134,9 +135,9 @@ def _gain(g, name: str, heads: int, dim: int, device):
         return None, 1
     if not isinstance(g, torch.Tensor) or g.device != device or g.dtype != torch.float32 or not g.is_contiguous():
         raise ValueError(f"{name} must be a contiguous fp32 tensor on {device}")
-    if tuple(g.shape) == (dim,):
+    if g.shape == (dim,):
         return g.data_ptr(), 1
-    if tuple(g.shape) == (heads, dim):
+    if g.shape == (heads, dim):
         return g.data_ptr(), heads
     raise ValueError(f"{name} must be [{dim}] or [{heads}, {dim}], got {tuple(g.shape)}")
 
