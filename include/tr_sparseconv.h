@@ -442,9 +442,11 @@ int tr_sparseconv_window_attention(const tr_sc_heads* q, const tr_sc_heads* k, c
                                    int64_t tokens_q, int64_t tokens_k, int dim, int dtype,
                                    void* workspace, size_t ws_bytes, void* stream);
 
-/* Its gradients: dout as out; out and lse from the forward; dq [tokens_q, q heads,
+/* Its gradients: dout as out; out and lse from the forward of the same tensors
+ * and window (that a row's weights sum to one is used); dq [tokens_q, q heads,
  * dim], dk, dv [tokens_k, kv heads, dim] of type dtype, contiguous. Keys past
- * k_len get zeros. No atomics: the same bits on every call. */
+ * k_len get zeros. The weights and the scores' gradients are rounded to dtype
+ * before their products; sums are fp32. No atomics: the same bits on every call. */
 size_t tr_sparseconv_window_attention_backward_workspace_bytes(const tr_sc_window* window,
                                                                int64_t tokens_q, int64_t tokens_k,
                                                                int q_heads, int kv_heads, int dim,

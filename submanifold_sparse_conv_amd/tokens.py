@@ -249,7 +249,7 @@ def window_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tens
                               right: int = -1, sinks: int = 0, scale: float | None = None, workspace=None):
     """(dq, dk, dv) of L = sum <out, dout> of window_attention with the same
     further arguments (tr_sparseconv_window_attention_backward); out and lse are
-    the forward's."""
+    the forward's on these tensors."""
     dt = _dtype(q, "q")
     hq = _heads(q, "q")
     n, _, dim = q.shape

@@ -508,3 +508,11 @@ def test_attention_gradient_of_short_windows_keeps_its_precision(dtype, dim):
         once = (b.to(TD[dtype]).double() - b).norm()
         err = (a.cpu().double() - b).norm()
         assert err < math.sqrt(2) * 7 / 6 * once, (name, float(err / once))
+
+
+@pytest.mark.parametrize("dtype,dim", [("bf16", 64), ("f16", 40), ("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("lens,hk,group,left,right,sinks", [
+    ([1100], 1, 3, -1, 0, 0), ([700, 333], 1, 5, 600, 600, 40), ([2050], 1, 1, 1200, -1, 3)])
+def test_attention_long_walks(dtype, dim, lens, hk, group, left, right, sinks):
+    """Few tiles with long walks: split over the keys in the forward, over the rows in the gradient of keys and values."""
+    run_case(lens, lens, hk, group, dim, dtype, left, right, sinks)
