@@ -31,8 +31,9 @@
 // products. fp32, 2,877 tokens in four sequences, 6 heads of 80 over 2, 255 either
 // way: 57 us, four splits a row tile to reach the chip, the products' padding (80
 // of 96) and the join. Token form: bytes; 32 caches of up to 4100 keys, 4 kv heads of
-// 128: 257 MB in 48 us, 5.3 TB/s; one cache of 65,540 keys: 134 MB in 31 us,
-// 4.3 TB/s, the join's launch included.
+// 128: 257 MB in 58 us, 4.4 TB/s; one cache of 65,540 keys: 134 MB in 36 us,
+// 3.8 TB/s, the join's launch (5 us) included; 48 and 31 us where the last call
+// has left part of them in the caches.
 #include "attn_common.h"
 
 namespace trsc {
@@ -589,7 +590,7 @@ AttnPlan plan_attention(const AttnArgs& a) {
   const int64_t per = p.token_form ? 4 : 1;  // tiles that a workgroup takes at once
   const int64_t key_rounds = (span + keys * per - 1) / (keys * per);
   // workgroups that the chip holds at once (by LDS: one a CU in the token form of wide heads, else two). Twice that
-  // in the token form: 53 us for 48 and 37 for 31; half or more than that of the others was no faster.
+  // in the token form: 62 us for 60 and 43 for 37; half or more than that of the others was no faster.
   const int64_t want = p.token_form && (a.dim > 64 || a.dtype == TR_SC_F32) ? 256 : 512;
   int64_t s = (want + tiles - 1) / tiles;
   // Rounds that a split has at least. The join and its launch are worth 5 us: eight rounds (512 keys) of the half

@@ -26,9 +26,10 @@
 //
 // What bounds it: memory, each element read and written once (backward: two
 // read). bf16, 73,881 tokens x 32 heads of 64: 605 MB in 122 us, 4.96 TB/s, the
-// rate of a large copy (5.03 TB/s). fp32, 16,219 x 16 heads of 72: 149 MB in
-// 26.6 us (in part from the caches). Backward, bf16, 15,800 x 24 heads of 128:
-// 291 MB in 58 us with the gains' sums, 5.0 TB/s. 32 tokens: 4.3 us, one launch.
+// rate of a large copy (5.03 TB/s). fp32, 16,219 x 16 heads of 72: 150 MB in
+// 29.8 us, 5.0 TB/s. Backward, bf16, 15,800 x 24 heads of 128: 291 MB in 63 us
+// with the gains' sums, 4.6 TB/s; vector instructions are busy for most of it.
+// 32 tokens: 4.3 us, one launch.
 #include "common.h"
 #include "token_types.h"
 #include "tokens.h"
