@@ -289,7 +289,7 @@ int group_lanes(int dim) {
 // Workgroups over the tokens: `fill` in all, fewer where a wave would have no
 // token, and evened out so that every wave walks as many. Forward: four a CU
 // (eight fit; 132 us for 122 with them at the first size above). Backward: the
-// five a CU that fit (three: 62 us for 58).
+// five a CU that fit (three: 59 us for 52 at 15,800 x 24 heads of 72).
 constexpr int kForwardFill = 1024, kBackwardFill = 1280;
 int token_blocks(int64_t tokens, int head_blocks, int fill) {
   const int64_t n = fill / head_blocks > 1 ? fill / head_blocks : 1;
