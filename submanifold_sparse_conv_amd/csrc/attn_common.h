@@ -26,12 +26,12 @@ __device__ __forceinline__ V read_lds(const void* __restrict p) { return *static
 __device__ __forceinline__ s16x4 read_tr(lds_s16x4* __restrict p) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p); }
 
 template <class E>
-struct AttnType;
+struct AttnType;  // wide: products in fp32; narrow: the type's exponents do not reach what fp32 sums hold
 template <>
 struct AttnType<__bf16> {
   typedef __bf16 elt;
   typedef __bf16 frag __attribute__((ext_vector_type(8)));
-  static constexpr bool wide = false;
+  static constexpr bool wide = false, narrow = false;
   static __device__ __forceinline__ f32x16 mma(frag a, frag b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
@@ -40,7 +40,7 @@ template <>
 struct AttnType<_Float16> {
   typedef _Float16 elt;
   typedef _Float16 frag __attribute__((ext_vector_type(8)));
-  static constexpr bool wide = false;
+  static constexpr bool wide = false, narrow = true;
   static __device__ __forceinline__ f32x16 mma(frag a, frag b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
@@ -49,7 +49,7 @@ template <>
 struct AttnType<float> {
   typedef float elt;
   typedef float frag __attribute__((ext_vector_type(8)));
-  static constexpr bool wide = true;
+  static constexpr bool wide = true, narrow = false;
   static __device__ __forceinline__ f32x16 mma(frag a, frag b, f32x16 c) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);

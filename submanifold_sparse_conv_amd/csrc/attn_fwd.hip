@@ -22,6 +22,7 @@
 // rounded to the tensors' type for the product with V (the matrix units take
 // half types; for fp32 tensors nothing is rounded), their sum takes them
 // unrounded: the result is off by that rounding's average and its own last one.
+// fp16's range is kept by a base that moves with the tiles (kMostSum16).
 //
 // What bounds it. bf16, 32,768 tokens, 16 query and 4 kv heads of 128, 4096 keys
 // back: 1.03 TFLOP in 1.00 ms, 1.03 PFLOP/s, of 1.19 that a large library product
@@ -47,6 +48,15 @@ constexpr float kLog2e = 1.4426950408889634f;
 // tile weighed anew. (fp16 holds weights up to 65504.) With the maximum of every
 // tile taken the two bf16 sizes above took 1.24 ms and 622 us.
 constexpr float kMostSum = 16384.f;
+// fp16 holds weights from 2^-14 (its smallest normal) to 65504, so the base moves down as well: where a lane's sum
+// of up to 32 keys falls below kLeastSum16 (a leading key before them, a sink say), the tile's own largest weight
+// becomes 2^kBase16 and the sums grow instead, which fp32 has room for. So the weights of every tile keep the type's
+// precision among themselves, and a row gets a share of 2^-30 as exactly as a large one. (With the base fixed by
+// the leading key, keys 16 nats below it had 2 to 4 bits left.) Right after, a tile's sum is 2^6 to 2^11: it may
+// rise by 4 powers of two and more, or fall by 15, before the base moves again, so scores that spread by a few nats
+// seldom move it. In a tile that itself spreads further the largest weight goes up to 2^kTop16: keys up to 20 nats
+// under it stay normal. No growing past sums of kMostL: what could still come is below 2^-64 of what was.
+constexpr float kMostSum16 = 49152.f, kLeastSum16 = 1.f / 512.f, kBase16 = 6.f, kTop16 = 15.f, kMostL = 1.8446744e19f;
 
 // The scores of 32 keys j0 + 8 g + 4 (lane / 32) + i: hidden ones become -inf.
 __device__ __forceinline__ void hide(f32x16& s, int j0, int lo, int hi, int sinks, int lane) {
@@ -120,6 +130,7 @@ struct RowState {
   typedef AttnType<E> A;
   typedef typename A::frag frag;
   static constexpr int ST = NB * 2, kAhead = A::wide ? 1 : 4;
+  static constexpr bool kNarrow = A::narrow;
   frag qf[ST];     // the queries
   f32x16 acc[NB];  // O^T
   float mc, l;     // scaled maximum (base 2) and sum of the weights
@@ -163,16 +174,38 @@ struct RowState {
         }
     return sum[0] + sum[1];
   }
+  // whether the tile's weights are in range (a row that sees none of it has the sum 0)
+  static __device__ __forceinline__ bool in_range(float sum) {
+    if constexpr (kNarrow) return sum < kMostSum16 && (sum >= kLeastSum16 || sum == 0.f);
+    return sum < kMostSum;
+  }
   __device__ __forceinline__ void weigh(float c) {
     float sum = weigh_by(c, mc);
-    if (__any(!(sum < kMostSum))) {  // also where the row has seen nothing before (mc = -inf)
+    if (__any(!in_range(sum))) {  // also where the row has seen nothing before (mc = -inf)
       float mx = -INFINITY;
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[kb][e]);
       const float2 mh = both_halves(mx);
-      mx = fmaxf(fmaxf(mh.x, mh.y) * c, mc);
+      mx = fmaxf(mh.x, mh.y) * c;
+      if constexpr (kNarrow) {
+        float mn = INFINITY;  // of the scores that the row sees
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) mn = fminf(mn, s[kb][e] == -INFINITY ? INFINITY : s[kb][e]);
+        const float2 nh = both_halves(mn), lh = both_halves(l);
+        const float to = mx - fminf(fmaxf(mx - fminf(nh.x, nh.y) * c - 14.f, kBase16), kTop16);
+        if (mx == -INFINITY)
+          mx = mc;
+        else if (to < mc)  // down, at most 30 a tile: l stays under 2^95
+          mx = lh.x + lh.y < kMostL ? fmaxf(to, mc - 30.f) : mc;
+        else
+          mx = to;
+      } else {
+        mx = fmaxf(mx, mc);
+      }
       const float f = mx == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mc - mx);
       l *= f;
 #pragma unroll
