@@ -48,6 +48,14 @@ constexpr int kRowTile = 32;      // rows of a tile of the dk, dv kernel
 constexpr int kSinkChunk = 512;   // rows of a sink workgroup (256, 1024: 2 % either way, the sizes differing)
 constexpr int kWantWgs = 512;     // workgroups that fill the chip: two on each of 256 CUs
 
+// Powers of two that a weight of the dk, dv kernel is raised by before it is rounded: weights reach 1, so fp16 would
+// have 14 powers of two for them and holds 29 this way (without, dv of keys 15 nats and more below a row's leading
+// one were off by their own size). Taken off with the sums' last factor; the rows' stored lse has it.
+template <class A>
+constexpr float kWeightShift = A::narrow ? 15.f : 0.f;
+template <class A>
+constexpr float kWeightBack = A::narrow ? 1.f / 32768.f : 1.f;
+
 template <class E, int NB>
 __device__ __forceinline__ void store_rows(E* p, const f32x16 (&acc)[NB], float f, int dim, int h) {
   typedef E out4 __attribute__((ext_vector_type(4)));
@@ -112,7 +120,7 @@ __device__ void careful_dkv(const AttnArgs& a, const Seq& q, int r0, int r1, int
     const float2 g = pair_of(static_cast<const E*>(a.dout.p) + q_at * a.dout.ts + head * a.dout.hs, a.dim, lane);
     const float s = wave_sum(x.x * y.x + x.y * y.y), dp = wave_sum(g.x * v.x + g.y * v.y);
     const float2 st = a.stat[(int64_t(kvh) * a.nq + q.q0) * group + r];
-    const float p = __builtin_amdgcn_exp2f(fmaf(s, c, -st.x));
+    const float p = __builtin_amdgcn_exp2f(fmaf(s, c, -st.x)) * kWeightBack<AttnType<E>>;
     const float ds = p * (dp - st.y) * a.scale;
     dv.x += p * g.x;
     dv.y += p * g.y;
@@ -278,7 +286,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
       for (int e = 0; e < 16; ++e) acc[d][e] = fmaf(-off, mean[d][e], acc[d][e]);
   }
   delta = half.x + half.y;
-  if (on && h == 0) a.stat[(int64_t(kvh) * a.nq + q.q0) * group + row] = make_float2(lse2, delta);
+  if (on && h == 0)
+    a.stat[(int64_t(kvh) * a.nq + q.q0) * group + row] = make_float2(lse2 - kWeightShift<A>, delta);
   const uint32_t bad = bad_rows(on ? zero_if_finite<NB>(acc) : 0.f);
   if (on && !((bad >> l32) & 1u))
     store_rows<E, NB>(static_cast<E*>(a.dq) + (q_at * a.hq + head) * a.dim, acc, a.scale, a.dim, h);
@@ -296,7 +305,7 @@ __device__ __forceinline__ int token_at(int64_t t, int lq) { return t < 0 ? 0 : 
 // What a tile's rows need besides their elements.
 template <int ROWS>
 struct alignas(16) RowStats {
-  float2 stat[ROWS];  // base-2 lse (0 for a row that sees nothing) and delta
+  float2 stat[ROWS];  // base-2 lse (0 for a row that sees nothing) less the weights' shift, and delta
   int pos[ROWS];      // position, or far below every window for a row that is not there
 };
 constexpr int kNoRow = -(1 << 30);  // kNoRow + right < 0, and kNoRow - left does not wrap
@@ -393,6 +402,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
 #pragma unroll
     for (int e = 0; e < 16; ++e) dk[d][e] = dv[d][e] = 0.f;
   const float c = a.scale * kLog2e;
+  const float ds_factor = kWeightBack<A>;
   const int n_tiles = r_end > r_begin ? (r_end - r_begin + kRows - 1) / kRows : 0;
   const E* qbase = static_cast<const E*>(a.q.p) + int64_t(q.q0) * a.q.ts + int64_t(kvh) * group * a.q.hs;
   const E* dbase = static_cast<const E*>(a.dout.p) + int64_t(q.q0) * a.dout.ts + int64_t(kvh) * group * a.dout.hs;
@@ -510,6 +520,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
           const int e = 4 * g + i;
           s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lv[i]));
           dp[e] = s[e] * (dp[e] - ev[i]);
+          if constexpr (A::narrow) dp[e] *= ds_factor;
         }
       }
       pack();
@@ -526,8 +537,10 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
           const int from = key < a.sinks ? 0 : pv[i] - a.left, to = key_on ? pv[i] + a.right : -1;
           const bool sees = (key <= to) & (key >= from);
           const float pr = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lv[i]));
+          float d = pr * (dp[e] - ev[i]);
+          if constexpr (A::narrow) d *= ds_factor;
           s[e] = sees ? pr : 0.f;
-          dp[e] = sees ? pr * (dp[e] - ev[i]) : 0.f;
+          dp[e] = sees ? d : 0.f;
         }
       }
       pack();
@@ -579,11 +592,11 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
     if (key < cap && !((bad >> l32) & 1u)) {
       if (float* dst = slot(key)) {
         store_rows<float, NB>(dst, dk, a.scale, a.dim, h);
-        store_rows<float, NB>(dst + a.dim, dv, 1.f, a.dim, h);
+        store_rows<float, NB>(dst + a.dim, dv, kWeightBack<A>, a.dim, h);
       } else {
         const int64_t at = (int64_t(q.k0 + key) * a.hk + kvh) * a.dim;
         store_rows<E, NB>(static_cast<E*>(a.dk) + at, dk, a.scale, a.dim, h);
-        store_rows<E, NB>(static_cast<E*>(a.dv) + at, dv, 1.f, a.dim, h);
+        store_rows<E, NB>(static_cast<E*>(a.dv) + at, dv, kWeightBack<A>, a.dim, h);
       }
     }
   } else {
@@ -634,7 +647,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
       if (key < a.sinks && !((bad >> l32) & 1u)) {
         float* dst = slot + int64_t(key) * 2 * a.dim;
         store_rows<float, NB>(dst, dk, a.scale, a.dim, h);
-        store_rows<float, NB>(dst + a.dim, dv, 1.f, a.dim, h);
+        store_rows<float, NB>(dst + a.dim, dv, kWeightBack<A>, a.dim, h);
       }
     }
   }

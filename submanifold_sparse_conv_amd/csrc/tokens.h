@@ -57,7 +57,7 @@ struct AttnArgs {
   HeadsRef q, k, v, o, dout;  // o: output of the forward, input of the backward
   void *dq, *dk, *dv;         // contiguous [tokens, heads, dim]
   float* lse;                 // [q_heads, tokens_q]
-  float2* stat;               // backward workspace: (base-2 lse, delta) of row r = token, head of the group of
+  float2* stat;               // backward workspace: (shifted base-2 lse, delta) of row r = token, head of the group of
                               // each kv head, [kv_heads, tokens_q * group]
   float* part;                // forward splits: partial outputs, then their statistics
   float* sink_part;           // backward workspace: the sinks' partial gradients

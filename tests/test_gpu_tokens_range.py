@@ -76,3 +76,24 @@ def test_attention_scores_that_fall_and_rise():
     r = R.attention(q[:, 0], k[:, 0], v[:, 0], torch.ones(300, n, dtype=torch.bool), dim ** -0.5)
     check(out[:, 0], r["out"], r["out_tol"], "out")
     check(lse[0], r["lse"], r["lse_tol"], "lse")
+
+
+# ---------------------------------------------------------------------------
+# Gradients
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lead", [12.0, 15.0, 18.0])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_gradient_of_values_beside_a_leading_key(dtype, lead, dim):
+    """dv of the keys that a leading one leaves small weights: their sums over 1000 rows of a large dout, within
+    the roundings of those weights."""
+    n = 1000
+    say("[leading key, dv]", dtype, lead, dim)
+    q, k, v = led(n, n, 1, dim, dtype, lead, 16)
+    dout = randn(gen(17), n, 1, dim, dtype=TD[dtype], scale=1000.0)
+    on = [x.to(DEV) for x in (q, k, v, dout)]
+    out, lse = sc.window_attention(*on[:3], return_lse=True)
+    dv = sc.window_attention_backward(on[3], *on[:3], out, lse)[2]
+    r = R.attention(q[:, 0], k[:, 0], v[:, 0], torch.ones(n, n, dtype=torch.bool), dim ** -0.5, dout[:, 0])
+    past = r["dv"].abs() >= torch.finfo(TD[dtype]).max * (1 + R.U[TD[dtype]] / 2)  # of the leading key: infinite
+    check(dv[:, 0], torch.where(past, r["dv"].sign() * math.inf, r["dv"]), r["dv_tol"], "dv")
