@@ -17,7 +17,8 @@
 // as dV^T += dO^T P and dK^T += Q^T dS take them.
 //
 // Precision. The weights and dS are rounded to the tensors' type for the
-// products; either costs a sum about as much as its own last rounding does. The
+// products (fp16: raised into its range first, whatever the size of dout and of
+// the weights); either costs a sum about as much as its own last rounding does. The
 // given o is rounded too, which would shift all dS of a row by the same share
 // of P: sum_j P_ij dP_ij, exact where o is not, comes with the walk over the
 // keys, so the dk, dv kernel takes that for delta, and dq is mended by a
@@ -55,6 +56,20 @@ template <class A>
 constexpr float kWeightShift = A::narrow ? 15.f : 0.f;
 template <class A>
 constexpr float kWeightBack = A::narrow ? 1.f / 32768.f : 1.f;
+
+// The score gradients dS = P (dP - delta) are as large as dout is and as small as P: fp16 would hold them for a dout
+// of about one and windows of about a thousand keys (with dout of 1e-4, or a leading key, dq and dk were 3 to 6 times
+// as far off as one rounding). So they are raised by a power of two before they are rounded. In dq it is each row's
+// own: one that makes |dout|, as a vector, about 2^kScoreShift. That is a guess of dS from half of its factors, so
+// the largest |dS| of a row is kept, and where it left [kLeastScore, kMostScore) the workgroup walks again with what
+// it is now known to be. So it does for rows whose outputs are near or below the type's smallest normal, which give no
+// usable delta, where dS is small enough for that to show (dq of heads past 64 was up to 280 roundings off). In dk it
+// is one for the rows that a workgroup walks, from their largest |dS|, which the dq kernel leaves for it: a row far
+// below the others adds little to the same sums.
+constexpr int kScoreShift = 9, kNoScore = -1000;
+constexpr float kLeastScore = 1.f / 512.f, kMostScore = 32768.f, kDeltaScore = 2.f, kLeastOut = 1.f / 2048.f;
+__device__ __forceinline__ int exponent_of(float v) { return __builtin_amdgcn_frexp_expf(v); }  // 0 if not finite
+__device__ __forceinline__ float power_of_two(int n) { return __builtin_ldexpf(1.f, n); }
 
 template <class E, int NB>
 __device__ __forceinline__ void store_rows(E* p, const f32x16 (&acc)[NB], float f, int dim, int h) {
@@ -171,7 +186,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
   const int pw0 = min(wrow, rows - 1) / group + shift, pw1 = min(wrow + 31, rows - 1) / group + shift;
   const int64_t q_at = q.q0 + tok;
   frag qf[ST], df[ST];
-  float delta = 0.f;
+  float delta = 0.f, squares = 0.f, out_most = 0.f;  // o . do, do . do, largest |o|
   {
     const E* qp = static_cast<const E*>(a.q.p) + q_at * a.q.ts + head * a.q.hs;
     const E* dp = static_cast<const E*>(a.dout.p) + q_at * a.dout.ts + head * a.dout.hs;
@@ -182,27 +197,44 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
       df[s] = row_from<E>(dp, on, s, a.dim, lane);
       const frag of = row_from<E>(op, on, s, a.dim, lane);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) delta = fmaf(float(of[e]), float(df[s][e]), delta);
+      for (int e = 0; e < 8; ++e) {
+        delta = fmaf(float(of[e]), float(df[s][e]), delta);
+        if constexpr (A::narrow) {
+          squares = fmaf(float(df[s][e]), float(df[s][e]), squares);
+          out_most = fmaxf(out_most, fabsf(float(of[e])));
+        }
+      }
     }
   }
   delta += __shfl_xor(delta, 32);
+  int up = 0;  // dS is raised by 2^up
+  bool low_out = false;
+  if constexpr (A::narrow) {
+    up = kScoreShift - (exponent_of(squares + __shfl_xor(squares, 32)) >> 1);
+    low_out = fmaxf(out_most, __shfl_xor(out_most, 32)) < kLeastOut;
+  }
   const float lse = on ? a.lse[int64_t(head) * a.nq + q_at] : 0.f;
   const float lse2 = lse == -INFINITY ? 0.f : lse * kLog2e;
+  // fp16: weights raised by 2^15 where they are rounded too (for the mean), else by 2^up at once
+  float lse_w = A::narrow ? lse2 - (kMean ? 15.f : float(up)) : lse2;
+  float ds_factor = A::narrow && kMean ? power_of_two(up - 15) : 1.f;
   const E* kbase = static_cast<const E*>(a.k.p) + int64_t(q.k0) * a.k.ts + kvh * a.k.hs;
   const E* vbase = static_cast<const E*>(a.v.p) + int64_t(q.k0) * a.v.ts + kvh * a.v.hs;
   const typename T::Lane at = T::lane_of(lane);
-  f32x16 acc[NB];
+  f32x16 acc[NB], mean[kMean ? NB : 1];
+  float sum[2], most;  // sum of P dP; largest |dS| of fp16
+  auto clear = [&]() {
 #pragma unroll
-  for (int d = 0; d < NB; ++d)
+    for (int d = 0; d < NB; ++d)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) acc[d][e] = 0.f;
-  f32x16 mean[kMean ? NB : 1];
+      for (int e = 0; e < 16; ++e) acc[d][e] = 0.f;
 #pragma unroll
-  for (int d = 0; d < (kMean ? NB : 1); ++d)
+    for (int d = 0; d < (kMean ? NB : 1); ++d)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) mean[d][e] = 0.f;
+      for (int e = 0; e < 16; ++e) mean[d][e] = 0.f;
+    sum[0] = sum[1] = most = 0.f;
+  };
   const float c = a.scale * kLog2e;
-  float sum[2] = {0.f, 0.f};  // of P dP
 
   typename T::template Copy<kKeyTile, 4> kc, vc;
   kc.start(a.k.ts, a.dim, wave, lane);
@@ -244,9 +276,11 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const float w = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lse2)), wd = w * dp[e];
+        const float w = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lse_w)), wd = w * dp[e];
         sum[e & 1] += wd;
         s[e] = fmaf(-w, delta, wd);
+        if constexpr (A::narrow && kMean) s[e] *= ds_factor;
+        if constexpr (A::narrow) most = fmaxf(most, fabsf(s[e]));
         if constexpr (kMean) dp[e] = w;
       }
       const frag sf[2] = {pack_frag8<E>(s, 0), pack_frag8<E>(s, 1)};
@@ -268,18 +302,53 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
       }
     }
   };
-  if (kt.n > 0) fetch(0, 0);
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
-  for (int it = 0; it < kt.n; ++it) {
-    if (it + 1 < kt.n) fetch(it + 1, (it & 1) ^ 1);
-    compute(it, it & 1);
+  float2 half;
+  for (int pass = 0;; ++pass) {
+    clear();
+    if (kt.n > 0) fetch(0, 0);
     __builtin_amdgcn_s_waitcnt(0);
-    bare_barrier();
+    __syncthreads();
+    for (int it = 0; it < kt.n; ++it) {
+      if (it + 1 < kt.n) fetch(it + 1, (it & 1) ^ 1);
+      compute(it, it & 1);
+      __builtin_amdgcn_s_waitcnt(0);
+      bare_barrier();
+    }
+    half = both_halves(sum[0] + sum[1]);
+    if constexpr (A::narrow) {
+      const float back = power_of_two(kMean ? -15 : -up);
+      half.x *= back;
+      half.y *= back;
+      most = fmaxf(most, __shfl_xor(most, 32));
+      if (pass > 0) break;
+      const bool redo = on && most > 0.f && most < INFINITY &&
+                        (most >= kMostScore || most < kLeastScore || (low_out && most < kDeltaScore));
+      // the whole workgroup walks again, or none of it (all reads of the tiles are done)
+      uint32_t* flags = reinterpret_cast<uint32_t*>(s_mem);
+      const bool mine = __any(redo);
+      if (lane == 0) flags[wave] = mine;
+      __syncthreads();
+      const uint32_t again = flags[0] | flags[1] | flags[2] | flags[3];
+      __syncthreads();
+      if (again == 0) break;
+      if (redo) {
+        up = min(up + 13 - exponent_of(most), 100);
+        lse_w = lse2 - (kMean ? 15.f : float(up));
+        ds_factor = kMean ? power_of_two(up - 15) : 1.f;
+        delta = half.x + half.y;
+      }
+    } else {
+      break;
+    }
   }
-  const float2 half = both_halves(sum[0] + sum[1]);
+  if constexpr (A::narrow) {
+    int largest = on && most > 0.f ? exponent_of(most) - up : kNoScore;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) largest = max(largest, __shfl_xor(largest, o));
+    if (wave_on && lane == 0) a.score_exp[(int64_t(kvh) * tiles + tile) * 4 + wave] = largest;
+  }
   if constexpr (kMean) {
-    const float off = half.x + half.y - delta;
+    const float off = (half.x + half.y - delta) * ds_factor;  // as acc and mean are raised
 #pragma unroll
     for (int d = 0; d < NB; ++d)
 #pragma unroll
@@ -290,7 +359,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
     a.stat[(int64_t(kvh) * a.nq + q.q0) * group + row] = make_float2(lse2 - kWeightShift<A>, delta);
   const uint32_t bad = bad_rows(on ? zero_if_finite<NB>(acc) : 0.f);
   if (on && !((bad >> l32) & 1u))
-    store_rows<E, NB>(static_cast<E*>(a.dq) + (q_at * a.hq + head) * a.dim, acc, a.scale, a.dim, h);
+    store_rows<E, NB>(static_cast<E*>(a.dq) + (q_at * a.hq + head) * a.dim, acc,
+                      A::narrow ? __builtin_ldexpf(a.scale, -up) : a.scale, a.dim, h);
   if (bad != 0) {
     for (int i = 0; i < 32; ++i) {
       if (!((bad >> i) & 1u)) continue;
@@ -402,7 +472,22 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
 #pragma unroll
     for (int e = 0; e < 16; ++e) dk[d][e] = dv[d][e] = 0.f;
   const float c = a.scale * kLog2e;
-  const float ds_factor = kWeightBack<A>;
+  int up = 0;  // dS is raised by 2^up, 2^15 of them by its weight
+  if constexpr (A::narrow) {
+    if (r_end > r_begin) {
+      const int dq_tiles = int(int64_t(a.nq) * group / kRowsWg) + a.batch;  // as launched
+      const int first = (a.cu_q ? first_tile(a.cu_q, b, group, kRowsWg) : 0) * 4;
+      const int32_t* exponents = a.score_exp + int64_t(kvh) * dq_tiles * 4;
+      int largest = kNoScore;
+      for (int i = r_begin / 32 + lane; i <= (r_end - 1) / 32; i += 64)
+        largest = max(largest, exponents[clamp_to(first + i, 0, dq_tiles * 4 - 1)]);
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) largest = max(largest, __shfl_xor(largest, o));
+      up = clamp_to(14 - __builtin_amdgcn_readfirstlane(largest), -60, 100);
+    }
+  }
+  const float ds_factor = power_of_two(up - 15);
+  const float dk_factor = A::narrow ? __builtin_ldexpf(a.scale, -up) : a.scale;
   const int n_tiles = r_end > r_begin ? (r_end - r_begin + kRows - 1) / kRows : 0;
   const E* qbase = static_cast<const E*>(a.q.p) + int64_t(q.q0) * a.q.ts + int64_t(kvh) * group * a.q.hs;
   const E* dbase = static_cast<const E*>(a.dout.p) + int64_t(q.q0) * a.dout.ts + int64_t(kvh) * group * a.dout.hs;
@@ -591,11 +676,11 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
     }
     if (key < cap && !((bad >> l32) & 1u)) {
       if (float* dst = slot(key)) {
-        store_rows<float, NB>(dst, dk, a.scale, a.dim, h);
+        store_rows<float, NB>(dst, dk, dk_factor, a.dim, h);
         store_rows<float, NB>(dst + a.dim, dv, kWeightBack<A>, a.dim, h);
       } else {
         const int64_t at = (int64_t(q.k0 + key) * a.hk + kvh) * a.dim;
-        store_rows<E, NB>(static_cast<E*>(a.dk) + at, dk, a.scale, a.dim, h);
+        store_rows<E, NB>(static_cast<E*>(a.dk) + at, dk, dk_factor, a.dim, h);
         store_rows<E, NB>(static_cast<E*>(a.dv) + at, dv, kWeightBack<A>, a.dim, h);
       }
     }
@@ -646,7 +731,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
       }
       if (key < a.sinks && !((bad >> l32) & 1u)) {
         float* dst = slot + int64_t(key) * 2 * a.dim;
-        store_rows<float, NB>(dst, dk, a.scale, a.dim, h);
+        store_rows<float, NB>(dst, dk, dk_factor, a.dim, h);
         store_rows<float, NB>(dst + a.dim, dv, kWeightBack<A>, a.dim, h);
       }
     }
@@ -765,6 +850,10 @@ hipError_t launch_type(const AttnArgs& a, hipStream_t st) {
 }  // namespace
 
 size_t attention_backward_stat_floats(const AttnArgs& a) { return size_t(a.hq) * a.nq * 2; }
+
+size_t attention_backward_exponents(const AttnArgs& a) {
+  return a.dtype == TR_SC_F16 ? size_t(tiles_of(a.nq, a.batch, a.hq / a.hk, kRowsWg)) * a.hk * 4 : 0;
+}
 
 size_t attention_backward_sink_floats(const AttnArgs& a) {
   if (a.sinks == 0) return 0;

@@ -59,6 +59,7 @@ struct AttnArgs {
   float* lse;                 // [q_heads, tokens_q]
   float2* stat;               // backward workspace: (shifted base-2 lse, delta) of row r = token, head of the group of
                               // each kv head, [kv_heads, tokens_q * group]
+  int32_t* score_exp;         // backward workspace, fp16: exponent of the largest score gradient of every 32 rows
   float* part;                // forward splits: partial outputs, then their statistics
   float* sink_part;           // backward workspace: the sinks' partial gradients
   float* dkv_part;            // backward workspace: dk, dv of the parts of the row walk
@@ -78,8 +79,10 @@ struct AttnPlan {
 };
 AttnPlan plan_attention(const AttnArgs& a);
 hipError_t launch_attention(const AttnArgs& a, const AttnPlan& plan, hipStream_t st);
-// Workspace of the backward, in floats: the rows' statistics, the sinks' partials, the parts'.
+// Workspace of the backward, in floats (or as many 32-bit integers): the rows' statistics and, of fp16, their score
+// gradients' exponents, the sinks' partials, the parts'.
 size_t attention_backward_stat_floats(const AttnArgs& a);
+size_t attention_backward_exponents(const AttnArgs& a);
 size_t attention_backward_sink_floats(const AttnArgs& a);
 size_t attention_backward_part_floats(const AttnArgs& a);
 hipError_t launch_attention_backward(const AttnArgs& a, hipStream_t st);

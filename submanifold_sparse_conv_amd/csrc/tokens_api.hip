@@ -195,12 +195,13 @@ bool sizes_only(const tr_sc_window* win, int64_t nq, int64_t nk, int q_heads, in
 }
 
 struct BackwardLayout {
-  size_t stat, sinks, parts, total;
+  size_t stat, exps, sinks, parts, total;
 };
 BackwardLayout backward_layout(const AttnArgs& a) {
   BackwardLayout l{};
   l.stat = 0;
-  l.sinks = align_up(attention_backward_stat_floats(a) * 4, 256);
+  l.exps = align_up(attention_backward_stat_floats(a) * 4, 256);
+  l.sinks = l.exps + align_up(attention_backward_exponents(a) * 4, 256);
   l.parts = l.sinks + align_up(attention_backward_sink_floats(a) * 4, 256);
   l.total = l.parts + align_up(attention_backward_part_floats(a) * 4, 256);
   return l;
@@ -326,6 +327,7 @@ int tr_sparseconv_window_attention_backward(const tr_sc_heads* dout, const tr_sc
   a.dk = dk;
   a.dv = dv;
   a.stat = reinterpret_cast<float2*>(static_cast<char*>(workspace) + l.stat);
+  a.score_exp = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + l.exps);
   a.dkv_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.parts);
   a.sink_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.sinks);
   const hipError_t e = launch_attention_backward(a, static_cast<hipStream_t>(stream));
