@@ -88,66 +88,106 @@ __device__ __forceinline__ void store_rows(E* p, const f32x16 (&acc)[NB], float 
     }
 }
 
-// dq of one row by a whole wave, touching only the keys it sees.
-template <class E>
-__device__ void careful_dq(const AttnArgs& a, const Seq& q, const KeyTiles& kt, int tok, int head, int kvh,
-                           float lse2, float delta, int lane) {
-  const int64_t q_at = q.q0 + tok;
-  const int p = tok + q.lk - q.lq;
+// Where a key tile stands to the rows at positions p0 .. p1 (of a wave): seen by any, or by all.
+__device__ __forceinline__ bool any_sees(const AttnArgs& a, int p0, int p1, int j0, int j1, int lk) {
+  return j0 < lk && j0 <= p1 + a.right && (j1 >= p0 - a.left || j0 < a.sinks);
+}
+__device__ __forceinline__ bool all_see(const AttnArgs& a, int p0, int p1, int j0, int j1, int lk) {
+  return j1 <= p0 + a.right && j1 < lk && (j0 >= p1 - a.left || j1 < a.sinks);
+}
+
+// dq (not scaled) of a wave's rows at positions p0 .. p1 again, adding only what each sees (attn_common.h); p: this
+// lane's position; qp, gp: its query and dout. lds: 4 KB of the wave's own.
+template <class E, int NB>
+__device__ void safe_dq(const AttnArgs& a, const Seq& q, const KeyTiles& kt, int p0, int p1, int p, bool on,
+                        const E* qp, const E* gp, int kvh, float lse2, float delta, float* lds, int lane,
+                        f32x16 (&acc)[NB]) {
+  constexpr int ST = NB * 2;
   const float c = a.scale * kLog2e;
-  const float2 x = pair_of(static_cast<const E*>(a.q.p) + q_at * a.q.ts + head * a.q.hs, a.dim, lane);
-  const float2 g = pair_of(static_cast<const E*>(a.dout.p) + q_at * a.dout.ts + head * a.dout.hs, a.dim, lane);
-  float2 o = make_float2(0.f, 0.f);
-  for (int it = 0; it < kt.n; ++it) {
-    for (int j = kt.at(it) * kKeyTile, je = j + kKeyTile; j < je; ++j) {
-      if (!sees_key(a, p, j, q.lk)) continue;
-      const int64_t at = q.k0 + j;
-      const float2 y = pair_of(static_cast<const E*>(a.k.p) + at * a.k.ts + kvh * a.k.hs, a.dim, lane);
-      const float2 v = pair_of(static_cast<const E*>(a.v.p) + at * a.v.ts + kvh * a.v.hs, a.dim, lane);
-      const float s = wave_sum(x.x * y.x + x.y * y.y), dp = wave_sum(g.x * v.x + g.y * v.y);
-      const float ds = __builtin_amdgcn_exp2f(fmaf(s, c, -lse2)) * (dp - delta);
-      o.x += ds * y.x;
-      o.y += ds * y.y;
+  const int lo = p - a.left, hi = min(p + a.right, q.lk - 1);
+  const E* kbase = static_cast<const E*>(a.k.p) + int64_t(q.k0) * a.k.ts + kvh * a.k.hs;
+  const E* vbase = static_cast<const E*>(a.v.p) + int64_t(q.k0) * a.v.ts + kvh * a.v.hs;
+  typename AttnType<E>::frag qf[ST], gf[ST];
+#pragma unroll
+  for (int s = 0; s < ST; ++s) {
+    qf[s] = row_from<E>(qp, on, s, a.dim, lane);
+    gf[s] = row_from<E>(gp, on, s, a.dim, lane);
+  }
+#pragma unroll
+  for (int d = 0; d < NB; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[d][e] = 0.f;
+  for (int it = 0; it < kt.n * (kKeyTile / 32); ++it) {
+    const int j0 = kt.at(it / (kKeyTile / 32)) * kKeyTile + it % (kKeyTile / 32) * 32;
+    if (!any_sees(a, p0, p1, j0, j0 + 31, q.lk)) continue;
+    const int mine = j0 + (lane & 31);
+    f32x16 s = scores_from<E, ST>(kbase + mine * a.k.ts, mine < q.lk, qf, a.dim, lane);
+    const f32x16 dp = scores_from<E, ST>(vbase + mine * a.v.ts, mine < q.lk, gf, a.dim, lane);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lse2)) * (dp[e] - delta);
+    put_factors(lds, s, lane);
+    wave_fence();
+    add_rows<E, NB>(
+        acc, lds, [&](int i) { return kbase + min(j0 + i, q.lk - 1) * a.k.ts; },
+        [&](int i) { return j0 + i <= hi && (j0 + i >= lo || j0 + i < a.sinks); }, 0, a.dim, lane);
+    wave_fence();
+  }
+}
+
+// dk (not scaled) and dv of a wave's 32 keys from jw over the rows [r0, r1) again, adding only rows that see them.
+// key_on: this lane's key is one. lds: 8 KB of the wave's own.
+template <class E, int NB>
+__device__ void safe_dkv(const AttnArgs& a, const Seq& q, int r0, int r1, int jw, bool key_on, int kvh, float* lds,
+                         int lane, f32x16 (&dk)[NB], f32x16 (&dv)[NB]) {
+  constexpr int ST = NB * 2;
+  const int group = a.hq / a.hk, shift = q.lk - q.lq, key = jw + (lane & 31);
+  const float c = a.scale * kLog2e;
+  const int64_t at = q.k0 + (key_on ? key : 0);
+  const E* kp = static_cast<const E*>(a.k.p) + at * a.k.ts + kvh * a.k.hs;
+  const E* vp = static_cast<const E*>(a.v.p) + at * a.v.ts + kvh * a.v.hs;
+  const float2* stat = a.stat + (int64_t(kvh) * a.nq + q.q0) * group;
+  auto q_row = [&](int r) {
+    const int tok = r / group;
+    return static_cast<const E*>(a.q.p) + int64_t(q.q0 + tok) * a.q.ts + (kvh * group + r - tok * group) * a.q.hs;
+  };
+  auto g_row = [&](int r) {
+    const int tok = r / group;
+    return static_cast<const E*>(a.dout.p) + int64_t(q.q0 + tok) * a.dout.ts +
+           (kvh * group + r - tok * group) * a.dout.hs;
+  };
+  typename AttnType<E>::frag kf[ST], vf[ST];
+#pragma unroll
+  for (int s = 0; s < ST; ++s) {
+    kf[s] = row_from<E>(kp, key_on, s, a.dim, lane);
+    vf[s] = row_from<E>(vp, key_on, s, a.dim, lane);
+  }
+#pragma unroll
+  for (int d = 0; d < NB; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) dk[d][e] = dv[d][e] = 0.f;
+  for (int t0 = r0; t0 < r1; t0 += 32) {
+    if (!any_sees(a, t0 / group + shift, min(t0 + 31, r1 - 1) / group + shift, jw, jw + 31, q.lk)) continue;
+    const int mine = min(t0 + (lane & 31), r1 - 1);
+    const bool on = t0 + (lane & 31) < r1;
+    f32x16 s = scores_from<E, ST>(q_row(mine), on, kf, a.dim, lane);
+    f32x16 dp = scores_from<E, ST>(g_row(mine), on, vf, a.dim, lane);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float2 st = stat[min(t0 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3), r1 - 1)];
+      s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -st.x)) * kWeightBack<AttnType<E>>;
+      dp[e] = s[e] * (dp[e] - st.y);
     }
+    put_factors(lds, s, lane);
+    put_factors(lds + 1024, dp, lane);
+    wave_fence();
+    auto sees = [&](int i) {
+      const int p = (t0 + i) / group + shift;
+      return key_on && t0 + i < r1 && key <= p + a.right && (key >= p - a.left || key < a.sinks);
+    };
+    add_rows<E, NB>(dv, lds, [&](int i) { return g_row(min(t0 + i, r1 - 1)); }, sees, 0, a.dim, lane);
+    add_rows<E, NB>(dk, lds + 1024, [&](int i) { return q_row(min(t0 + i, r1 - 1)); }, sees, 0, a.dim, lane);
+    wave_fence();
   }
-  typedef E out2 __attribute__((ext_vector_type(2)));
-  if (2 * lane < a.dim)
-    *reinterpret_cast<out2*>(static_cast<E*>(a.dq) + (q_at * a.hq + head) * a.dim + 2 * lane) =
-        out2{static_cast<E>(o.x * a.scale), static_cast<E>(o.y * a.scale)};
-}
-
-// dk and dv (elements 2 lane, 2 lane + 1) of one key over the rows [r0, r1) by
-// a whole wave, touching only the rows that see it.
-template <class E>
-__device__ void careful_dkv(const AttnArgs& a, const Seq& q, int r0, int r1, int key, int kvh, float2& dk, float2& dv,
-                            int lane) {
-  const int group = a.hq / a.hk;
-  const float c = a.scale * kLog2e;
-  const int64_t at = q.k0 + key;
-  const float2 y = pair_of(static_cast<const E*>(a.k.p) + at * a.k.ts + kvh * a.k.hs, a.dim, lane);
-  const float2 v = pair_of(static_cast<const E*>(a.v.p) + at * a.v.ts + kvh * a.v.hs, a.dim, lane);
-  dk = dv = make_float2(0.f, 0.f);
-  for (int r = r0; r < r1; ++r) {
-    const int tok = r / group, head = kvh * group + r - tok * group;
-    if (!sees_key(a, tok + q.lk - q.lq, key, q.lk)) continue;
-    const int64_t q_at = q.q0 + tok;
-    const float2 x = pair_of(static_cast<const E*>(a.q.p) + q_at * a.q.ts + head * a.q.hs, a.dim, lane);
-    const float2 g = pair_of(static_cast<const E*>(a.dout.p) + q_at * a.dout.ts + head * a.dout.hs, a.dim, lane);
-    const float s = wave_sum(x.x * y.x + x.y * y.y), dp = wave_sum(g.x * v.x + g.y * v.y);
-    const float2 st = a.stat[(int64_t(kvh) * a.nq + q.q0) * group + r];
-    const float p = __builtin_amdgcn_exp2f(fmaf(s, c, -st.x)) * kWeightBack<AttnType<E>>;
-    const float ds = p * (dp - st.y) * a.scale;
-    dv.x += p * g.x;
-    dv.y += p * g.y;
-    dk.x += ds * x.x;
-    dk.y += ds * x.y;
-  }
-}
-
-template <class E>
-__device__ __forceinline__ void store_pair(E* p, float2 v, int dim, int lane) {
-  typedef E out2 __attribute__((ext_vector_type(2)));
-  if (2 * lane < dim) *reinterpret_cast<out2*>(p + 2 * lane) = out2{static_cast<E>(v.x), static_cast<E>(v.y)};
 }
 
 // dq and delta: 128 rows a workgroup, 32 a wave.
@@ -252,8 +292,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
       const int j0 = jt + 32 * kb, j1 = j0 + 31;
-      if (!wave_on || j0 >= q.lk || j0 > pw1 + a.right || (j1 < pw0 - a.left && j0 >= a.sinks)) continue;
-      const bool all = j1 <= pw0 + a.right && j1 < q.lk && (j0 >= pw1 - a.left || j1 < a.sinks);
+      if (!wave_on || !any_sees(a, pw0, pw1, j0, j1, q.lk)) continue;
+      const bool all = all_see(a, pw0, pw1, j0, j1, q.lk);
       f32x16 s, dp;
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[e] = dp[e] = 0.f;
@@ -358,14 +398,14 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
   if (on && h == 0)
     a.stat[(int64_t(kvh) * a.nq + q.q0) * group + row] = make_float2(lse2 - kWeightShift<A>, delta);
   const uint32_t bad = bad_rows(on ? zero_if_finite<NB>(acc) : 0.f);
-  if (on && !((bad >> l32) & 1u))
-    store_rows<E, NB>(static_cast<E*>(a.dq) + (q_at * a.hq + head) * a.dim, acc,
-                      A::narrow ? __builtin_ldexpf(a.scale, -up) : a.scale, a.dim, h);
+  E* const dqp = static_cast<E*>(a.dq) + (q_at * a.hq + head) * a.dim;
+  const bool mine = (bad >> l32) & 1u;
+  if (on && !mine) store_rows<E, NB>(dqp, acc, A::narrow ? __builtin_ldexpf(a.scale, -up) : a.scale, a.dim, h);
   if (bad != 0) {
-    for (int i = 0; i < 32; ++i) {
-      if (!((bad >> i) & 1u)) continue;
-      careful_dq<E>(a, q, kt, __shfl(tok, i), __shfl(head, i), kvh, __shfl(lse2, i), __shfl(delta, i), lane);
-    }
+    safe_dq<E, NB>(a, q, kt, pw0, pw1, p, on, static_cast<const E*>(a.q.p) + q_at * a.q.ts + head * a.q.hs,
+                   static_cast<const E*>(a.dout.p) + q_at * a.dout.ts + head * a.dout.hs, kvh, lse2, delta,
+                   reinterpret_cast<float*>(s_mem) + wave * 1024, lane, acc);
+    if (on && mine) store_rows<E, NB>(dqp, acc, a.scale, a.dim, h);
   }
 }
 
@@ -561,9 +601,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
     const int p1 = (even ? min(p0 + max(tok_step, 1) - 1, (r_end - 1) / group + shift)
                          : min(t0 + kRowTile - 1, r_end - 1) / group + shift);
     const int j1 = jw + 31;
-    if (jw >= q.lk || jw > p1 + a.right || (j1 < p0 - a.left && jw >= a.sinks)) return;
-    const bool all = t0 + kRowTile <= r_end && j1 <= p0 + a.right && j1 < q.lk &&
-                     (jw >= p1 - a.left || j1 < a.sinks);
+    if (!any_sees(a, p0, p1, jw, j1, q.lk)) return;
+    const bool all = t0 + kRowTile <= r_end && all_see(a, p0, p1, jw, j1, q.lk);
     f32x16 s, dp;
 #pragma unroll
     for (int e = 0; e < 16; ++e) s[e] = dp[e] = 0.f;
@@ -661,28 +700,23 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
       if (parts > 1) return a.dkv_part + ((int64_t(part) * a.nk + q.k0 + j) * a.hk + kvh) * 2 * a.dim;
       return nullptr;
     };
-    for (uint32_t left = bad; left != 0; left &= left - 1) {
-      const int j = jw + __builtin_ctz(left);
-      float2 gk, gv;
-      careful_dkv<E>(a, q, r_begin, r_end, j, kvh, gk, gv, lane);
-      if (float* dst = slot(j)) {
-        store_pair<float>(dst, gk, a.dim, lane);
-        store_pair<float>(dst + a.dim, gv, a.dim, lane);
-      } else {
-        const int64_t at = (int64_t(q.k0 + j) * a.hk + kvh) * a.dim;
-        store_pair<E>(static_cast<E*>(a.dk) + at, gk, a.dim, lane);
-        store_pair<E>(static_cast<E*>(a.dv) + at, gv, a.dim, lane);
-      }
-    }
-    if (key < cap && !((bad >> l32) & 1u)) {
+    auto store = [&](bool which, float k_factor, float v_factor) {
+      if (key >= cap || !which) return;
       if (float* dst = slot(key)) {
-        store_rows<float, NB>(dst, dk, dk_factor, a.dim, h);
-        store_rows<float, NB>(dst + a.dim, dv, kWeightBack<A>, a.dim, h);
+        store_rows<float, NB>(dst, dk, k_factor, a.dim, h);
+        store_rows<float, NB>(dst + a.dim, dv, v_factor, a.dim, h);
       } else {
         const int64_t at = (int64_t(q.k0 + key) * a.hk + kvh) * a.dim;
-        store_rows<E, NB>(static_cast<E*>(a.dk) + at, dk, dk_factor, a.dim, h);
-        store_rows<E, NB>(static_cast<E*>(a.dv) + at, dv, kWeightBack<A>, a.dim, h);
+        store_rows<E, NB>(static_cast<E*>(a.dk) + at, dk, k_factor, a.dim, h);
+        store_rows<E, NB>(static_cast<E*>(a.dv) + at, dv, v_factor, a.dim, h);
       }
+    };
+    const bool mine = (bad >> l32) & 1u;
+    store(!mine, dk_factor, kWeightBack<A>);
+    if (bad != 0) {
+      safe_dkv<E, NB>(a, q, r_begin, r_end, jw, key_on, kvh, reinterpret_cast<float*>(s_mem) + wave * 2048, lane, dk,
+                      dv);
+      store(mine, a.scale, 1.f);
     }
   } else {
     __builtin_amdgcn_s_waitcnt(0);
@@ -722,17 +756,17 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
       float* const slot = a.sink_part + (int64_t(a.batch) * parts + tile) * a.hk * a.sinks * 2 * a.dim +
                           int64_t(kvh) * a.sinks * 2 * a.dim;
       const uint32_t bad = bad_rows(key < a.sinks ? zero_if_finite<NB>(dk) + zero_if_finite<NB>(dv) : 0.f);
-      for (uint32_t left = bad; left != 0; left &= left - 1) {
-        const int j = jw + __builtin_ctz(left);
-        float2 gk, gv;
-        careful_dkv<E>(a, q, r_begin, r_end, j, kvh, gk, gv, lane);
-        store_pair<float>(slot + int64_t(j) * 2 * a.dim, gk, a.dim, lane);
-        store_pair<float>(slot + int64_t(j) * 2 * a.dim + a.dim, gv, a.dim, lane);
-      }
-      if (key < a.sinks && !((bad >> l32) & 1u)) {
+      auto store = [&](bool which, float k_factor, float v_factor) {
+        if (key >= a.sinks || !which) return;
         float* dst = slot + int64_t(key) * 2 * a.dim;
-        store_rows<float, NB>(dst, dk, dk_factor, a.dim, h);
-        store_rows<float, NB>(dst + a.dim, dv, kWeightBack<A>, a.dim, h);
+        store_rows<float, NB>(dst, dk, k_factor, a.dim, h);
+        store_rows<float, NB>(dst + a.dim, dv, v_factor, a.dim, h);
+      };
+      const bool mine = (bad >> l32) & 1u;
+      store(!mine, dk_factor, kWeightBack<A>);
+      if (bad != 0) {
+        safe_dkv<E, NB>(a, q, r_begin, r_end, jw, key_on, kvh, red, lane, dk, dv);
+        store(mine, a.scale, 1.f);
       }
     }
   }

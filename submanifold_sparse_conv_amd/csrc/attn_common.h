@@ -302,10 +302,14 @@ __device__ __forceinline__ KeyTiles key_tiles(const AttnArgs& a, int p0, int p1,
 
 // ---------------------------------------------------------------------------
 // Non-finite elements that a row does not see. A weight of zero times such an
-// element is NaN in the matrix products, so a result that is not finite is
-// computed again, one row (or key) at a time by a whole wave that only touches
-// what is seen; lane l has the elements 2 l and 2 l + 1. No cost where all is
-// finite but one check of the result.
+// element is NaN in the products that sum over keys (or rows), so where a
+// result of a wave is not finite, the wave walks again: scores by products from
+// memory, which keep what is not finite to its own key and row, and sums key by
+// key in vector instructions, each lane adding only what it sees. No cost where
+// all is finite but one check of the result. Where something is not, the waves
+// that it reaches take 10 to 30 times their time (32,768 tokens, 16 heads of 128
+// over 4, 4096 keys back, NaN in a sink's value, which all rows see: forward 32
+// ms, gradient 132; a row or key at a time by a whole wave took 500 times).
 // ---------------------------------------------------------------------------
 template <int NB>
 __device__ __forceinline__ float zero_if_finite(const f32x16 (&acc)[NB]) {  // NaN if any element is not finite
@@ -321,17 +325,55 @@ __device__ __forceinline__ uint32_t bad_rows(float t) {
   const uint64_t m = __ballot(t != t);
   return uint32_t(m) | uint32_t(m >> 32);
 }
-__device__ __forceinline__ float wave_sum(float v) {
+// Scores of 32 rows of `a` (this lane's: pa, if on) against the fragments b: rows down, columns across.
+template <class E, int ST>
+__device__ __forceinline__ f32x16 scores_from(const E* pa, bool on, const typename AttnType<E>::frag (&b)[ST], int dim,
+                                              int lane) {
+  f32x16 s;
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  for (int e = 0; e < 16; ++e) s[e] = 0.f;
+#pragma unroll
+  for (int st = 0; st < ST; ++st) s = AttnType<E>::mma(row_from<E>(pa, on, st, dim, lane), b[st], s);
+  return s;
 }
-template <class E>
-__device__ __forceinline__ float2 pair_of(const E* row, int dim, int lane) {
-  return 2 * lane < dim ? make_float2(float(row[2 * lane]), float(row[2 * lane + 1])) : make_float2(0.f, 0.f);
+// 32 x 32 factors to the wave's own LDS, row by row, and one of them back as every row's of this lane's column.
+__device__ __forceinline__ void put_factors(float* lds, const f32x16& s, int lane) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) lds[(8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) * 32 + (lane & 31)] = s[e];
 }
-__device__ __forceinline__ bool sees_key(const AttnArgs& a, int p, int j, int lk) {
-  return j < lk && j <= p + a.right && (j >= p - a.left || j < a.sinks);
+__device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+// acc += factor i * row(i) for the 32 rows i of which sees(i), blocks d0 .. d0 + DN of 32 elements: the factors in
+// LDS as put_factors laid them; row(i) can be read whether seen or not, and the next is on its way meanwhile.
+template <class E, int DN, int NB, class Row, class Sees>
+__device__ __forceinline__ void add_rows(f32x16 (&acc)[NB], const float* lds, const Row& row, const Sees& sees, int d0,
+                                         int dim, int lane) {
+  typedef E elt4 __attribute__((ext_vector_type(4)));
+  elt4 x[2][DN][4];
+  auto load = [&](int i, elt4 (&to)[DN][4]) {
+    const E* from = row(i);
+#pragma unroll
+    for (int d = 0; d < DN; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int col = 32 * (d0 + d) + 8 * g + 4 * (lane >> 5);
+        if (col < dim) to[d][g] = *reinterpret_cast<const elt4*>(from + col);
+      }
+  };
+  load(0, x[0]);
+  for (int i = 0; i < 32; i += 2) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (i + b + 1 < 32) load(i + b + 1, x[b ^ 1]);
+      if (!sees(i + b)) continue;
+      const float w = lds[(i + b) * 32 + (lane & 31)];
+#pragma unroll
+      for (int d = 0; d < DN; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)  // columns past dim: not stored
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[d][4 * g + e] = fmaf(w, static_cast<float>(x[b][d][g][e]), acc[d][4 * g + e]);
+    }
+  }
 }
 
 }  // namespace trsc

@@ -70,59 +70,6 @@ __device__ __forceinline__ void hide(f32x16& s, int j0, int lo, int hi, int sink
   }
 }
 
-// Result of one row: elements 2 lane, 2 lane + 1 (already divided by the sum),
-// and the base-2 log of the sum.
-template <class E>
-__device__ __forceinline__ void store_row(const AttnArgs& a, int splits, int split, int head, int64_t q_at, float2 o,
-                                          float lg, int lane) {
-  typedef E out2 __attribute__((ext_vector_type(2)));
-  const bool in = 2 * lane < a.dim;
-  if (splits == 1) {
-    E* op = static_cast<E*>(const_cast<void*>(a.o.p)) + q_at * a.o.ts + head * a.o.hs + 2 * lane;
-    if (in) *reinterpret_cast<out2*>(op) = out2{static_cast<E>(o.x), static_cast<E>(o.y)};
-    if (a.lse != nullptr && lane == 0) a.lse[int64_t(head) * a.nq + q_at] = lg * 0.6931471805599453f;
-  } else {
-    const int64_t at = (int64_t(split) * a.hq + head) * a.nq + q_at;
-    if (in) *reinterpret_cast<float2*>(a.part + at * a.dim + 2 * lane) = o;
-    if (lane == 0) a.part[int64_t(splits) * a.hq * a.nq * a.dim + at] = lg;
-  }
-}
-
-// One row over the key tiles [first, end), touching only the keys it sees.
-template <class E, int KT>
-__device__ void careful_row(const AttnArgs& a, const Seq& q, const KeyTiles& kt, int first, int end, int splits,
-                            int split, int tok, int head, int kvh, int lane) {
-  const int64_t q_at = q.q0 + tok;
-  const int p = tok + q.lk - q.lq;
-  const float c = a.scale * kLog2e;
-  const float2 x = pair_of(static_cast<const E*>(a.q.p) + q_at * a.q.ts + head * a.q.hs, a.dim, lane);
-  float2 o = make_float2(0.f, 0.f);
-  float m = -INFINITY, l = 0.f;
-  for (int it = first; it < end; ++it) {
-    for (int j = kt.at(it) * KT, je = j + KT; j < je; ++j) {
-      if (!sees_key(a, p, j, q.lk)) continue;
-      const int64_t at = q.k0 + j;
-      const float2 y = pair_of(static_cast<const E*>(a.k.p) + at * a.k.ts + kvh * a.k.hs, a.dim, lane);
-      const float2 v = pair_of(static_cast<const E*>(a.v.p) + at * a.v.ts + kvh * a.v.hs, a.dim, lane);
-      const float s = wave_sum(x.x * y.x + x.y * y.y);
-      const float mx = fmaxf(m, s), ms = mx == -INFINITY ? 0.f : mx;
-      const float f = __builtin_amdgcn_exp2f((m - ms) * c), w = __builtin_amdgcn_exp2f((s - ms) * c);
-      if (f != 1.f) {
-        l *= f;
-        o.x *= f;
-        o.y *= f;
-      }
-      m = mx;
-      l += w;
-      o.x += w * v.x;
-      o.y += w * v.y;
-    }
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const float lg = l == 0.f ? -INFINITY : m * c + __builtin_amdgcn_logf(l);
-  store_row<E>(a, splits, split, head, q_at, make_float2(o.x * inv, o.y * inv), lg, lane);
-}
-
 // A wave's 32 rows on their way over the keys: lane l and l + 32 hold row l.
 template <class E, int NB, int KB>
 struct RowState {
@@ -313,6 +260,64 @@ __device__ __forceinline__ bool tile_whole(const AttnArgs& a, const WaveRows& w,
   return j1 <= w.p0 + a.right && j1 < lk && (j0 >= w.p1 - a.left || j1 < a.sinks);
 }
 
+// A wave's rows again over the key tiles [first, end), adding only what each sees (attn_common.h): blocks d0 ..
+// d0 + DN of O^T, the scaled maximum and the sum. lds: 4 KB of the wave's own.
+template <class E, int NB, int KT, int DN>
+__device__ void safe_rows(const AttnArgs& a, const RowTile& t, const KeyTiles& kt, int first, int end,
+                          const WaveRows& w, int kvh, int d0, float* lds, int lane, f32x16 (&acc)[NB], float& mc,
+                          float& l) {
+  constexpr int ST = NB * 2;
+  const Seq& q = t.q;
+  const E* qp = static_cast<const E*>(a.q.p) + int64_t(q.q0 + w.tok) * a.q.ts + w.head * a.q.hs;
+  const E* kbase = static_cast<const E*>(a.k.p) + int64_t(q.k0) * a.k.ts + kvh * a.k.hs;
+  const E* vbase = static_cast<const E*>(a.v.p) + int64_t(q.k0) * a.v.ts + kvh * a.v.hs;
+  const float c = a.scale * kLog2e;
+  typename AttnType<E>::frag qf[ST];
+#pragma unroll
+  for (int st = 0; st < ST; ++st) qf[st] = row_from<E>(qp, w.on, st, a.dim, lane);
+#pragma unroll
+  for (int d = 0; d < DN; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[d][e] = 0.f;
+  float m = -INFINITY;
+  l = 0.f;
+  for (int it = first * (KT / 32); it < end * (KT / 32); ++it) {
+    const int j0 = kt.at(it / (KT / 32)) * KT + it % (KT / 32) * 32;
+    if (!tile_seen(a, w, j0, j0 + 31)) continue;
+    const int mine = j0 + (lane & 31);
+    f32x16 s = scores_from<E, ST>(kbase + mine * a.k.ts, mine < q.lk, qf, a.dim, lane);
+    hide(s, j0, w.lo, w.hi, a.sinks, lane);
+    float mx = m;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[e]);
+    const float2 mh = both_halves(mx);
+    mx = fmaxf(mh.x, mh.y);
+    const float ms = mx == -INFINITY ? 0.f : mx, f = __builtin_amdgcn_exp2f((m - ms) * c);
+    m = mx;
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      s[e] = __builtin_amdgcn_exp2f((s[e] - ms) * c);
+      l += s[e];
+    }
+    if (f != 1.f) {
+#pragma unroll
+      for (int d = 0; d < DN; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[d][e] *= f;
+    }
+    put_factors(lds, s, lane);
+    wave_fence();
+    add_rows<E, DN>(
+        acc, lds, [&](int i) { return vbase + min(j0 + i, q.lk - 1) * a.v.ts; },
+        [&](int i) { return j0 + i <= w.hi && (j0 + i >= w.lo || j0 + i < a.sinks); }, d0, a.dim, lane);
+    wave_fence();
+  }
+  mc = m * c;
+  const float2 lh = both_halves(l);
+  l = lh.x + lh.y;
+}
+
 template <class E, int NB, bool TOKEN>
 struct FwdShape {
   typedef Tile<E, NB> T;
@@ -464,37 +469,38 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 && NB == 4                ? 1
   }
   // rows whose sums are not finite, again without what they do not see
   {
-    float t = 0.f;
+    float zero = 0.f;
     if (writer && wr.on) {
       if constexpr (TOKEN) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) t = fmaf(st.acc[0][e], 0.f, t);
+        for (int e = 0; e < 16; ++e) zero = fmaf(st.acc[0][e], 0.f, zero);
       } else {
-        t = zero_if_finite<NB>(st.acc);
+        zero = zero_if_finite<NB>(st.acc);
       }
     }
-    uint32_t bad = bad_rows(t);
-    if constexpr (TOKEN) {  // each wave has seen some of the columns: the rows of all four, shared out
+    uint32_t bad = bad_rows(zero);
+    if constexpr (TOKEN) {  // each wave has seen some of the columns: the rows of all four
       uint32_t* flags = reinterpret_cast<uint32_t*>(s_mem);
       __syncthreads();
       if (lane == 0) flags[wave] = bad;
       __syncthreads();
       bad = flags[0] | flags[1] | flags[2] | flags[3];
     }
+    auto store = [&](bool which) {
+      if (wr.on && writer && which)
+        store_tile_row<E, NB>(a, splits, split, wr.head, q.q0 + wr.tok, st.acc, mc, l, TOKEN ? wave : 0,
+                              TOKEN ? 1 : NB, h == 0 && (!TOKEN || wave == 0), h);
+    };
+    const bool mine = (bad >> l32) & 1u;
+    store(!mine);
     if (bad != 0) {
-      const int base = wr.first;
-      for (int i = 0; i < 32; ++i) {
-        if (!((bad >> i) & 1u) || (TOKEN && (i & 3) != wave)) continue;
-        const int t_i = (base + i) / group;
-        careful_row<E, F::kKeys>(a, q, kt, first, end, splits, split, t_i, kvh * group + base + i - t_i * group, kvh,
-                                 lane);
-      }
-      if ((bad >> l32) & 1u) return;  // its row is written
+      if constexpr (TOKEN) __syncthreads();  // the flags are read
+      if (!writer) return;
+      safe_rows<E, NB, F::kKeys, TOKEN ? 1 : NB>(a, t, kt, first, end, wr, kvh, TOKEN ? wave : 0,
+                                                 reinterpret_cast<float*>(s_mem) + wave * 1024, lane, st.acc, mc, l);
+      store(mine);
     }
   }
-  if (!wr.on || !writer) return;
-  store_tile_row<E, NB>(a, splits, split, wr.head, q.q0 + wr.tok, st.acc, mc, l, TOKEN ? wave : 0, TOKEN ? 1 : NB,
-                        h == 0 && (!TOKEN || wave == 0), h);
 }
 
 // Joins the splits of a row: o = sum_s 2^{l_s - l} o_s, l = log2 sum_s 2^{l_s}.
