@@ -89,10 +89,11 @@ int fill_norm(const char* who, const tr_sc_heads* q, const tr_sc_heads* k, const
   if ((q_gain != nullptr && q_gain_rows != 1 && q_gain_rows != q->heads) ||
       (k_gain != nullptr && k_gain_rows != 1 && k_gain_rows != k->heads))
     return fail(TR_SC_ERR_INVALID_ARG, "%s: a gain has one row or one a head", who);
-  a->q = NormSide{q->data, q->token_stride, q->head_stride, nullptr, 0, 0, nullptr, 0, 0, q_gain, q_gain_rows,
-                  nullptr, q->heads};
-  a->k = NormSide{k->data, k->token_stride, k->head_stride, nullptr, 0, 0, nullptr, 0, 0, k_gain, k_gain_rows,
-                  nullptr, k->heads};
+  // the rows of a gain that is not there are whatever the caller left
+  a->q = NormSide{q->data, q->token_stride, q->head_stride, nullptr, 0, 0, nullptr, 0, 0, q_gain,
+                  q_gain != nullptr ? q_gain_rows : 1, nullptr, q->heads};
+  a->k = NormSide{k->data, k->token_stride, k->head_stride, nullptr, 0, 0, nullptr, 0, 0, k_gain,
+                  k_gain != nullptr ? k_gain_rows : 1, nullptr, k->heads};
   a->pos = rot->pos;
   a->pos_ts = rot->pos_stride;
   a->freqs = rot->freqs;
