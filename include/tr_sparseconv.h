@@ -368,9 +368,10 @@ typedef struct {
  *     y = x / sqrt(mean(x^2) + eps) * gain[h],  then y's pairs turned.
  * q, k         inputs [tokens, heads, dim] of type dtype; each its own head count.
  * *_gain       device fp32 [rows, dim], rows 1 (shared by the heads) or the
- *              heads; NULL: no gain.
+ *              heads; NULL: no gain (its rows are not read).
  * q_out, k_out outputs of the same shape and type; may be q, k themselves (same
- *              strides), otherwise they must not overlap the inputs.
+ *              strides), otherwise they must not overlap the inputs or each
+ *              other (TR_SC_ERR_INVALID_ARG).
  * dim a multiple of 8 up to 128; fp32 arithmetic, rounded once. The angles are
  * reduced in 64 bits, so they are as good at large positions as at small ones. */
 int tr_sparseconv_qk_norm_rope(const tr_sc_heads* q, const tr_sc_heads* k, const tr_sc_rotation* rotation,
@@ -380,9 +381,10 @@ int tr_sparseconv_qk_norm_rope(const tr_sc_heads* q, const tr_sc_heads* k, const
 
 /* Its gradient: dq_out, dk_out -> dq, dk (all [tokens, heads, dim] of type
  * dtype), dq_gain, dk_gain (fp32, as the gains, 16-byte aligned; NULL: not
- * wanted). q, k: the forward's inputs. dq, dk may be dq_out, dk_out themselves (same strides). The
- * gains' sums are taken in a fixed order (no atomics: the same bits on every
- * call). workspace: >= the bytes below, 256-byte aligned. */
+ * wanted). q, k: the forward's inputs. dq, dk may be dq_out, dk_out or q, k
+ * themselves (same strides), otherwise they must not overlap the inputs or each
+ * other. The gains' sums are taken in a fixed order (no atomics: the same bits
+ * on every call). workspace: >= the bytes below, 256-byte aligned. */
 size_t tr_sparseconv_qk_norm_rope_backward_workspace_bytes(int64_t tokens, int q_heads, int kv_heads,
                                                            int dim);
 int tr_sparseconv_qk_norm_rope_backward(const tr_sc_heads* dq_out, const tr_sc_heads* dk_out,
@@ -433,7 +435,9 @@ typedef struct {
  * workspace  >= the bytes below, 256-byte aligned (0 bytes: may be NULL). The
  *            query needs batch, left, right, sinks and scale of the window, not
  *            its device arrays beyond whether they are NULL.
- * No atomics: the same bits on every call. out must not overlap q, k, v. */
+ * No atomics: the same bits on every call. out and lse must not overlap q, k, v
+ * or each other (TR_SC_ERR_INVALID_ARG; views of unlike token strides in one
+ * range count as overlapping). */
 size_t tr_sparseconv_window_attention_workspace_bytes(const tr_sc_window* window, int64_t tokens_q,
                                                       int64_t tokens_k, int q_heads, int kv_heads,
                                                       int dim, int dtype);
@@ -446,7 +450,8 @@ int tr_sparseconv_window_attention(const tr_sc_heads* q, const tr_sc_heads* k, c
  * and window (that a row's weights sum to one is used); dq [tokens_q, q heads,
  * dim], dk, dv [tokens_k, kv heads, dim] of type dtype, contiguous. Keys past
  * k_len get zeros. The weights and the scores' gradients are rounded to dtype
- * before their products; sums are fp32. No atomics: the same bits on every call. */
+ * before their products; sums are fp32. No atomics: the same bits on every call.
+ * dq, dk, dv must not overlap the inputs or each other. */
 size_t tr_sparseconv_window_attention_backward_workspace_bytes(const tr_sc_window* window,
                                                                int64_t tokens_q, int64_t tokens_k,
                                                                int q_heads, int kv_heads, int dim,

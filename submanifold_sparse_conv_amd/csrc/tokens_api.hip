@@ -48,6 +48,86 @@ int check_heads(const char* who, const char* name, const tr_sc_heads* t, int64_t
   return TR_SC_OK;
 }
 
+// ---------------------------------------------------------------------------
+// Outputs that overlap. A view's elements are, in bytes, `dim` from each of
+// at + t ts + h hs, t < tokens, h < heads.
+// ---------------------------------------------------------------------------
+typedef __int128 wide_t;  // strides up to 2^42 bytes times 2^30 tokens
+struct View {
+  const char* name;
+  int64_t at, ts, hs, tokens, heads, dim;
+  wide_t end() const { return wide_t(tokens - 1) * ts + wide_t(heads - 1) * hs + at + dim; }
+};
+
+View view_of(const char* name, const tr_sc_heads* t, int64_t tokens, int dim, int dtype) {
+  const int64_t b = elem_bytes(dtype);
+  return View{name, reinterpret_cast<int64_t>(t->data), t->token_stride * b, t->head_stride * b, tokens, t->heads, dim * b};
+}
+View packed_view(const char* name, const void* p, int64_t tokens, int64_t heads, int64_t dim, int64_t bytes) {
+  return View{name, reinterpret_cast<int64_t>(p), heads * dim * bytes, dim * bytes, tokens, heads, dim * bytes};
+}
+
+// Whether a step s of [lo, hi] brings [d + s ts, d + s ts + len) onto [0, width).
+bool meets(wide_t d, int64_t ts, int64_t lo, int64_t hi, int64_t len, int64_t width) {
+  if (ts == 0) return d < width && d + len > 0;
+  // the first step whose end passes 0
+  wide_t s = -(d + len) / ts - 1;
+  while (d + s * ts + len <= 0) ++s;
+  s = s < lo ? lo : s;
+  return s <= hi && d + s * ts + len > 0 && d + s * ts < width;
+}
+
+bool overlap(const View& a, const View& b) {
+  if (a.tokens == 0 || b.tokens == 0 || a.heads == 0 || b.heads == 0 || a.dim == 0 || b.dim == 0) return false;
+  if (a.end() <= b.at || b.end() <= a.at) return false;
+  // Tokens at unlike strides in one range: taken to overlap.
+  if (a.tokens > 1 && b.tokens > 1 && a.ts != b.ts) return true;
+  const int64_t ts = a.tokens > 1 ? a.ts : b.ts;
+  // Slices of the same rows, side by side.
+  if (ts > 0) {
+    const int64_t d = ((b.at - a.at) % ts + ts) % ts;
+    if ((a.heads - 1) * a.hs + a.dim <= d && d + (b.heads - 1) * b.hs + b.dim <= ts) return false;
+  }
+  // Heads that alternate: each with each, within reason.
+  if (a.heads * b.heads > 65536) return true;
+  for (int64_t i = 0; i < a.heads; ++i)
+    for (int64_t j = 0; j < b.heads; ++j)
+      if (meets(b.at + j * b.hs - a.at - i * a.hs, ts, 1 - a.tokens, b.tokens - 1, b.dim, a.dim)) return true;
+  return false;
+}
+
+bool rows_overlap(const View& a) {  // of one view
+  if (a.tokens == 0 || (a.heads - 1) * a.hs + a.dim <= a.ts || (a.tokens - 1) * a.ts + a.dim <= a.hs) return false;
+  if (a.tokens > 1 && a.ts < a.dim) return true;
+  for (int64_t h = 1; h < a.heads; ++h)
+    if (meets(h * a.hs, a.ts, 1 - a.tokens, a.tokens - 1, a.dim, a.dim)) return true;
+  return false;
+}
+
+bool same_view(const View& a, const View& b) {
+  return a.at == b.at && a.tokens == b.tokens && a.heads == b.heads && (a.tokens <= 1 || a.ts == b.ts) &&
+         (a.heads <= 1 || a.hs == b.hs);
+}
+
+// Each output's own rows, and each against the inputs and the outputs before it. in_place[i] (may be null): views
+// that output i may be itself.
+struct Output {
+  View view;
+  const View* in_place[2];
+};
+int check_overlap(const char* who, const Output* outs, int n_outs, const View* ins, int n_ins) {
+  for (int i = 0; i < n_outs; ++i) {
+    const View& o = outs[i].view;
+    if (rows_overlap(o)) return fail(TR_SC_ERR_INVALID_ARG, "%s: rows of %s overlap", who, o.name);
+    for (int j = 0; j < n_ins + i; ++j) {
+      const View& x = j < n_ins ? ins[j] : outs[j - n_ins].view;
+      const bool allowed = (outs[i].in_place[0] == &x || outs[i].in_place[1] == &x) && same_view(o, x);
+      if (!allowed && overlap(o, x)) return fail(TR_SC_ERR_INVALID_ARG, "%s: %s overlaps %s", who, o.name, x.name);
+    }
+  }
+  return TR_SC_OK;
+}
+
 int check_workspace(const char* who, const void* ws, size_t have, size_t need) {
   if (have < need) return fail(TR_SC_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", who, have, need);
   if (need > 0 && (ws == nullptr || reinterpret_cast<uintptr_t>(ws) % 256 != 0))
@@ -222,6 +302,11 @@ int tr_sparseconv_qk_norm_rope(const tr_sc_heads* q, const tr_sc_heads* k, const
   if (c == TR_SC_OK) c = check_heads(who, "q_out", q_out, tokens, q->heads, dim, dtype, true);
   if (c == TR_SC_OK) c = check_heads(who, "k_out", k_out, tokens, k->heads, dim, dtype, true);
   if (c != TR_SC_OK) return c;
+  const View ins[] = {view_of("q", q, tokens, dim, dtype), view_of("k", k, tokens, dim, dtype)};
+  const Output outs[] = {{view_of("q_out", q_out, tokens, dim, dtype), {&ins[0], nullptr}},
+                         {view_of("k_out", k_out, tokens, dim, dtype), {&ins[1], nullptr}}};
+  c = check_overlap(who, outs, 2, ins, 2);
+  if (c != TR_SC_OK) return c;
   set_out(&a.q, q_out);
   set_out(&a.k, k_out);
   const hipError_t e = launch_norm_rope(a, static_cast<hipStream_t>(stream));
@@ -251,6 +336,12 @@ int tr_sparseconv_qk_norm_rope_backward(const tr_sc_heads* dq_out, const tr_sc_h
   if (c == TR_SC_OK)
     c = check_workspace(who, workspace, ws_bytes,
                         tr_sparseconv_qk_norm_rope_backward_workspace_bytes(tokens, q->heads, k->heads, dim));
+  if (c != TR_SC_OK) return c;
+  const View ins[] = {view_of("q", q, tokens, dim, dtype), view_of("k", k, tokens, dim, dtype),
+                      view_of("dq_out", dq_out, tokens, dim, dtype), view_of("dk_out", dk_out, tokens, dim, dtype)};
+  const Output outs[] = {{view_of("dq", dq, tokens, dim, dtype), {&ins[0], &ins[2]}},
+                         {view_of("dk", dk, tokens, dim, dtype), {&ins[1], &ins[3]}}};
+  c = check_overlap(who, outs, 2, ins, 4);
   if (c != TR_SC_OK) return c;
   if ((dq_gain != nullptr && q_gain == nullptr) || (dk_gain != nullptr && k_gain == nullptr))
     return fail(TR_SC_ERR_INVALID_ARG, "%s: the gradient of a gain that is not there", who);
@@ -286,6 +377,12 @@ int tr_sparseconv_window_attention(const tr_sc_heads* q, const tr_sc_heads* k, c
   const AttnPlan plan = plan_attention(a);
   c = check_workspace(who, workspace, ws_bytes, align_up(plan.part_floats * 4, 256));
   if (c != TR_SC_OK) return c;
+  const View ins[] = {view_of("q", q, tokens_q, dim, dtype), view_of("k", k, tokens_k, dim, dtype),
+                      view_of("v", v, tokens_k, dim, dtype)};
+  const Output outs[] = {{view_of("out", out, tokens_q, dim, dtype), {nullptr, nullptr}},
+                         {packed_view("lse", lse, lse != nullptr ? q->heads : 0, 1, tokens_q, 4), {nullptr, nullptr}}};
+  c = check_overlap(who, outs, 2, ins, 3);
+  if (c != TR_SC_OK) return c;
   a.o = ref(out);
   a.lse = lse;
   a.part = static_cast<float*>(workspace);
@@ -320,6 +417,15 @@ int tr_sparseconv_window_attention_backward(const tr_sc_heads* dout, const tr_sc
     return fail(TR_SC_ERR_INVALID_ARG, "%s: dq, dk and dv must be 16-byte aligned", who);
   const BackwardLayout l = backward_layout(a);
   c = check_workspace(who, workspace, ws_bytes, l.total);
+  if (c != TR_SC_OK) return c;
+  const View ins[] = {view_of("q", q, tokens_q, dim, dtype),       view_of("k", k, tokens_k, dim, dtype),
+                      view_of("v", v, tokens_k, dim, dtype),       view_of("out", out, tokens_q, dim, dtype),
+                      view_of("dout", dout, tokens_q, dim, dtype), packed_view("lse", lse, q->heads, 1, tokens_q, 4)};
+  const int b = elem_bytes(dtype);
+  const Output outs[] = {{packed_view("dq", dq, tokens_q, q->heads, dim, b), {nullptr, nullptr}},
+                         {packed_view("dk", dk, tokens_k, k->heads, dim, b), {nullptr, nullptr}},
+                         {packed_view("dv", dv, tokens_k, k->heads, dim, b), {nullptr, nullptr}}};
+  c = check_overlap(who, outs, 3, ins, 6);
   if (c != TR_SC_OK) return c;
   a.dout = ref(dout);
   a.o = ref(out);

@@ -152,7 +152,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, freqs: tor
     pos: int32 [tokens, axes] (1 to 3; coords[:, 1:] serves) or [tokens]; freqs:
     fp32 [dim / 2], radians a step (rope_frequencies); sections: pairs of each
     axis, default dim / 2 // axes. Gains: fp32 [dim] (shared) or [heads, dim].
-    q_out / k_out may be q / k themselves."""
+    q_out / k_out may be q / k themselves; other overlaps are refused."""
     dt = _dtype(q, "q")
     hq = _heads(q, "q")
     n, _, dim = q.shape
