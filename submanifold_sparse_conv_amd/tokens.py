@@ -64,6 +64,8 @@ def _scratch(nbytes: int, device, given):
     if given is not None:
         if given.nbytes < nbytes:
             raise ValueError(f"workspace of {given.nbytes} bytes, {nbytes} needed")
+        if given.buf.device != device:
+            raise ValueError(f"the workspace is on {given.buf.device}, the tensors on {device}")
         return given.ptr, given.nbytes, given
     if nbytes == 0:
         return None, 0, None

@@ -1,0 +1,22 @@
+"""Arguments that the token operators' binding refuses itself; none of them reaches a kernel."""
+import pytest
+import torch
+
+from tests.test_gpu_tokens import DEV, gen, randn
+
+pytestmark = pytest.mark.gpu
+
+sc = pytest.importorskip("submanifold_sparse_conv_amd")
+
+
+def test_workspace_in_host_memory():
+    q = randn(gen(91), 64, 2, 64, dtype=torch.bfloat16).to(DEV)
+    pos = torch.arange(64, dtype=torch.int32, device=DEV)
+    f = sc.rope_frequencies(64, device=DEV)
+    out, lse = sc.window_attention(q, q, q, left=3, right=0, return_lse=True)
+    ws = sc.Workspace(1 << 22, "cpu")
+    for call in (lambda: sc.window_attention(q[:1], q, q, workspace=ws),
+                 lambda: sc.window_attention_backward(q, q, q, q, out, lse, left=3, right=0, workspace=ws),
+                 lambda: sc.qk_norm_rope_backward(q, q, q, q, pos, f, workspace=ws)):
+        with pytest.raises(ValueError, match="workspace is on cpu"):
+            call()
