@@ -125,8 +125,8 @@ def _rotation(pos, freqs, sections, interleaved, tokens, dim, device) -> Rotatio
         raise ValueError(f"freqs must be fp32 [{dim // 2}] on {device}")
     if sections is None:
         sections = [dim // 2 // axes] * axes
-    if len(sections) != axes:
-        raise ValueError(f"{axes} axes need {axes} sections, got {list(sections)}")
+    if len(sections) != axes or not all(0 <= s <= dim for s in sections):
+        raise ValueError(f"{axes} axes need {axes} sections of pairs, got {list(sections)}")
     return Rotation(pos.data_ptr() if tokens else None, pos.stride(0) if tokens > 1 else 0, freqs.data_ptr(), axes,
                     _Pairs(*sections), bool(interleaved))
 
@@ -205,6 +205,9 @@ def _window(cu_q, cu_k, k_len, left, right, sinks, scale, dim, device) -> Window
         raise ValueError("cu_q and cu_k go together")
     if cu_q is not None and isinstance(cu_q, torch.Tensor) and cu_q.dim() == 1 and cu_q.shape[0] < 2:
         raise ValueError("cu_q needs two elements at least (one sequence)")
+    # a number past its C field would be taken modulo its range
+    if not (-1 <= left < 1 << 63 and -1 <= right < 1 << 63 and 0 <= sinks < 1 << 31):
+        raise ValueError(f"window ({left}, {right}) with {sinks} sinks: sides are -1 or more, sinks 0 or more")
     batch = 1 if cu_q is None else len(cu_q) - 1
     return Window(_ints(cu_q, "cu_q", -1, device), _ints(cu_k, "cu_k", batch + 1, device),
                   _ints(k_len, "k_len", batch, device), batch, left, right, sinks,
