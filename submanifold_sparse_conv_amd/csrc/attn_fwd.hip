@@ -52,11 +52,12 @@ constexpr float kMostSum = 16384.f;
 // of up to 32 keys falls below kLeastSum16 (a leading key before them, a sink say), the tile's own largest weight
 // becomes 2^kBase16 and the sums grow instead, which fp32 has room for. So the weights of every tile keep the type's
 // precision among themselves, and a row gets a share of 2^-30 as exactly as a large one. (With the base fixed by
-// the leading key, keys 16 nats below it had 2 to 4 bits left.) Right after, a tile's sum is 2^6 to 2^11: it may
-// rise by 4 powers of two and more, or fall by 15, before the base moves again, so scores that spread by a few nats
-// seldom move it. In a tile that itself spreads further the largest weight goes up to 2^kTop16: keys up to 20 nats
-// under it stay normal. No growing past sums of kMostL: what could still come is below 2^-64 of what was.
-constexpr float kMostSum16 = 49152.f, kLeastSum16 = 1.f / 512.f, kBase16 = 6.f, kTop16 = 15.f, kMostL = 1.8446744e19f;
+// the leading key, keys 16 nats below it had 2 to 4 bits left.) Right after, a tile's sum is 2^2 to 2^7: it may
+// rise by 8 powers of two and more, or fall by 11, before the base moves again, so scores that spread by a few nats
+// seldom move it (2^6 in place of 2^2: 33.8 us for 30.5, the forward of 4,616 tokens, 16 heads of 64 over 4; with a
+// base that only rises 31.1). In a tile that itself spreads further the largest weight goes up to 2^kTop16: keys up
+// to 20 nats under it stay normal. No growing past sums of kMostL: what could still come is below 2^-64 of what was.
+constexpr float kMostSum16 = 49152.f, kLeastSum16 = 1.f / 512.f, kBase16 = 2.f, kTop16 = 15.f, kMostL = 1.8446744e19f;
 
 // The scores of 32 keys j0 + 8 g + 4 (lane / 32) + i: hidden ones become -inf.
 __device__ __forceinline__ void hide(f32x16& s, int j0, int lo, int hi, int sinks, int lane) {
@@ -121,14 +122,15 @@ struct RowState {
         }
     return sum[0] + sum[1];
   }
-  // whether the tile's weights are in range (a row that sees none of it has the sum 0)
+  // whether the tile's weights are in range
   static __device__ __forceinline__ bool in_range(float sum) {
-    if constexpr (kNarrow) return sum < kMostSum16 && (sum >= kLeastSum16 || sum == 0.f);
+    if constexpr (kNarrow) return __builtin_amdgcn_fmed3f(sum, kLeastSum16, kMostSum16) == sum;
     return sum < kMostSum;
   }
   __device__ __forceinline__ void weigh(float c) {
     float sum = weigh_by(c, mc);
-    if (__any(!in_range(sum))) {  // also where the row has seen nothing before (mc = -inf)
+    const bool out = !in_range(sum);  // also where the row has seen nothing before (mc = -inf: the sum is NaN)
+    if (__any(out) && (!kNarrow || __any(out && sum != 0.f))) {  // a row that sees none of the tile has the sum 0
       float mx = -INFINITY;
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb)
