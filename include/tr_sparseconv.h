@@ -373,7 +373,8 @@ typedef struct {
  *              strides), otherwise they must not overlap the inputs or each
  *              other (TR_SC_ERR_INVALID_ARG).
  * dim a multiple of 8 up to 128; fp32 arithmetic, rounded once. The angles are
- * reduced in 64 bits, so they are as good at large positions as at small ones. */
+ * reduced in 64 bits: as good where position x frequency is 2^28 as at small
+ * positions, and off by 7e-8 turns near 2^31. */
 int tr_sparseconv_qk_norm_rope(const tr_sc_heads* q, const tr_sc_heads* k, const tr_sc_rotation* rotation,
                                const float* q_gain, int q_gain_rows, const float* k_gain,
                                int k_gain_rows, float eps, const tr_sc_heads* q_out,
@@ -428,7 +429,8 @@ typedef struct {
  * bf16, f16 or f32; dim a multiple of 8 up to 128. fp32 scores, statistics and
  * sums; the weights of a row are rounded to dtype before they multiply v.
  * What lies in keys and values that a row does not see (NaN, infinities) does
- * not reach it.
+ * not reach it; where a result is not finite the call takes 10 to 30 times as
+ * long.
  * lse        fp32 [q heads, tokens_q] or NULL: log of the sum of the
  *            exponentials of the scaled scores, -infinity for a row that sees
  *            none. The backward reads it.
@@ -450,7 +452,9 @@ int tr_sparseconv_window_attention(const tr_sc_heads* q, const tr_sc_heads* k, c
  * and window (that a row's weights sum to one is used); dq [tokens_q, q heads,
  * dim], dk, dv [tokens_k, kv heads, dim] of type dtype, contiguous. Keys past
  * k_len get zeros. The weights and the scores' gradients are rounded to dtype
- * before their products; sums are fp32. No atomics: the same bits on every call.
+ * before their products (in fp16 with powers of two that keep them in its range,
+ * whatever the sizes of dout and v); sums are fp32. The workspace holds 8 bytes a
+ * row of q, and for sinks about q's elements x sinks / 64 bytes. No atomics: the same bits on every call.
  * dq, dk, dv must not overlap the inputs or each other. */
 size_t tr_sparseconv_window_attention_backward_workspace_bytes(const tr_sc_window* window,
                                                                int64_t tokens_q, int64_t tokens_k,

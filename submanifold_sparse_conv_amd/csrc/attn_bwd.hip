@@ -24,15 +24,16 @@
 // keys, so the dk, dv kernel takes that for delta, and dq is mended by a
 // second product (see attn_dq). Without either, dq and dk of windows of 32
 // keys were 1.8 times as far from the exact gradient as rounding once (now 1.5
-// at most); the second product is 4 % of the gradient's time.
+// at most); the second product is 4 % of the gradient's time. fp16's ranges take
+// 8 us of the 150 below.
 //
-// What bounds it. bf16, 15,800 tokens, 12 heads of 128, 512 keys either way: 490
-// us for 0.25 TFLOP (10 flops a pair and element; 16 with what is computed twice
-// and the second product, 800 TFLOP/s): matrix units and the LDS reads that feed
-// them, one fragment a product, at two workgroups a CU (registers). fp16, 4,616
-// tokens in two sequences, 16 heads of 64 over 4, 1023 back: 137 us, latencies: each
-// SIMD has two waves, and a wave's products, exponentials and packings follow
-// one another.
+// What bounds it. bf16, 15,800 tokens, 12 heads of 128, 512 keys either way: 495
+// to 510 us for 0.25 TFLOP (10 flops a pair and element; 16 with what is computed
+// twice and the second product, 780 TFLOP/s): matrix units and the LDS reads that
+// feed them, one fragment a product, at two workgroups a CU (registers). fp16,
+// 4,616 tokens in two sequences, 16 heads of 64 over 4, 1023 back: 150 us,
+// latencies: each SIMD has two waves, and a wave's products, exponentials and
+// packings follow one another.
 //
 // Sinks. All later rows see the sinks, so the tile that holds them would walk
 // all rows. Its rows past the band go to workgroups of their own, in chunks;
@@ -430,8 +431,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dkv(AttnArgs
   typedef AttnType<E> A;
   typedef typename A::frag frag;
   constexpr int ST = NB * 2, kAhead = A::wide ? 1 : SINK ? 2 : 4;
-  // Rows between two barriers: heads of 64 and less have the LDS for twice as many (the fp16 size above 173 us with
-  // its forward, 181 without).
+  // Rows between two barriers: heads of 64 and less have the LDS for twice as many (the fp16 size above 182 us with
+  // its forward, 187 without).
   constexpr int kRows = SINK || A::wide || NB > 2 ? kRowTile : 2 * kRowTile;
   typedef RowStats<kRows> Stats;
   constexpr int kTileBytes = kRows * T::kPitch;
@@ -823,7 +824,7 @@ __global__ __launch_bounds__(256) void attn_parts(AttnArgs a, int parts) {
 
 // Parts of the row walk of a key tile: few key tiles with many rows each (short
 // sequences, many query heads to a kv head) would leave most of the chip idle
-// (the fp16 size above: 175 us with its forward and four parts, 236 with one).
+// (the fp16 size above: 182 us with its forward and four parts, 244 with one).
 int row_parts(const AttnArgs& a) {
   const int64_t wgs = tiles_of(a.nk, a.batch, 1, kKeysWg) * a.hk, group = a.hq / a.hk;
   const int64_t reach = int64_t(a.left) + a.right + 1 + kKeysWg;

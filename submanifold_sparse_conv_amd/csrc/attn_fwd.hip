@@ -24,17 +24,20 @@
 // unrounded: the result is off by that rounding's average and its own last one.
 // fp16's range is kept by a base that moves with the tiles (kMostSum16).
 //
-// What bounds it. bf16, 32,768 tokens, 16 query and 4 kv heads of 128, 4096 keys
-// back: 1.03 TFLOP in 1.00 ms, 1.03 PFLOP/s, of 1.19 that a large library product
-// reaches (both on clocks that power lowers): matrix units, one LDS fragment a
-// product. bf16, 73,881 tokens, 16 heads of 64, 512 keys either way: 0.31 TFLOP in
-// 426 us, 735 TFLOP/s: the 16 exponentials, sums and packings of every 8
-// products. fp32, 2,877 tokens in four sequences, 6 heads of 80 over 2, 255 either
-// way: 57 us, four splits a row tile to reach the chip, the products' padding (80
-// of 96) and the join. Token form: bytes; 32 caches of up to 4100 keys, 4 kv heads of
-// 128: 257 MB in 58 us, 4.4 TB/s; one cache of 65,540 keys: 134 MB in 36 us,
-// 3.8 TB/s, the join's launch (5 us) included; 48 and 31 us where the last call
-// has left part of them in the caches.
+// What bounds it (ranges: cards and their clocks differ). bf16, 32,768 tokens, 16
+// query and 4 kv heads of 128, 4096 keys back: 1.03 TFLOP in 0.99 to 1.05 ms, 0.98
+// to 1.04 PFLOP/s, of 1.19 that a large library product reaches (both on clocks
+// that power lowers): matrix units, one LDS fragment a product; fp16 1.05 to 1.09
+// ms. bf16, 73,881 tokens, 16 heads of 64, 512 keys either way: 0.31 TFLOP in 411
+// to 436 us, 708 to 750 TFLOP/s: vector instructions in 68 % of cycles (16
+// exponentials, sums and packings to every 8 products, and the window's edges) and
+// matrix units in 42 %, hardly at the same time; fp16 437 to 454 us. fp32, 2,877
+// tokens in four sequences, 6 heads of 80 over 2, 255 either way: 54.5 us, four
+// splits a row tile to reach the chip, the products' padding (80 of 96) and the
+// join. Token form: bytes; 32 caches of up to 4100 keys, 4 kv heads of 128: 257 MB
+// in 58.5 us, 4.4 TB/s (fp32 513 MB in 118); one cache of 65,540 keys: 134 MB in
+// 35.6 us, 3.8 TB/s (fp32 72.5 us), the join's launch (5 us) included; 48 and 31 us
+// where the last call has left part of them in the caches.
 #include "attn_common.h"
 
 namespace trsc {

@@ -6,7 +6,9 @@ tr_sparseconv_ prefix, in include/tr_sparseconv.h).
     y = window_attention(q, k, v, cu_q=cu, cu_k=cu, left=512, right=512, sinks=4)
 
 Tensors of heads are [tokens, heads, dim]; their rows' elements are adjacent,
-tokens and heads may be strided (slices of one projection's rows).
+tokens and heads may be strided (slices of one projection's rows) by multiples
+of 16 bytes. The calls record no gradients: the *_backward calls compute them
+(examples/voxel_transformer.py has autograd functions around both).
 """
 from __future__ import annotations
 
