@@ -66,9 +66,13 @@ constexpr float kWeightBack = A::narrow ? 1.f / 32768.f : 1.f;
 // it is now known to be. So it does for rows whose outputs are near or below the type's smallest normal, which give no
 // usable delta, where dS is small enough for that to show (dq of heads past 64 was up to 280 roundings off). In dk it
 // is one for the rows that a workgroup walks, from their largest |dS|, which the dq kernel leaves for it: a row far
-// below the others adds little to the same sums.
+// below the others adds little to the same sums. No |dS| counts as less than kScoreNoise (|lse| + 16) |o| |dout|, the
+// error of P delta: where one key has all the weight dS is that noise, another in either kernel, and raised to the
+// range's top in one it would overflow in the other (scores that spread by 60 nats: 660 us for 110, in a gradient of
+// 8192 tokens, 8 heads of 64).
 constexpr int kScoreShift = 9, kNoScore = -1000;
 constexpr float kLeastScore = 1.f / 512.f, kMostScore = 32768.f, kDeltaScore = 2.f, kLeastOut = 1.f / 2048.f;
+constexpr float kScoreNoise = 1.f / (1 << 20);
 __device__ __forceinline__ int exponent_of(float v) { return __builtin_amdgcn_frexp_expf(v); }  // 0 if not finite
 __device__ __forceinline__ float power_of_two(int n) { return __builtin_ldexpf(1.f, n); }
 
@@ -227,7 +231,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
   const int pw0 = min(wrow, rows - 1) / group + shift, pw1 = min(wrow + 31, rows - 1) / group + shift;
   const int64_t q_at = q.q0 + tok;
   frag qf[ST], df[ST];
-  float delta = 0.f, squares = 0.f, out_most = 0.f;  // o . do, do . do, largest |o|
+  float delta = 0.f, squares = 0.f, out_squares = 0.f, out_most = 0.f;  // o . do, do . do, o . o, largest |o|
   {
     const E* qp = static_cast<const E*>(a.q.p) + q_at * a.q.ts + head * a.q.hs;
     const E* dp = static_cast<const E*>(a.dout.p) + q_at * a.dout.ts + head * a.dout.hs;
@@ -242,6 +246,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
         delta = fmaf(float(of[e]), float(df[s][e]), delta);
         if constexpr (A::narrow) {
           squares = fmaf(float(df[s][e]), float(df[s][e]), squares);
+          out_squares = fmaf(float(of[e]), float(of[e]), out_squares);
           out_most = fmaxf(out_most, fabsf(float(of[e])));
         }
       }
@@ -251,7 +256,9 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
   int up = 0;  // dS is raised by 2^up
   bool low_out = false;
   if constexpr (A::narrow) {
-    up = kScoreShift - (exponent_of(squares + __shfl_xor(squares, 32)) >> 1);
+    squares += __shfl_xor(squares, 32);
+    out_squares += __shfl_xor(out_squares, 32);
+    up = kScoreShift - (exponent_of(squares) >> 1);
     low_out = fmaxf(out_most, __shfl_xor(out_most, 32)) < kLeastOut;
   }
   const float lse = on ? a.lse[int64_t(head) * a.nq + q_at] : 0.f;
@@ -360,7 +367,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 4 ? 1 : 2) void attn_dq(AttnArgs 
       const float back = power_of_two(kMean ? -15 : -up);
       half.x *= back;
       half.y *= back;
-      most = fmaxf(most, __shfl_xor(most, 32));
+      const float noise = sqrtf(squares * out_squares) * (fabsf(lse2) + 16.f) * kScoreNoise;
+      most = fmaxf(fmaxf(most, __shfl_xor(most, 32)), noise * power_of_two(up));
       if (pass > 0) break;
       const bool redo = on && most > 0.f && most < INFINITY &&
                         (most >= kMostScore || most < kLeastScore || (low_out && most < kDeltaScore));

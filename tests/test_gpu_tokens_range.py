@@ -244,3 +244,32 @@ def test_gradient_of_keys_without_the_outputs_rounding(dtype, dim, left, right, 
     _, _, want, tol = score_grad_bounds(q[:, 0], k[:, 0], v[:, 0], R.visible(n, n, left, right, sinks), dim ** -0.5,
                                         dout[:, 0])
     check(dk[:, 0], want, tol, "dk")
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("spread,left,right,length", [(8.0, 512, 512, 8192), (3.0, 512, 512, 8192), (1.3, 0, 0, 8192),
+                                                      (1.3, 512, 0, 32)])
+def test_sharp_attention_keeps_the_usual_path(spread, left, right, length, dim):
+    """Rows that give nearly all their weight to one key have score gradients of rounding noise; raising that into
+    fp16's range would only overflow where the noise is another. fp16 takes no more than twice bf16's time."""
+    n = 8192
+    g = gen(43)
+    cu = torch.arange(0, n + 1, length, dtype=torch.int32, device=DEV)
+    how = dict(cu_q=cu, cu_k=cu, left=left, right=right)
+    times = {}
+    for dtype in (torch.bfloat16, torch.float16):
+        q, k, v, dout = (randn(g, n, 8, dim, dtype=dtype, scale=s).to(DEV) for s in (spread, spread, 1.0, 1.0))
+        times[dtype] = []
+        for same in (False, True):  # queries of their own, or each its key
+            args = (k if same else q, k, v)
+            out, lse = sc.window_attention(*args, return_lse=True, **how)
+            at = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            best = math.inf
+            for _ in range(5):
+                at[0].record()
+                sc.window_attention_backward(dout, *args, out, lse, **how)
+                at[1].record()
+                at[1].synchronize()
+                best = min(best, at[0].elapsed_time(at[1]))
+            times[dtype].append(best)
+    assert all(a < 2 * b for a, b in zip(times[torch.float16], times[torch.bfloat16])), times
