@@ -247,6 +247,25 @@ def test_gradient_of_keys_without_the_outputs_rounding(dtype, dim, left, right, 
 
 
 @pytest.mark.parametrize("dim", [64, 128])
+def test_gradient_beside_an_outlier(dim):
+    """One row's output gradient 2^22 above the others': dk of the keys that it does not see, but for those that
+    share a block of 32 with one that it does, is as exact as without it."""
+    n, left, at = 1500, 40, 700
+    g = gen(47)
+    q, k, v, dout = (randn(g, n, 1, dim, dtype=torch.float16, scale=s) for s in (1.3, 1.3, 1.0, 2.0 ** -9))
+    dout[at] *= 2.0 ** 22
+    on = [x.to(DEV) for x in (q, k, v, dout)]
+    how = dict(left=left, right=0)
+    out, lse = sc.window_attention(*on[:3], return_lse=True, **how)
+    got = sc.window_attention_backward(on[3], *on[:3], out, lse, **how)
+    want = exact_grads(q[:, 0], k[:, 0], v[:, 0], dout[:, 0], R.visible(n, n, left, 0, 0), dim ** -0.5)
+    first, end = (at - left) // 32 * 32, at // 32 * 32 + 32
+    for name, part in (("before", slice(0, first)), ("after", slice(end, None)), ("near", slice(end, end + 64))):
+        ratio = rms_of_roundings(got[1][:, 0], want[1], torch.float16, part)
+        assert ratio < TWICE, (name, ratio)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("spread,left,right,length", [(8.0, 512, 512, 8192), (3.0, 512, 512, 8192), (1.3, 0, 0, 8192),
                                                       (1.3, 512, 0, 32)])
 def test_sharp_attention_keeps_the_usual_path(spread, left, right, length, dim):
