@@ -468,6 +468,89 @@ int tr_sparseconv_window_attention_backward(const tr_sc_heads* dout, const tr_sc
                                             void* workspace, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Paged key-value cache: serving models over voxel tokens. Sequences of unlike
+ * and growing lengths share one pool of pages; a step appends the new tokens'
+ * keys and values to their places and attends over the pages.
+ * ------------------------------------------------------------------------ */
+
+/* The pool and its sequences. Element (page, slot, head, e) of k lies at
+ * page * k_page_stride + slot * k_slot_stride + head * k_head_stride + e, v's
+ * likewise (strides in elements, multiples of 16 bytes; slot strides below
+ * 16 MiB). Key j of sequence b is slot j % page_size of page
+ * table[b * table_stride + j / page_size]; the sequence has len[b] keys, of the
+ * table's table_pages * page_size at most.
+ * k, v         device, pages of the type of the call's tensors.
+ * page_size    a power of two from 8 to 65536.
+ * table, len   device int32, [batch, table_pages] and [batch]. Entries past a
+ *              sequence's length are not read. Lengths are clamped to the table on
+ *              the device by the attention. An entry that is no page of the pool is
+ *              not followed: attention takes its keys and values as zeros, the
+ *              append leaves its tokens out. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t k_page_stride, k_slot_stride, k_head_stride;
+  int64_t v_page_stride, v_slot_stride, v_head_stride;
+  int64_t pages;
+  int page_size;
+  int heads;
+  const int32_t* table;
+  int64_t table_stride;
+  int table_pages;
+  const int32_t* len;
+  int batch;
+} tr_sc_pages;
+
+/* Norm and rotation of new tokens' queries and keys (as qk_norm_rope), the keys
+ * and values to the pages in the same pass.
+ * cu_q     device int32 [batch + 1]: sequence b has the new tokens cu_q[b] ..
+ *          cu_q[b + 1]; NULL: tokens / batch each (which must divide). pages->len
+ *          counts them already: token i of Lq is the sequence's key len - Lq + i.
+ *          One that would be no key of the table (a length below Lq or past the
+ *          table) is not stored, its query is.
+ * norm     0: rotation alone (no gains; eps is not read).
+ * q, k, v  [tokens, q heads, dim], [tokens, kv heads, dim] twice; the values are
+ *          copied bit by bit.
+ * q_out    as q, may be q itself (same strides). Rows of tokens in no sequence are
+ *          left as they are.
+ * q_out must not overlap k, v or the pages, the pages not the inputs, k's pages
+ * not v's (side by side in one tensor is fine). Where the tables give two tokens
+ * the same place, one of them is stored. */
+int tr_sparseconv_qk_norm_rope_append(const tr_sc_heads* q, const tr_sc_heads* k, const tr_sc_heads* v,
+                                      const tr_sc_rotation* rotation, const float* q_gain, int q_gain_rows,
+                                      const float* k_gain, int k_gain_rows, int norm, float eps,
+                                      const tr_sc_heads* q_out, const tr_sc_pages* pages, const int32_t* cu_q,
+                                      int64_t tokens, int dim, int dtype, void* stream);
+
+/* Attention over pages: window_attention with sequence b's keys and values in its
+ * pages. window: batch as the pages', cu_k and k_len NULL; cu_q NULL: tokens_q /
+ * batch rows each. Types, head sizes, rounding, lse, and what holds for keys
+ * that a row does not see are window_attention's. Rows of out and lse that
+ * belong to no sequence are left as they are. out and lse must not overlap q, the
+ * pages or each other. No atomics: the same bits on every call.
+ *
+ * shared_prefix_attention: every sequence's keys are the prefix's prefix_len, in
+ * the pool's pages prefix_pages (device int32 [prefix_len / page_size, rounded
+ * up]), then its own len[b]; the window and the sinks go over both. The
+ * prefix's keys and values are read for the batch, not for every sequence.
+ * prefix_len = 0: the same as paged_window_attention.
+ *
+ * workspace: >= the bytes of the query (which reads no device array; prefix_len 0
+ * for paged_window_attention), 256-byte aligned; 0 bytes: may be NULL. */
+size_t tr_sparseconv_paged_attention_workspace_bytes(const tr_sc_pages* pages, const tr_sc_window* window,
+                                                     int64_t prefix_len, int64_t tokens_q, int q_heads,
+                                                     int dim, int dtype);
+int tr_sparseconv_paged_window_attention(const tr_sc_heads* q, const tr_sc_pages* pages,
+                                         const tr_sc_window* window, const tr_sc_heads* out, float* lse,
+                                         int64_t tokens_q, int dim, int dtype, void* workspace,
+                                         size_t ws_bytes, void* stream);
+int tr_sparseconv_shared_prefix_attention(const tr_sc_heads* q, const tr_sc_pages* pages,
+                                          const int32_t* prefix_pages, int64_t prefix_len,
+                                          const tr_sc_window* window, const tr_sc_heads* out, float* lse,
+                                          int64_t tokens_q, int dim, int dtype, void* workspace,
+                                          size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Measured ceilings (for the benchmark's roofline fractions; they compute
  * nothing of the convolution). Both enqueue one kernel on `stream`.
  * ------------------------------------------------------------------------ */

@@ -9,7 +9,8 @@ library; torch only provides device memory and the current stream.
     y = forward(m, x, w)            # x [N, C_in], w [27, C_in, C_out] -> [N, C_out]
 
 The transformer layers over the same voxels (norm with position rotation, and
-windowed attention) are in tokens.py and exported here.
+windowed attention) are in tokens.py, their serving from a paged cache in
+paged.py; both are exported here.
 """
 from __future__ import annotations
 
@@ -19,6 +20,7 @@ import torch
 
 from . import _lib
 from ._lib import TrSparseConvError, check  # noqa: F401
+from .paged import paged_window_attention, qk_norm_rope_append, shared_prefix_attention  # noqa: F401
 from .tokens import (qk_norm_rope, qk_norm_rope_backward, rope_frequencies, window_attention,  # noqa: F401
                      window_attention_backward)
 
@@ -28,7 +30,7 @@ __all__ = ["build_hash", "build_kernel_map", "forward", "pack_weights", "forward
            "status", "hash_lookup", "hash_sorted_rows", "HashTable", "KernelMap", "PackedWeights",
            "TrSparseConvError", "version", "forward_workspace_bytes", "Workspace", "forward_noalloc",
            "qk_norm_rope", "qk_norm_rope_backward", "rope_frequencies", "window_attention",
-           "window_attention_backward"]
+           "window_attention_backward", "qk_norm_rope_append", "paged_window_attention", "shared_prefix_attention"]
 
 _DTYPES = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16, torch.float16: _lib.F16}
 _ACTS = {"none": _lib.ACT_NONE, "relu": _lib.ACT_RELU, "silu": _lib.ACT_SILU}

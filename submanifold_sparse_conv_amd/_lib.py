@@ -59,7 +59,16 @@ class Window(ctypes.Structure):
                 ("sinks", _I), ("scale", _F)]
 
 
+class Pages(ctypes.Structure):
+    """tr_sc_pages."""
+    _fields_ = [("k", _P), ("v", _P), ("k_page_stride", _I64), ("k_slot_stride", _I64), ("k_head_stride", _I64),
+                ("v_page_stride", _I64), ("v_slot_stride", _I64), ("v_head_stride", _I64), ("pages", _I64),
+                ("page_size", _I), ("heads", _I), ("table", _P), ("table_stride", _I64), ("table_pages", _I),
+                ("len", _P), ("batch", _I)]
+
+
 _H = ctypes.POINTER(Heads)
+_G = ctypes.POINTER(Pages)
 _R = ctypes.POINTER(Rotation)
 _W = ctypes.POINTER(Window)
 SIGNATURES = [
@@ -102,6 +111,11 @@ SIGNATURES = [
     ("tr_sparseconv_window_attention_backward_workspace_bytes", _SZ, [_W, _I64, _I64, _I, _I, _I, _I]),
     ("tr_sparseconv_window_attention_backward", _I,
      [_H, _H, _H, _H, _H, _P, _W, _P, _P, _P, _I64, _I64, _I, _I, _P, _SZ, _P]),
+    ("tr_sparseconv_qk_norm_rope_append", _I,
+     [_H, _H, _H, _R, _P, _I, _P, _I, _I, _F, _H, _G, _P, _I64, _I, _I, _P]),
+    ("tr_sparseconv_paged_attention_workspace_bytes", _SZ, [_G, _W, _I64, _I64, _I, _I, _I]),
+    ("tr_sparseconv_paged_window_attention", _I, [_H, _G, _W, _H, _P, _I64, _I, _I, _P, _SZ, _P]),
+    ("tr_sparseconv_shared_prefix_attention", _I, [_H, _G, _P, _I64, _W, _H, _P, _I64, _I, _I, _P, _SZ, _P]),
     ("tr_sparseconv_ceiling_mfma_flops", _I64, [_I, _I]),
     ("tr_sparseconv_ceiling_mfma", _I, [_P, _I, _I, _P]),
     ("tr_sparseconv_ceiling_copy", _I, [_P, _P, _SZ, _I, _P]),

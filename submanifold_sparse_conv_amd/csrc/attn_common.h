@@ -284,20 +284,24 @@ struct KeyTiles {
   __device__ __forceinline__ int at(int i) const { return i < sink ? i : band + i - sink; }
 };
 template <int KT>
-__device__ __forceinline__ KeyTiles key_tiles(const AttnArgs& a, int p0, int p1, int lk) {
+__device__ __forceinline__ KeyTiles key_tiles(int left, int right, int most_sinks, int p0, int p1, int lk) {
   KeyTiles t;
-  const int hi = min(lk, p1 + a.right + 1);  // positions and sides are within 2^30 each
+  const int hi = min(lk, p1 + right + 1);  // positions and sides are within 2^30 each
   if (hi <= 0) {
     t.sink = t.band = t.n = 0;
     return t;
   }
-  const int lo = max(0, p0 - a.left);
-  const int sinks = min(a.sinks, min(lo, hi));
+  const int lo = max(0, p0 - left);
+  const int sinks = min(most_sinks, min(lo, hi));
   t.sink = (sinks + KT - 1) / KT;
   t.band = max(lo / KT, t.sink);
   const int end = (hi + KT - 1) / KT;
   t.n = t.sink + max(0, end - t.band);
   return t;
+}
+template <int KT>
+__device__ __forceinline__ KeyTiles key_tiles(const AttnArgs& a, int p0, int p1, int lk) {
+  return key_tiles<KT>(a.left, a.right, a.sinks, p0, p1, lk);
 }
 
 // ---------------------------------------------------------------------------

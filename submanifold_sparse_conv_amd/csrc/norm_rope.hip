@@ -34,6 +34,7 @@
 // of it. The same in fp16: 61 us, in fp32: 122.
 // 32 tokens: 4.3 us, one launch.
 #include "common.h"
+#include "rotate.h"
 #include "token_types.h"
 #include "tokens.h"
 
@@ -41,7 +42,7 @@ namespace trsc {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int E = 4;  // elements of either half of a row in a lane
+constexpr int E = kRowElts;
 constexpr int kNormThreads = kWaves * 64;
 
 template <class T>
@@ -68,23 +69,6 @@ __device__ __forceinline__ SidePtrs<T> side_ptrs(const NormArgs& a, int head, in
   p.yts = s.yts;
   p.gain = s.gain ? s.gain + (s.gain_rows > 1 ? h * a.dim : 0) + off : nullptr;
   return p;
-}
-
-// (cos, sin) of this lane's pair at token t into the wave's table.
-__device__ __forceinline__ void turn_table(const NormArgs& a, int32_t p, double freq_turns, bool turns, int lane,
-                                           float2* table) {
-  float2 cs = make_float2(1.f, 0.f);
-  if (turns) {
-    const double t = double(p) * freq_turns;
-    const float f = float(t - rint(t));
-    sincospif(2.f * f, &cs.y, &cs.x);
-  }
-  table[lane] = cs;
-}
-
-__device__ __forceinline__ float group_sum(float v, int group) {
-  for (int o = group >> 1; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
 }
 
 template <class T, bool IL, bool BWD>
@@ -142,7 +126,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_rope_kernel(NormArgs a, int
         u[1][e] = u1.get(e);
       }
     }
-    turn_table(a, pos, freq, turns, lane, s_turn[wave]);
+    turn_table(pos, freq, turns, lane, s_turn[wave]);
     if (t + step < a.tokens) fetch(t + step);
     float ss = 0.f;
 #pragma unroll
@@ -280,13 +264,6 @@ __global__ __launch_bounds__(256) void gain_sum(NormArgs a, int splits) {
     __syncthreads();
   }
   if (slice == 0 && col < cols) *reinterpret_cast<float4*>(s.dgain + col) = v;
-}
-
-int group_lanes(int dim) {
-  const int lanes = dim / (2 * E);
-  int g = 1;
-  while (g < lanes) g <<= 1;
-  return g;
 }
 
 // Workgroups over the tokens: `fill` in all, fewer where a wave would have no
