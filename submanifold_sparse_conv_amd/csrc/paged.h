@@ -59,10 +59,14 @@ struct PagedArgs {
   int32_t left, right, sinks;
   float scale;
 };
+// shorts: a workgroup an item of 32 rows; whole_tiles: of 128; tokens, tiles: the items' units dealt to the chip's waves
+// or workgroups; mixed: the prefix's to workgroups, the others to waves.
+enum class PagedForm { shorts, whole_tiles, tokens, tiles, mixed };
 struct PagedPlan {
-  bool token_form, prefix_token_form;  // 32 rows a workgroup whose waves share them, or 128
-  int splits, prefix_splits;           // parts of the key axis in different workgroups
-  size_t part_floats;
+  PagedForm form;
+  int grid;
+  size_t part_floats;  // of the workspace
+  bool fits;           // the work list's numbers
 };
 PagedPlan plan_paged_attention(const PagedArgs& a);
 hipError_t launch_paged_attention(const PagedArgs& a, const PagedPlan& plan, hipStream_t st);

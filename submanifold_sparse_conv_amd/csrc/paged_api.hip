@@ -103,9 +103,11 @@ int fill_pool(const char* who, const tr_sc_pages* p, int heads, int dim, int dty
     }
     if (!aligned)
       return fail(TR_SC_ERR_INVALID_ARG, "%s: the pages must be 16-byte aligned in pointers and strides", who);
-    // a tile's rows of a page lie within 32-bit offsets of its first
-    if (ks[1] * b >= (int64_t(1) << 24) || vs[1] * b >= (int64_t(1) << 24))
-      return fail(TR_SC_ERR_UNSUPPORTED, "%s: slot strides too large", who);
+    // rows of a page within 32-bit offsets, in units of 16 bytes; those of a copy to LDS in bytes
+    const int64_t most = int64_t(1) << 24;
+    if (ks[1] * b >= most || vs[1] * b >= most || ks[1] * b * p->page_size >= (most << 12) ||
+        vs[1] * b * p->page_size >= (most << 12) || ks[0] * b >= (most << 12) || vs[0] * b >= (most << 12))
+      return fail(TR_SC_ERR_UNSUPPORTED, "%s: slot or page strides too large", who);
   }
   *r = PoolRef{p->k, p->v, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], int32_t(p->pages), log2, p->table, p->table_stride,
                p->pages > 0 ? p->table_pages : 0, p->len};
@@ -182,6 +184,7 @@ int attend(const char* who, const tr_sc_heads* q, const tr_sc_pages* pages, cons
   if (c == TR_SC_OK) c = check_heads(who, "out", out, nq, q->heads, dim, dtype, true);
   if (c != TR_SC_OK) return c;
   const PagedPlan plan = plan_paged_attention(a);
+  if (!plan.fits) return fail(TR_SC_ERR_UNSUPPORTED, "%s: too many rows and keys", who);
   c = check_workspace(who, workspace, ws_bytes, align_up(plan.part_floats * 4, 256));
   if (c != TR_SC_OK) return c;
   const View ins[] = {view_of("q", q, nq, dim, dtype)};

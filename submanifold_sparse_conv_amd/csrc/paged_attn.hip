@@ -8,14 +8,26 @@
 // o = sum_s 2^{l_s - l} o_s, l = log2 sum_s 2^{l_s}.
 //
 // Rows. A sequence's own keys: row r is its token r / G, head r % G of the
-// group, tiles of 128 rows (32 a wave) or, for few rows, 32 that the four waves
-// share. The prefix: the rows of all sequences are one matrix, so its keys are
-// read once for 128 rows, whatever sequence they belong to; each row has its own
-// position. A query that is i-th of Lq stands at i + P + Lk - Lq.
+// group, in tiles of 32 (few rows: one wave holds them) or 128 rows (four waves
+// that share the key tiles). The prefix: the rows of all sequences are one
+// matrix, so its keys are read once for a tile, whatever sequence its rows
+// belong to; each row has its own position. A query that is i-th of Lq stands at
+// i + P + Lk - Lq.
+//
+// Work. An item is a row tile with all key tiles that it sees; a unit is one of
+// those. The units of all items in a row are dealt out evenly, each wave (32
+// rows) or workgroup (128) taking one contiguous run of them for one kv head:
+// lengths differ and only the device knows them, so every workgroup sums them up
+// (one read of the lengths) and finds its run. An item that two runs share leaves
+// parts in the workspace that the join adds up in order. The heads' runs are cut
+// at the same places and lie in neighbouring waves, which so read neighbouring
+// memory at the same time.
 //
 // Pages. A copy to LDS of a wave takes 2 to 8 rows, which lie in one page: a
 // page holds a multiple of 8. The pages of a tile's rows are read a tile ahead,
 // one a lane, and taken from there as scalars.
+#include <type_traits>
+
 #include "attn_rows.h"
 #include "paged.h"
 
@@ -29,46 +41,70 @@ struct Keys {
   int sinks;  // of them
 };
 
+// A value that all lanes hold alike, in a scalar register. What comes from a division, a load or a 64-bit comparison is
+// in vector registers otherwise, and with it all that is computed from it, down to the copies' descriptors, which then
+// cost a loop over the lanes each.
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Copies rows [0, ROWS) of a tile of keys from their pages to LDS: this wave's copies first, first + STEP, ... of 64
+// lanes x 16 bytes. Offsets in the pool are taken in units of 16 bytes, 32 bits a factor.
 template <class E, int NB, int ROWS, int STEP>
 struct PagedCopy {
   typedef Tile<E, NB> T;
   static constexpr int kRows = T::kRowsPerCopy, kCopies = ROWS / kRows, kN = (kCopies + STEP - 1) / STEP;
-  uint32_t off[kN], row_bytes;
+  uint32_t off[kN], page16, slot16, full;
   int first;
-  __device__ __forceinline__ void start(int64_t stride, int dim, int first_, int lane) {
+  __device__ __forceinline__ void start(int64_t page_stride, int64_t stride, int dim, int first_, int lane) {
     first = first_;
-    row_bytes = uint32_t(dim * T::kElt);
+    page16 = uni(uint32_t(page_stride / T::kPer));
+    slot16 = uni(uint32_t(stride / T::kPer));
+    full = uint32_t(kRows - 1) * slot16 * 16 + uint32_t(dim * T::kElt);
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
       const int row = lane / T::kChunks;  // of the copy
       const int chunk = (lane % T::kChunks) ^ T::key((first + j * STEP) * kRows + row);
-      off[j] = chunk * T::kPer < dim ? uint32_t(row) * uint32_t(stride * T::kElt) + chunk * 16 : 0x80000000u;
+      off[j] = chunk * T::kPer < dim ? uint32_t(row) * slot16 * 16 + chunk * 16 : 0x80000000u;
     }
   }
-  // base: the head's first element in the pool; ids: page of row l of the tile in lane l, -1 for none; slot: the
-  // first row's slot in its page; left: rows from the tile's first to the last key's. Rows without a page and past
-  // the end read as zero.
-  __device__ __forceinline__ void run(unsigned char* lds, const E* base, int64_t ps, int64_t ss, int ids, int page_mask,
-                                      int t0, int left) const {
+  // base: the head's first element in the pool; ids: page of row l of the tile in lane l, -1 for none; t0: the tile's
+  // first key, left: keys from there on. Rows without a page and past the end read as zero.
+  __device__ __forceinline__ void run(unsigned char* lds, const E* base, int ids, int page_mask, int t0, int left) const {
+    const uint64_t at = reinterpret_cast<uint64_t>(base);
+    const uint64_t from = (uint64_t(uint32_t(uni(int(at >> 32)))) << 32) | uint32_t(uni(int(at)));
+    page_mask = uni(page_mask);
+    t0 = uni(t0);
+    left = uni(left);
+    if (left >= ROWS)
+      copies<true>(lds, from, ids, page_mask, t0, left);
+    else
+      copies<false>(lds, from, ids, page_mask, t0, left);
+  }
+  template <bool WHOLE>
+  __device__ __forceinline__ void copies(unsigned char* lds, uint64_t base, int ids, int page_mask, int t0, int left) const {
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
       const int copy = first + j * STEP;
       if (!((j + 1) * STEP <= kCopies || copy < kCopies)) continue;
       const int row = copy * kRows;
       const int page = __builtin_amdgcn_readlane(ids, row);
-      const int n = left - row > kRows ? kRows : left - row;
-      const uint32_t bytes = page < 0 || n <= 0 ? 0u : uint32_t(n - 1) * uint32_t(ss * T::kElt) + row_bytes;
-      const E* from = base + (page < 0 ? 0 : page) * ps + ((t0 + row) & page_mask) * ss;
-      copy_lds16(buffer_of(from, bytes), off[j], lds + copy * 1024);
+      uint32_t bytes = full;
+      if constexpr (!WHOLE) bytes = full - uint32_t(kRows - clamp_to(left - row, 1, kRows)) * slot16 * 16;
+      bytes = page < 0 ? 0u : bytes;  // a row past the end has no page
+      const uint64_t at = uint64_t(uint32_t(page < 0 ? 0 : page)) * page16 + uint32_t((t0 + row) & page_mask) * slot16;
+      copy_lds16(buffer_of(reinterpret_cast<const void*>(base + (at << 4)), bytes), off[j], lds + copy * 1024);
     }
   }
 };
 
-// The page of key j, -1 where there is none.
-__device__ __forceinline__ int page_of(const PagedArgs& a, const Keys& keys, int j) {
-  if (j >= keys.n) return -1;
-  const int page = keys.table[j >> a.pool.log2];
-  return page >= 0 && page < a.pool.pages ? page : -1;
+// The table's entry for key j, -1 past the last; and whether it is a page of the pool. Apart, since the comparison
+// waits for the entry and with it for the copies in flight.
+__device__ __forceinline__ int entry_of(const PagedArgs& a, const Keys& keys, int j) {
+  int page = -1;
+  if (j < keys.n) page = keys.table[j >> a.pool.log2];
+  return page;
+}
+__device__ __forceinline__ int checked(const PagedArgs& a, int page) {
+  return uint32_t(page) < uint32_t(a.pool.pages) ? page : -1;
 }
 
 // The sequence of token t: the last that starts at or before it. One load per lane and level.
@@ -103,7 +139,7 @@ __device__ __forceinline__ OwnSeq paged_sequence(const PagedArgs& a, int b) {
 
 // The rows of a wave, lanes l and l + 32 row l. Positions are those of the run of keys.
 struct Rows {
-  bool any, on;
+  int any, on;  // truth values
   int tok, head;
   int lo, hi;  // keys that the lane's row sees: [lo, hi], and the sinks up to hi
   int p0, p1;  // least and largest position of the wave's rows
@@ -122,8 +158,8 @@ __device__ __forceinline__ Rows own_rows(const PagedArgs& a, const OwnSeq& s, co
   r.tok = s.q0 + i;
   r.head = kvh * group + (r.on ? row - i * group : 0);
   see(a, keys, i + shift, r);
-  r.p0 = min(first, rows - 1) / group + shift;
-  r.p1 = min(first + 31, rows - 1) / group + shift;
+  r.p0 = uni(min(first, rows - 1) / group + shift);
+  r.p1 = uni(min(first + 31, rows - 1) / group + shift);
   return r;
 }
 // Rows first .. first + 31 of all sequences against the prefix.
@@ -138,16 +174,17 @@ __device__ __forceinline__ Rows prefix_rows(const PagedArgs& a, const Keys& keys
     const OwnSeq s = paged_sequence(a, r.tok / a.seqs.each);
     p = r.tok - s.q0 + s.lk - s.lq;
   } else {
-    // tokens of the wave's rows in order, a sequence at a time
-    int b = sequence_of(a.seqs, __builtin_amdgcn_readfirstlane(r.tok));
+    // a sequence at a time: that of the first row which has none yet
     bool found = false;
-    for (; b < a.seqs.batch; ++b) {
-      const OwnSeq s = paged_sequence(a, b);
-      if (!found && r.tok >= s.q0 && r.tok < s.q0 + s.lq) {
+    uint64_t open = __ballot(r.on);
+    while (open != 0) {
+      const int first_open = __ffsll(static_cast<unsigned long long>(open)) - 1;
+      const OwnSeq s = paged_sequence(a, sequence_of(a.seqs, __builtin_amdgcn_readlane(r.tok, first_open)));
+      if (r.on && !found && r.tok >= s.q0 && r.tok < s.q0 + s.lq) {
         found = true;
         p = r.tok - s.q0 + s.lk - s.lq;
       }
-      if (!__any(r.on && !found && r.tok >= s.q0 + s.lq)) break;
+      open &= ~(1ull << first_open) & ~__ballot(found);
     }
     r.on = r.on && found;
   }
@@ -171,17 +208,37 @@ __device__ __forceinline__ bool tile_whole(const PagedArgs& a, const Keys& keys,
   return j1 <= r.p0 + a.right && j1 < keys.n && (j0 >= r.p1 - a.left || j1 < keys.sinks);
 }
 
-// A lane's row: blocks first .. first + count of 32 columns, and the statistic if `with_sum`, to the output or, of a
-// part of the keys, to slot `slot` of `parts`.
+// Where the parts of a call lie (bytes from the workspace's start).
+struct PartMap {
+  int64_t head, table, whole[2], slots[2];  // [0]: the sequences' own keys, [1]: the prefix
+  int rows[2];                              // rows of a slot
+  int64_t slot_count[2];
+};
+// A run of the work list in the workspace: T units in W runs. [0]: own, [1]: prefix (the same list where one kind of
+// worker takes both; own units then follow the prefix's `before`).
+struct Lists {
+  int32_t units[2], runs[2];
+  int32_t pre_n;  // units of an item of the prefix
+};
+struct Entry {  // of the table: a row tile's first unit and its units
+  int32_t first, n;
+};
+
+// Where a lane puts its row: `out`, or a part of `rows` rows with the statistics behind the elements.
+struct Target {
+  float* part;
+  int64_t row, rows;
+};
+
+// A lane's row: blocks first .. first + count of 32 columns, and the statistic if `with_sum`.
 template <class E, int NB>
-__device__ __forceinline__ void store_row(const PagedArgs& a, int parts, int slot, const Rows& r, const f32x16 (&acc)[NB],
+__device__ __forceinline__ void store_row(const PagedArgs& a, const Target& to, const Rows& r, const f32x16 (&acc)[NB],
                                           float mc, float l, int first, int count, bool with_sum, int h) {
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const float lg = l == 0.f ? -INFINITY : mc + __builtin_amdgcn_logf(l);  // base 2
-  const int64_t n = int64_t(a.hq) * a.nq, at_row = slot * n + int64_t(r.head) * a.nq + r.tok;
   typedef E out4 __attribute__((ext_vector_type(4)));
   E* const op = static_cast<E*>(const_cast<void*>(a.o.p)) + r.tok * a.o.ts + r.head * a.o.hs;
-  float* const pp = a.part + at_row * a.dim;
+  float* const pp = to.part + to.row * a.dim;
 #pragma unroll
   for (int d = 0; d < NB; ++d) {
     if (d >= count) break;
@@ -189,7 +246,7 @@ __device__ __forceinline__ void store_row(const PagedArgs& a, int parts, int slo
     for (int g = 0; g < 4; ++g) {
       const int col = 32 * (first + d) + 8 * g + 4 * h;
       if (col >= a.dim) continue;
-      if (parts == 1) {
+      if (to.part == nullptr) {
         out4 v;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = static_cast<E>(acc[d][4 * g + i] * inv);
@@ -201,8 +258,8 @@ __device__ __forceinline__ void store_row(const PagedArgs& a, int parts, int slo
     }
   }
   if (!with_sum) return;
-  if (parts > 1)
-    a.part[parts * n * a.dim + at_row] = lg;
+  if (to.part != nullptr)
+    to.part[to.rows * a.dim + to.row] = lg;
   else if (a.lse != nullptr)
     a.lse[int64_t(r.head) * a.nq + r.tok] = lg * 0.6931471805599453f;
 }
@@ -230,7 +287,7 @@ __device__ void safe_rows(const PagedArgs& a, const Keys& keys, const KeyTiles& 
   for (int it = first * (KT / 32); it < end * (KT / 32); ++it) {
     const int j0 = kt.at(it / (KT / 32)) * KT + it % (KT / 32) * 32;
     if (!tile_seen(a, keys, r, j0, j0 + 31)) continue;
-    const int mine = j0 + (lane & 31), page = page_of(a, keys, mine);
+    const int mine = j0 + (lane & 31), page = checked(a, entry_of(a, keys, mine));
     f32x16 s = scores_from<E, ST>(kbase + max(page, 0) * a.pool.kps + (mine & mask) * a.pool.kss, page >= 0, qf, a.dim,
                                   lane);
     hide(s, j0, r.lo, r.hi, keys.sinks, lane);
@@ -284,289 +341,802 @@ struct PagedShape {  // as the contiguous kernels' (attn_fwd.hip)
   static constexpr int kRows = TOKEN ? 32 : 128;
 };
 
-// Workgroups of one run of keys: tiles row tiles by kv heads by splits; slot0, parts: the first split's slot, and
-// slots in all.
-template <class E, int NB, bool TOKEN, bool PREFIX>
-__global__ __launch_bounds__(256, TOKEN || sizeof(E) == 4 ? 1 : NB <= 2 ? 4 : 2) void paged_attn(PagedArgs a, int tiles,
-                                                                                                int splits, int slot0,
-                                                                                                int parts) {
-  typedef PagedShape<E, NB, TOKEN> F;
+// ---------------------------------------------------------------------------
+// The work list: first the prefix's items, row tile by row tile, then the
+// sequences'.
+// ---------------------------------------------------------------------------
+struct List {
+  int pre_units, units;  // the prefix's; all (below 2^31, checked by the caller)
+  int pre_tiles;         // row tiles of the prefix in this list
+  KeyTiles pre;          // its key tiles, of all rows together
+};
+// No member smaller than 32 bits: the compiler puts the copied padding into LDS, and finds its place there by a read of
+// the dispatch packet in host memory, 8 us of the kernel's time.
+struct Item {
+  int prefix;     // truth value
+  int b, inside;  // sequence; row tile (of the prefix: of all rows)
+  OwnSeq s;
+  Keys keys;
+  KeyTiles kt;
+  int n;  // units: an item without keys has one, which writes its zeros
+};
+__device__ __forceinline__ OwnSeq uniform_sequence(const PagedArgs& a, int b) {
+  const OwnSeq s = paged_sequence(a, b);
+  return OwnSeq{uni(s.q0), uni(s.lq), uni(s.lk)};
+}
+// Row tile `inside` of a sequence.
+template <int R, int KT>
+__device__ __forceinline__ void own_tile(const PagedArgs& a, int b, const OwnSeq& s, int inside, Item& it) {
+  const int group = a.hq / a.hk, rows = s.lq * group, r0 = inside * R, shift = s.lk - s.lq;
+  it.prefix = false;
+  it.b = b;
+  it.inside = inside;
+  it.s = s;
+  it.keys = Keys{a.pool.table + b * a.pool.table_ts, s.lk, max(0, a.sinks - a.prefix_len)};
+  it.kt = key_tiles<KT>(a.left, a.right, it.keys.sinks, r0 / group + shift, min(rows - 1, r0 + R - 1) / group + shift,
+                        s.lk);
+  it.n = max(it.kt.n, 1);
+}
+template <int R>
+__device__ __forceinline__ int row_tiles(const PagedArgs& a, const OwnSeq& s) {
+  return (s.lq * (a.hq / a.hk) + R - 1) / R;
+}
+template <int R>  // number of a sequence's first row tile in the table (find_sequence)
+__device__ __forceinline__ int first_entry(const PagedArgs& a, int b, const OwnSeq& s) {
+  const int group = a.hq / a.hk;
+  return a.seqs.cu == nullptr ? b * ((a.seqs.each * group + R - 1) / R) : s.q0 * group / R + b;
+}
+
+// Sums up the list: every workgroup for itself, 256 threads. cum: kCum ints of LDS, the first 257 the sums of the
+// threads' sequences' units. (Part of the kernel's one LDS array: with others beside it the compiler has every read of
+// a tile wait for the next tile's copies: 32 caches of up to 4100 keys, 72 us for 67.) The
+// prefix's positions are those of all sequences: what a tile of its rows does not see costs no products.
+constexpr int kCum = 272;
+template <int R, int KT, int PR, int PKT>
+__device__ __forceinline__ List sum_up(const PagedArgs& a, bool with_prefix, int* cum, Entry* table) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int per = (a.seqs.batch + 255) / 256;
+  int mine = 0;
+  int p0 = 0x7fffffff, p1 = -0x7fffffff;
+  for (int b = tid * per; b < min(a.seqs.batch, (tid + 1) * per); ++b) {
+    const OwnSeq s = paged_sequence(a, b);
+    const int tiles = row_tiles<R>(a, s);
+    for (int i = 0; i < tiles; ++i) {
+      Item it;
+      own_tile<R, KT>(a, b, s, i, it);
+      mine += it.n;
+    }
+    if (tiles > 0) {
+      p0 = min(p0, s.lk - s.lq + a.prefix_len);
+      p1 = max(p1, s.lk - 1 + a.prefix_len);
+    }
+  }
+  int sum = mine;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int x = __shfl_up(sum, o);
+    if (lane >= o) sum += x;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    p0 = min(p0, __shfl_xor(p0, o));
+    p1 = max(p1, __shfl_xor(p1, o));
+  }
+  int *const s_sum = cum + 257, *const s_p = cum + 261;
+  if (lane == 63) s_sum[wave] = sum;
+  if (lane == 0) s_p[wave] = p0, s_p[4 + wave] = p1;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) sum += s_sum[w];
+  cum[tid + 1] = sum;
+  if (tid == 0) cum[0] = 0;
+  List l{};
+  if (a.prefix_len > 0) {
+    p0 = min(min(s_p[0], s_p[1]), min(s_p[2], s_p[3]));
+    p1 = max(max(s_p[4], s_p[5]), max(s_p[6], s_p[7]));
+    l.pre = key_tiles<PKT>(a.left, a.right, min(a.sinks, a.prefix_len), p0, p1, a.prefix_len);
+    if (with_prefix) {
+      l.pre_tiles = uni((a.nq * (a.hq / a.hk) + PR - 1) / PR);
+      l.pre_units = l.pre_tiles * max(l.pre.n, 1);
+    }
+  }
+  l.units = l.pre_units + s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+  if (table != nullptr) {
+    int at = l.pre_units + sum - mine;
+    for (int b = tid * per; b < min(a.seqs.batch, (tid + 1) * per); ++b) {
+      const OwnSeq s = paged_sequence(a, b);
+      const int tiles = row_tiles<R>(a, s), first = first_entry<R>(a, b, s);
+      for (int i = 0; i < tiles; ++i) {
+        Item it;
+        own_tile<R, KT>(a, b, s, i, it);
+        table[first + i] = Entry{at, it.n};
+        at += it.n;
+      }
+    }
+  }
+  __syncthreads();
+  l.pre_units = uni(l.pre_units);
+  l.units = uni(l.units);
+  l.pre = KeyTiles{uni(l.pre.sink), uni(l.pre.band), uni(l.pre.n)};
+  return l;
+}
+
+__device__ __forceinline__ int run_start(int units, int runs, int w) { return uni(int(int64_t(units) * w / runs)); }
+__device__ __forceinline__ int owner(int units, int runs, int u) { return int(((int64_t(u) + 1) * runs - 1) / units); }
+
+__device__ __forceinline__ void prefix_item(const PagedArgs& a, const List& l, int tile, Item& it) {
+  it.prefix = true;
+  it.inside = tile;
+  it.keys = Keys{a.prefix, a.prefix_len, min(a.sinks, a.prefix_len)};
+  it.kt = l.pre;
+  it.n = max(l.pre.n, 1);
+}
+__device__ __forceinline__ void to_scalars(const PagedArgs& a, Item& it) {
+  it.b = uni(it.b);
+  it.inside = uni(it.inside);
+  it.s = OwnSeq{uni(it.s.q0), uni(it.s.lq), uni(it.s.lk)};
+  it.prefix = uni(it.prefix);
+  it.keys = Keys{it.prefix ? a.prefix : a.pool.table + it.b * a.pool.table_ts, uni(it.keys.n), uni(it.keys.sinks)};
+  it.kt = KeyTiles{uni(it.kt.sink), uni(it.kt.band), uni(it.kt.n)};
+  it.n = uni(it.n);
+}
+// The item of unit u, and the unit's number in it.
+template <int R, int KT>
+__device__ __forceinline__ int locate(const PagedArgs& a, const List& l, const int* cum, int u, Item& it) {
+  if (u < l.pre_units) {
+    const int n = max(l.pre.n, 1), item = uni(u / n);
+    prefix_item(a, l, item, it);
+    it.b = 0;
+    it.s = OwnSeq{0, 0, 0};
+    return u - item * n;
+  }
+  u -= l.pre_units;
+  const int lane = threadIdx.x & 63;
+  int t = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) t += __popcll(__ballot(cum[64 * q + lane] <= u));
+  t = uni(t) - 1;
+  u -= uni(cum[t]);
+  const int per = uni((a.seqs.batch + 255) / 256), last = min(a.seqs.batch, (t + 1) * per);
+  for (int b = t * per; b < last; ++b) {  // u is less than this thread's sequences' units
+    const OwnSeq s = uniform_sequence(a, b);
+    const int tiles = uni(row_tiles<R>(a, s));
+    for (int i = 0; i < tiles; ++i) {
+      own_tile<R, KT>(a, b, s, i, it);
+      const int n = uni(it.n);
+      if (u < n) {
+        to_scalars(a, it);
+        return u;
+      }
+      u -= n;
+    }
+  }
+  it.n = 0;
+  return 0;
+}
+// The item after `it`, whose first unit is u.
+template <int R, int KT>
+__device__ __forceinline__ void advance(const PagedArgs& a, const List& l, const int* cum, int u, Item& it) {
+  if (it.prefix && it.inside + 1 < l.pre_tiles) {
+    ++it.inside;
+  } else if (!it.prefix && it.inside + 1 < uni(row_tiles<R>(a, it.s))) {
+    own_tile<R, KT>(a, it.b, it.s, it.inside + 1, it);
+    to_scalars(a, it);
+  } else {
+    locate<R, KT>(a, l, cum, u, it);
+  }
+}
+
+// The target of a lane's row after units [t0, t1) of an item by run w of kv head kvh.
+__device__ __forceinline__ Target target_of(const PagedArgs& a, const PartMap& m, const Item& it, const Rows& r, int w, int kvh,
+                                            int t0, int t1, int row_in_tile) {
+  Target t{nullptr, 0, 0};
+  char* const ws = reinterpret_cast<char*>(a.part);
+  const int kind = it.prefix;
+  if (t0 == 0 && t1 == it.n) {
+    if (a.prefix_len == 0) return t;
+    t.part = reinterpret_cast<float*>(ws + (kind ? m.whole[1] : m.whole[0]));
+    t.row = int64_t(r.head) * a.nq + r.tok;
+    t.rows = int64_t(a.hq) * a.nq;
+  } else {  // an item that goes on in the next run: its second slot
+    const int rows = kind ? m.rows[1] : m.rows[0];
+    t.part = reinterpret_cast<float*>(ws + (kind ? m.slots[1] : m.slots[0]));
+    t.row = ((int64_t(w) * a.hk + kvh) * 2 + (t0 == 0)) * rows + row_in_tile;
+    t.rows = (kind ? m.slot_count[1] : m.slot_count[0]) * rows;
+  }
+  return t;
+}
+
+template <class E, int NB, int KEYS, int KB>
+__device__ __forceinline__ void compute_tile(const PagedArgs& a, const Keys& keys, const KeyTiles& kt, const Rows& r,
+                                             RowState<E, NB, KB>& st, const unsigned char* ks, int it, float c,
+                                             const typename Tile<E, NB>::Lane& at, int lane) {
+  typedef Tile<E, NB> T;
+#pragma unroll
+  for (int part = 0; part < KEYS / (32 * KB); ++part) {
+    const int j0 = kt.at(it) * KEYS + part * 32 * KB, j1 = j0 + 32 * KB - 1;
+    if (!tile_seen(a, keys, r, j0, j1)) continue;
+    st.scores(ks + part * 32 * KB * T::kPitch, (a.dim + 15) / 16, at);
+    if (!tile_whole(a, keys, r, j0, j1)) {
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) hide(st.s[kb], j0 + 32 * kb, r.lo, r.hi, keys.sinks, lane);
+    }
+    st.weigh(c);
+    st.multiply(ks + KEYS * T::kPitch + part * 32 * KB * T::kPitch, at);
+  }
+}
+
+// The arguments of a kernel that takes StreamArgs alone, read again where they are used: held in scalar registers from
+// the kernel's start on they crowd out what the loops need (200 spills a kernel).
+struct StreamArgs {
+  PagedArgs a;
+  PartMap m;
+};
+__device__ __forceinline__ const StreamArgs& arguments() {
+  typedef __attribute__((address_space(4))) const StreamArgs* Ptr;
+  Ptr p = (Ptr)(__builtin_amdgcn_kernarg_segment_ptr());
+  asm volatile("" : "+s"(p));
+  return *(const StreamArgs*)(p);
+}
+
+// Run w of the list for one kv head, one wave: items of 32 rows, the next tile always on its way to LDS, over items' borders too.
+template <class E, int NB>
+__device__ __forceinline__ void token_run(const List& l, const int* cum, int kvh, int w, int runs, unsigned char* mem) {
+  typedef PagedShape<E, NB, true> F;
+  typedef Tile<E, NB> T;
+  constexpr int KB = 1;
+  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+  int u = run_start(l.units, runs, w);
+  const int u_end = run_start(l.units, runs, w + 1);
+  if (u >= u_end) return;
+  const typename T::Lane at = T::lane_of(lane);
+  PagedCopy<E, NB, F::kKeys, 1> kc, vc;
+  Item item;
+  int t, buf = 0, ids;
+  auto pages = [&](const PagedArgs& a, const Item& i, int tile) {
+    return tile < i.kt.n && lane < F::kKeys ? entry_of(a, i.keys, i.kt.at(tile) * F::kKeys + lane) : -1;
+  };
+  auto fetch = [&](const PagedArgs& a, const Item& i, int tile, int to, int of) {
+    if (tile >= i.kt.n) return;
+    const int t0 = i.kt.at(tile) * F::kKeys, mask = (1 << a.pool.log2) - 1;
+    unsigned char* dst = mem + to * 2 * F::kTileBytes;
+    of = checked(a, of);
+    kc.run(dst, static_cast<const E*>(a.pool.k) + kvh * a.pool.khs, of, mask, t0, i.keys.n - t0);
+    vc.run(dst + F::kTileBytes, static_cast<const E*>(a.pool.v) + kvh * a.pool.vhs, of, mask, t0, i.keys.n - t0);
+  };
+  {
+    const PagedArgs& a = arguments().a;
+    kc.start(a.pool.kps, a.pool.kss, a.dim, 0, lane);
+    vc.start(a.pool.vps, a.pool.vss, a.dim, 0, lane);
+    t = locate<F::kRows, F::kKeys>(a, l, cum, u, item);
+    to_scalars(a, item);
+    ids = pages(a, item, t);
+  }
+  RowState<E, NB, KB> st;
+  bool fetched = false;
+  while (u < u_end && item.n > 0) {
+    const int t0 = uni(t), t1 = uni(min(item.n, t + (u_end - u)));
+    u += t1 - t0;
+    Rows r;
+    {
+      const PagedArgs& a = arguments().a;
+      r = item.prefix ? prefix_rows(a, item.keys, item.inside * F::kRows, kvh, l32)
+                      : own_rows(a, item.s, item.keys, item.inside * F::kRows, kvh, l32);
+      st.start(static_cast<const E*>(a.q.p) + r.tok * a.q.ts + r.head * a.q.hs, r.on, a.dim, lane);
+    }
+    {
+      const PagedArgs& a = arguments().a;
+      const float c = a.scale * kLog2e;
+      if (F::kBuffers == 2 && !fetched) {  // the run's first tile, behind the queries
+        fetch(a, item, t, 0, ids);
+        ids = pages(a, item, t + 1);
+        fetched = true;
+      }
+      for (t = t0; t < t1; ++t) {
+        if constexpr (F::kBuffers == 2) {
+          __builtin_amdgcn_s_waitcnt(0);
+          asm volatile("" ::: "memory");
+          if (t + 1 < t1) {
+            fetch(a, item, t + 1, buf ^ 1, ids);
+            ids = pages(a, item, t + 2);
+          }
+          if (t + 1 == t1) break;  // the last tile: below, behind the next item's first
+          if (t < item.kt.n)
+            compute_tile<E, NB, F::kKeys, KB>(a, item.keys, item.kt, r, st, mem + buf * 2 * F::kTileBytes, t, c, at, lane);
+          buf ^= 1;
+        } else {
+          __builtin_amdgcn_s_waitcnt(0);  // the last tile's reads are done
+          fetch(a, item, t, 0, ids);
+          ids = pages(a, item, t + 1);
+          __builtin_amdgcn_s_waitcnt(0);
+          asm volatile("" ::: "memory");
+          if (t < item.kt.n) compute_tile<E, NB, F::kKeys, KB>(a, item.keys, item.kt, r, st, mem, t, c, at, lane);
+        }
+      }
+    }
+    Item next = item;
+    if (u < u_end) {
+      const PagedArgs& a = arguments().a;
+      advance<F::kRows, F::kKeys>(a, l, cum, u, next);
+      to_scalars(a, next);
+      ids = pages(a, next, 0);
+      if constexpr (F::kBuffers == 2) {
+        fetch(a, next, 0, buf ^ 1, ids);
+        ids = pages(a, next, 1);
+      }
+    }
+    const StreamArgs& sa = arguments();
+    const PagedArgs& a = sa.a;
+    if constexpr (F::kBuffers == 2) {
+      if (t < item.kt.n)
+        compute_tile<E, NB, F::kKeys, KB>(a, item.keys, item.kt, r, st, mem + buf * 2 * F::kTileBytes, t,
+                                          a.scale * kLog2e, at, lane);
+      buf ^= 1;
+    }
+    st.join_halves();
+    const Target to = target_of(a, sa.m, item, r, w, kvh, t0, t1, l32);
+    const uint32_t bad = bad_rows(r.on ? zero_if_finite<NB>(st.acc) : 0.f);
+    const bool mine = (bad >> l32) & 1u;
+    if (r.on && !mine) store_row<E, NB>(a, to, r, st.acc, st.mc, st.l, 0, NB, h == 0, h);
+    if (bad != 0) {  // again without what the rows do not see; the tile just used is free
+      float* const lds = reinterpret_cast<float*>(mem + (F::kBuffers == 2 ? buf ^ 1 : 0) * 2 * F::kTileBytes);
+      safe_rows<E, NB, F::kKeys, NB>(a, item.keys, item.kt, t0, min(t1, item.kt.n), r, kvh, 0, lds, lane, st.acc,
+                                     st.mc, st.l);
+      if (r.on && mine) store_row<E, NB>(a, to, r, st.acc, st.mc, st.l, 0, NB, h == 0, h);
+    }
+    item = next;
+    t = 0;
+  }
+}
+
+// Units u .. u_end of the list by one workgroup, from unit t of `item` on: items of 128 rows, 32 a wave. WHOLE: one
+// item, straight to out.
+template <class E, int NB, bool WHOLE>
+__device__ __forceinline__ void tile_run(const List& l, const int* cum, int kvh, Item item, int t, int u, int u_end,
+                                         int w, unsigned char* mem) {
+  typedef PagedShape<E, NB, false> F;
   typedef Tile<E, NB> T;
   constexpr int KB = NB <= 2 ? 1 : F::kKeys / 32;
+  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const typename T::Lane at = T::lane_of(lane);
+  PagedCopy<E, NB, F::kKeys, 4> kc, vc;
+  {
+    const PagedArgs& a = arguments().a;
+    kc.start(a.pool.kps, a.pool.kss, a.dim, wave, lane);
+    vc.start(a.pool.vps, a.pool.vss, a.dim, wave, lane);
+  }
+  RowState<E, NB, KB> st;
+  while (u < u_end && item.n > 0) {
+    const int t0 = uni(t), t1 = uni(min(item.n, t + (u_end - u))), end = min(t1, item.kt.n);
+    u += t1 - t0;
+    Rows r;
+    {
+      const PagedArgs& a = arguments().a;
+      r = item.prefix ? prefix_rows(a, item.keys, item.inside * F::kRows + 32 * wave, kvh, l32)
+                      : own_rows(a, item.s, item.keys, item.inside * F::kRows + 32 * wave, kvh, l32);
+      st.start(static_cast<const E*>(a.q.p) + r.tok * a.q.ts + r.head * a.q.hs, r.on, a.dim, lane);
+    }
+    {
+      const PagedArgs& a = arguments().a;
+      const E* kbase = static_cast<const E*>(a.pool.k) + kvh * a.pool.khs;
+      const E* vbase = static_cast<const E*>(a.pool.v) + kvh * a.pool.vhs;
+      const float c = a.scale * kLog2e;
+      const int mask = (1 << a.pool.log2) - 1;
+      auto pages = [&](int i) {
+        return i < end && lane < F::kKeys ? entry_of(a, item.keys, item.kt.at(i) * F::kKeys + lane) : -1;
+      };
+      auto fetch = [&](int i, int buf, int ids) {
+        const int j0 = item.kt.at(i) * F::kKeys;
+        unsigned char* dst = mem + buf * 2 * F::kTileBytes;
+        ids = checked(a, ids);
+        kc.run(dst, kbase, ids, mask, j0, item.keys.n - j0);
+        vc.run(dst + F::kTileBytes, vbase, ids, mask, j0, item.keys.n - j0);
+      };
+      if (t0 < end) fetch(t0, 0, pages(t0));
+      int ids = pages(t0 + 1);
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      for (int i = t0; i < end; i += 2) {  // two tiles a round: the buffers' addresses are constants
+#pragma unroll
+        for (int buf = 0; buf < 2; ++buf) {
+          if (i + buf >= end) break;
+          if (i + buf + 1 < end) {
+            fetch(i + buf + 1, buf ^ 1, ids);
+            ids = pages(i + buf + 2);
+          }
+          compute_tile<E, NB, F::kKeys, KB>(a, item.keys, item.kt, r, st, mem + buf * 2 * F::kTileBytes, i + buf, c, at,
+                                            lane);
+          __builtin_amdgcn_s_waitcnt(0);
+          bare_barrier();
+        }
+      }
+    }
+    st.join_halves();
+    const StreamArgs& sa = arguments();
+    const PagedArgs& a = sa.a;
+    const Target to = WHOLE ? Target{nullptr, 0, 0} : target_of(a, sa.m, item, r, w, kvh, t0, t1, 32 * wave + l32);
+    const uint32_t bad = bad_rows(r.on ? zero_if_finite<NB>(st.acc) : 0.f);
+    const bool mine = (bad >> l32) & 1u;
+    if (r.on && !mine) store_row<E, NB>(a, to, r, st.acc, st.mc, st.l, 0, NB, h == 0, h);
+    if (bad != 0) {
+      safe_rows<E, NB, F::kKeys, NB>(a, item.keys, item.kt, t0, end, r, kvh, 0,
+                                     reinterpret_cast<float*>(mem) + wave * 1024, lane, st.acc, st.mc, st.l);
+      if (r.on && mine) store_row<E, NB>(a, to, r, st.acc, st.mc, st.l, 0, NB, h == 0, h);
+    }
+    if constexpr (WHOLE) return;
+    if (u < u_end) {
+      advance<F::kRows, F::kKeys>(a, l, cum, u, item);
+      to_scalars(a, item);
+      t = 0;
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();  // the tiles are read
+    }
+  }
+}
+
+// How many runs `units` are dealt to: `most`, or fewer of `least` units.
+__device__ __forceinline__ int runs_of(int units, int most, int least) {
+  const int r = units / least;
+  return uni(r < 1 ? 1 : r < most ? r : most);
+}
+constexpr int kLeastTokenUnits = 2, kLeastTileUnits = 4;
+
+// Waves take the whole list, or workgroups do, or the first workgroups the prefix and the others' waves the sequences'
+// own keys. The launch has a wave (token runs) or workgroup (tile runs) at least for every kv head.
+enum { kTokens = 0, kTiles = 1, kMixed = 2 };
+template <class E, int NB, int MODE>
+struct ModeShape {
+  typedef PagedShape<E, NB, true> FT;
+  typedef PagedShape<E, NB, false> FP;
+  static constexpr int kLds = MODE == kTokens  ? FT::kLds
+                              : MODE == kTiles ? FP::kLds
+                                               : (FT::kLds > FP::kLds ? FT::kLds : FP::kLds);
+  // workgroups that a CU holds
+  static constexpr int kPerCu = MODE == kTiles ? (sizeof(E) == 4 ? (NB == 4 ? 1 : 2) : NB <= 2 ? 4 : 2)
+                                               : (kLds > 80 * 1024 ? 1 : 2);
+  static constexpr int kGrid = 256 * kPerCu;
+};
+// Time of a prefix unit of a workgroup, in those of a wave's own.
+constexpr float kPrefixCost = 1.5f;
+
+template <class E, int NB, int MODE>
+__global__ __launch_bounds__(256, (ModeShape<E, NB, MODE>::kPerCu)) void paged_stream(StreamArgs) {
+  typedef ModeShape<E, NB, MODE> M;
+  typedef typename M::FT FT;
+  typedef typename M::FP FP;
+  __shared__ __attribute__((aligned(1024))) unsigned char s_mem[M::kLds + kCum * 4];
+  int* const s_cum = reinterpret_cast<int*>(s_mem + M::kLds);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int grid = gridDim.x, block = blockIdx.x;
+  const StreamArgs& sa = arguments();
+  const PagedArgs& a = sa.a;
+  char* const ws = reinterpret_cast<char*>(a.part);
+  Entry* const table = block == 0 ? reinterpret_cast<Entry*>(ws + sa.m.table) : nullptr;
+  Lists* const lists = reinterpret_cast<Lists*>(ws + sa.m.head);
+  if constexpr (MODE == kTokens) {
+    const List l = sum_up<FT::kRows, FT::kKeys, FT::kRows, FT::kKeys>(a, true, s_cum, table);
+    const int runs = runs_of(l.units, 4 * grid / a.hk, kLeastTokenUnits);
+    if (block == 0 && threadIdx.x == 0) *lists = Lists{{l.units, l.units}, {runs, runs}, max(l.pre.n, 1)};
+    const int at = block * 4 + wave, w = uni(at / a.hk);
+    if (w < runs) token_run<E, NB>(l, s_cum, at - w * a.hk, w, runs, s_mem + wave * (FT::kLds / 4));
+  } else if constexpr (MODE == kTiles) {
+    const List l = sum_up<FP::kRows, FP::kKeys, FP::kRows, FP::kKeys>(a, true, s_cum, table);
+    const int runs = runs_of(l.units, grid / a.hk, kLeastTileUnits);
+    if (block == 0 && threadIdx.x == 0) *lists = Lists{{l.units, l.units}, {runs, runs}, max(l.pre.n, 1)};
+    const int w = uni(block / a.hk);
+    if (w >= runs) return;
+    const int u = run_start(l.units, runs, w);
+    Item item;
+    const int t = locate<FP::kRows, FP::kKeys>(a, l, s_cum, u, item);
+    to_scalars(a, item);
+    tile_run<E, NB, false>(l, s_cum, block - w * a.hk, item, t, u, run_start(l.units, runs, w + 1), w, s_mem);
+  } else {
+    const List l = sum_up<FT::kRows, FT::kKeys, FP::kRows, FP::kKeys>(a, false, s_cum, table);
+    List p = l;
+    p.pre_tiles = uni((a.nq * (a.hq / a.hk) + FP::kRows - 1) / FP::kRows);
+    p.pre_units = p.units = p.pre_tiles * max(l.pre.n, 1);
+    const float cost = kPrefixCost * float(p.units), own = 0.25f * float(l.units);
+    int share = int(float(grid) * cost / (cost + own) + 0.5f);
+    share = min(max(share, a.hk), grid - (a.hk + 3) / 4);
+    const int pre_runs = runs_of(p.units, share / a.hk, kLeastTileUnits), pre_blocks = pre_runs * a.hk;
+    const int runs = runs_of(l.units, 4 * (grid - pre_blocks) / a.hk, kLeastTokenUnits);
+    if (block == 0 && threadIdx.x == 0) *lists = Lists{{l.units, p.units}, {runs, pre_runs}, max(l.pre.n, 1)};
+    if (block < pre_blocks) {
+      const int w = uni(block / a.hk), u = run_start(p.units, pre_runs, w);
+      Item item;
+      const int t = locate<FP::kRows, FP::kKeys>(a, p, s_cum, u, item);
+      to_scalars(a, item);
+      tile_run<E, NB, false>(p, s_cum, block - w * a.hk, item, t, u, run_start(p.units, pre_runs, w + 1), w, s_mem);
+    } else {
+      const int at = (block - pre_blocks) * 4 + wave, w = uni(at / a.hk);
+      if (w < runs) token_run<E, NB>(l, s_cum, at - w * a.hk, w, runs, s_mem + wave * (FT::kLds / 4));
+    }
+  }
+}
+
+// One item a workgroup, straight to out: prompts of many rows.
+template <class E, int NB>
+__global__ __launch_bounds__(256, (ModeShape<E, NB, kTiles>::kPerCu)) void paged_tiles(StreamArgs, int tiles) {
+  typedef PagedShape<E, NB, false> F;
+  __shared__ __attribute__((aligned(1024))) unsigned char s_mem[F::kLds];
+  const PagedArgs& a = arguments().a;
+  const int group = a.hq / a.hk, w = xcd_remap(blockIdx.x, gridDim.x), tile = w % tiles;
+  int inside, b;
+  if (a.seqs.cu == nullptr) {
+    const int per = (a.seqs.each * group + F::kRows - 1) / F::kRows;
+    b = tile / per;
+    inside = tile - b * per;
+  } else {
+    b = find_sequence(a.seqs.cu, a.seqs.batch, group, F::kRows, tile, &inside);
+  }
+  const OwnSeq s = uniform_sequence(a, b);
+  if (inside < 0 || inside >= row_tiles<F::kRows>(a, s)) return;
+  Item item;
+  own_tile<F::kRows, F::kKeys>(a, b, s, inside, item);
+  to_scalars(a, item);
+  tile_run<E, NB, true>(List{}, nullptr, uni(w / tiles), item, 0, 0, item.n, 0, s_mem);
+}
+
+// Few rows over few keys: one item a workgroup, whose four waves share its rows and split its keys, straight to out.
+template <class E, int NB>
+__global__ __launch_bounds__(256, (ModeShape<E, NB, kTokens>::kPerCu)) void paged_short(PagedArgs a, int tiles) {
+  typedef PagedShape<E, NB, true> F;
+  typedef Tile<E, NB> T;
+  constexpr int KB = 1;
   __shared__ __attribute__((aligned(1024))) unsigned char s_mem[F::kLds];
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int group = a.hq / a.hk;
-  const int w = xcd_remap(blockIdx.x, gridDim.x);
-  const int tile = w % tiles, kvh = (w / tiles) % a.hk, split = w / tiles / a.hk;
-  Keys keys;
-  Rows r;
-  KeyTiles kt;
-  if constexpr (PREFIX) {
-    keys = Keys{a.prefix, a.prefix_len, min(a.sinks, a.prefix_len)};
-    r = prefix_rows(a, keys, tile * F::kRows + (TOKEN ? 0 : 32 * wave), kvh, l32);
-    int p0 = r.p0, p1 = r.p1;
-    if constexpr (!TOKEN) {  // of the workgroup's rows
-      int* const red = reinterpret_cast<int*>(s_mem);
-      if (lane == 0) red[wave] = p0, red[4 + wave] = p1;
-      __syncthreads();
-      p0 = min(min(red[0], red[1]), min(red[2], red[3]));
-      p1 = max(max(red[4], red[5]), max(red[6], red[7]));
-      __syncthreads();
-    }
-    if (p0 > p1) return;
-    kt = key_tiles<F::kKeys>(a.left, a.right, keys.sinks, p0, p1, keys.n);
+  const int group = a.hq / a.hk, tile = blockIdx.x % tiles, kvh = uni(blockIdx.x / tiles);
+  int inside, b;
+  if (a.seqs.cu == nullptr) {
+    const int per = (a.seqs.each * group + F::kRows - 1) / F::kRows;
+    b = tile / per;
+    inside = tile - b * per;
   } else {
-    int inside, b;
-    if (a.seqs.cu == nullptr) {
-      const int per = (a.seqs.each * group + F::kRows - 1) / F::kRows;
-      b = tile / per;
-      inside = tile - b * per;
-    } else {
-      b = find_sequence(a.seqs.cu, a.seqs.batch, group, F::kRows, tile, &inside);
-    }
-    const OwnSeq s = paged_sequence(a, b);
-    const int rows = s.lq * group;
-    if (inside < 0 || inside > rows / F::kRows || inside * F::kRows >= rows) return;
-    const int r0 = inside * F::kRows, last = min(rows - 1, r0 + F::kRows - 1) / group, shift = s.lk - s.lq;
-    keys = Keys{a.pool.table + b * a.pool.table_ts, s.lk, max(0, a.sinks - a.prefix_len)};
-    kt = key_tiles<F::kKeys>(a.left, a.right, keys.sinks, r0 / group + shift, last + shift, s.lk);
-    r = own_rows(a, s, keys, r0 + (TOKEN ? 0 : 32 * wave), kvh, l32);
+    b = find_sequence(a.seqs.cu, a.seqs.batch, group, F::kRows, tile, &inside);
   }
+  const OwnSeq s = uniform_sequence(a, b);
+  if (inside < 0 || inside >= row_tiles<F::kRows>(a, s)) return;
+  Item item;
+  own_tile<F::kRows, F::kKeys>(a, b, s, inside, item);
+  to_scalars(a, item);
+  const Rows r = own_rows(a, s, item.keys, inside * F::kRows, kvh, l32);
   const typename T::Lane at = T::lane_of(lane);
   RowState<E, NB, KB> st;
   st.start(static_cast<const E*>(a.q.p) + r.tok * a.q.ts + r.head * a.q.hs, r.on, a.dim, lane);
   const E* kbase = static_cast<const E*>(a.pool.k) + kvh * a.pool.khs;
   const E* vbase = static_cast<const E*>(a.pool.v) + kvh * a.pool.vhs;
   const float c = a.scale * kLog2e;
-  const int mask = (1 << a.pool.log2) - 1;
-
-  const int first = int(int64_t(kt.n) * split / splits), end = int(int64_t(kt.n) * (split + 1) / splits);
-  unsigned char* const mem = s_mem + (TOKEN ? wave * F::kBuffers * 2 * F::kTileBytes : 0);
-  PagedCopy<E, NB, F::kKeys, TOKEN ? 1 : 4> kc, vc;
-  kc.start(a.pool.kss, a.dim, TOKEN ? 0 : wave, lane);
-  vc.start(a.pool.vss, a.dim, TOKEN ? 0 : wave, lane);
-  auto pages = [&](int it) { return it < end && lane < F::kKeys ? page_of(a, keys, kt.at(it) * F::kKeys + lane) : -1; };
-  auto fetch = [&](int it, int buf, int ids) {
-    const int t0 = kt.at(it) * F::kKeys;
+  const int mask = (1 << a.pool.log2) - 1, end = item.kt.n;
+  unsigned char* const mem = s_mem + wave * F::kBuffers * 2 * F::kTileBytes;
+  PagedCopy<E, NB, F::kKeys, 1> kc, vc;
+  kc.start(a.pool.kps, a.pool.kss, a.dim, 0, lane);
+  vc.start(a.pool.vps, a.pool.vss, a.dim, 0, lane);
+  auto pages = [&](int i) {
+    return i < end && lane < F::kKeys ? entry_of(a, item.keys, item.kt.at(i) * F::kKeys + lane) : -1;
+  };
+  auto fetch = [&](int i, int buf, int ids) {
+    const int j0 = item.kt.at(i) * F::kKeys;
     unsigned char* dst = mem + buf * 2 * F::kTileBytes;
-    kc.run(dst, kbase, a.pool.kps, a.pool.kss, ids, mask, t0, keys.n - t0);
-    vc.run(dst + F::kTileBytes, vbase, a.pool.vps, a.pool.vss, ids, mask, t0, keys.n - t0);
+    ids = checked(a, ids);
+    kc.run(dst, kbase, ids, mask, j0, item.keys.n - j0);
+    vc.run(dst + F::kTileBytes, vbase, ids, mask, j0, item.keys.n - j0);
   };
-  auto compute = [&](int it, int buf) {
-    const unsigned char* ks = mem + buf * 2 * F::kTileBytes;
-#pragma unroll
-    for (int part = 0; part < F::kKeys / (32 * KB); ++part) {
-      const int j0 = kt.at(it) * F::kKeys + part * 32 * KB, j1 = j0 + 32 * KB - 1;
-      if (!tile_seen(a, keys, r, j0, j1)) continue;
-      st.scores(ks + part * 32 * KB * T::kPitch, (a.dim + 15) / 16, at);
-      if (!tile_whole(a, keys, r, j0, j1)) {
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) hide(st.s[kb], j0 + 32 * kb, r.lo, r.hi, keys.sinks, lane);
+  // each wave its own tiles and LDS: no barrier in the loop
+  constexpr int NBUF = F::kBuffers;
+  int i = wave, buf = 0, ids = pages(i);
+  if (NBUF == 2 && i < end) {
+    fetch(i, 0, ids);
+    ids = pages(i + 4);
+  }
+  for (; i < end; i += 4) {
+    if constexpr (NBUF == 2) {
+      __builtin_amdgcn_s_waitcnt(0);
+      asm volatile("" ::: "memory");
+      if (i + 4 < end) {
+        fetch(i + 4, buf ^ 1, ids);
+        ids = pages(i + 8);
       }
-      st.weigh(c);
-      st.multiply(ks + F::kTileBytes + part * 32 * KB * T::kPitch, at);
-    }
-  };
-
-  if constexpr (!TOKEN) {
-    if (first < end) fetch(first, 0, pages(first));
-    int ids = pages(first + 1);
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    for (int it = first; it < end; it += 2) {  // two tiles a round: the buffers' addresses are constants
-#pragma unroll
-      for (int buf = 0; buf < 2; ++buf) {
-        if (it + buf >= end) break;
-        if (it + buf + 1 < end) {
-          fetch(it + buf + 1, buf ^ 1, ids);
-          ids = pages(it + buf + 2);
-        }
-        compute(it + buf, buf);
-        __builtin_amdgcn_s_waitcnt(0);
-        bare_barrier();
-      }
-    }
-  } else {
-    // each wave its own tiles and LDS: no barrier in the loop
-    constexpr int NBUF = F::kBuffers;
-    int it = first + wave, buf = 0, ids = pages(it);
-    if (NBUF == 2 && it < end) {
-      fetch(it, 0, ids);
-      ids = pages(it + 4);
-    }
-    for (; it < end; it += 4) {
-      if constexpr (NBUF == 2) {
-        __builtin_amdgcn_s_waitcnt(0);
-        asm volatile("" ::: "memory");
-        if (it + 4 < end) {
-          fetch(it + 4, buf ^ 1, ids);
-          ids = pages(it + 8);
-        }
-        compute(it, buf);
-        buf ^= 1;
-      } else {
-        __builtin_amdgcn_s_waitcnt(0);  // the last tile's reads are done
-        fetch(it, 0, ids);
-        ids = pages(it + 4);
-        __builtin_amdgcn_s_waitcnt(0);
-        asm volatile("" ::: "memory");
-        compute(it, 0);
-      }
+      compute_tile<E, NB, F::kKeys, KB>(a, item.keys, item.kt, r, st, mem + buf * 2 * F::kTileBytes, i, c, at, lane);
+      buf ^= 1;
+    } else {
+      __builtin_amdgcn_s_waitcnt(0);  // the last tile's reads are done
+      fetch(i, 0, ids);
+      ids = pages(i + 4);
+      __builtin_amdgcn_s_waitcnt(0);
+      asm volatile("" ::: "memory");
+      compute_tile<E, NB, F::kKeys, KB>(a, item.keys, item.kt, r, st, mem, i, c, at, lane);
     }
   }
   st.join_halves();
-  float mc = st.mc, l = st.l;
-  bool writer = true;
-  if constexpr (TOKEN) {
-    // the four waves hold the same rows over different keys: join them in wave
-    // order; wave w sums the blocks d = w, w + 4, ...
-    float* red = reinterpret_cast<float*>(s_mem);
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    if (lane < 32) {
-      red[wave * 64 + lane] = mc;
-      red[wave * 64 + 32 + lane] = l;
-    }
-    __syncthreads();
-    float mm = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) mm = fmaxf(mm, red[i * 64 + l32]);
-    float f[4], ll = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float mi = red[i * 64 + l32];
-      f[i] = mi == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mi - mm);
-      ll += f[i] * red[i * 64 + 32 + l32];
-    }
-    const float mine = f[0] * (wave == 0) + f[1] * (wave == 1) + f[2] * (wave == 2) + f[3] * (wave == 3);
-    const bool any = mc != -INFINITY;
-    mc = mm;
-    l = ll;
-    __syncthreads();
-#pragma unroll
-    for (int d = 0; d < NB; ++d)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) red[((wave * NB + d) * 16 + e) * 64 + lane] = any ? st.acc[d][e] * mine : 0.f;
-    __syncthreads();
-    writer = wave < NB;
-    if (writer) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        float v = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v += red[((i * NB + wave) * 16 + e) * 64 + lane];
-        st.acc[0][e] = v;
-      }
-    }
+  // the four waves hold the same rows over different keys: join them in wave
+  // order; wave w sums the blocks d = w, w + 4, ...
+  float* red = reinterpret_cast<float*>(s_mem);
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  if (lane < 32) {
+    red[wave * 64 + lane] = st.mc;
+    red[wave * 64 + 32 + lane] = st.l;
   }
-  // rows whose sums are not finite, again without what they do not see
+  __syncthreads();
+  float mc = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) mc = fmaxf(mc, red[w * 64 + l32]);
+  float l = 0.f, mine = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float mw = red[w * 64 + l32];
+    const float f = mw == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mw - mc);
+    l += f * red[w * 64 + 32 + l32];
+    if (w == wave) mine = f;
+  }
+  const bool any = st.mc != -INFINITY;
+  __syncthreads();
+#pragma unroll
+  for (int d = 0; d < NB; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) red[((wave * NB + d) * 16 + e) * 64 + lane] = any ? st.acc[d][e] * mine : 0.f;
+  __syncthreads();
+  const bool writer = wave < NB;
   float zero = 0.f;
-  if (writer && r.on) {
-    if constexpr (TOKEN) {
+  if (writer) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) zero = fmaf(st.acc[0][e], 0.f, zero);
-    } else {
-      zero = zero_if_finite<NB>(st.acc);
+    for (int e = 0; e < 16; ++e) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) v += red[((w * NB + wave) * 16 + e) * 64 + lane];
+      st.acc[0][e] = v;
+      if (r.on) zero = fmaf(v, 0.f, zero);
     }
   }
+  // rows whose sums are not finite, again without what they do not see; each wave has seen some of the columns: the
+  // rows of all four
   uint32_t bad = bad_rows(zero);
-  if constexpr (TOKEN) {  // each wave has seen some of the columns: the rows of all four
-    uint32_t* flags = reinterpret_cast<uint32_t*>(s_mem);
-    __syncthreads();
-    if (lane == 0) flags[wave] = bad;
-    __syncthreads();
-    bad = flags[0] | flags[1] | flags[2] | flags[3];
-  }
-  auto store = [&](bool which) {
-    if (r.on && writer && which)
-      store_row<E, NB>(a, parts, slot0 + split, r, st.acc, mc, l, TOKEN ? wave : 0, TOKEN ? 1 : NB,
-                       h == 0 && (!TOKEN || wave == 0), h);
-  };
-  const bool mine = (bad >> l32) & 1u;
-  store(!mine);
+  uint32_t* flags = reinterpret_cast<uint32_t*>(s_mem);
+  __syncthreads();
+  if (lane == 0) flags[wave] = bad;
+  __syncthreads();
+  bad = flags[0] | flags[1] | flags[2] | flags[3];
+  const Target to{nullptr, 0, 0};
+  const bool again = (bad >> l32) & 1u;
+  if (r.on && writer && !again) store_row<E, NB>(a, to, r, st.acc, mc, l, wave, 1, h == 0 && wave == 0, h);
   if (bad != 0) {
-    if constexpr (TOKEN) __syncthreads();  // the flags are read
+    __syncthreads();  // the flags are read
     if (!writer) return;
-    safe_rows<E, NB, F::kKeys, TOKEN ? 1 : NB>(a, keys, kt, first, end, r, kvh, TOKEN ? wave : 0,
-                                               reinterpret_cast<float*>(s_mem) + wave * 1024, lane, st.acc, mc, l);
-    store(mine);
+    safe_rows<E, NB, F::kKeys, 1>(a, item.keys, item.kt, 0, end, r, kvh, wave,
+                                  reinterpret_cast<float*>(s_mem) + wave * 1024, lane, st.acc, mc, l);
+    if (r.on && again) store_row<E, NB>(a, to, r, st.acc, mc, l, wave, 1, h == 0 && wave == 0, h);
   }
 }
 
-// Joins the parts of a row: WPR waves a (token, head); a lane has four
-// elements, and the parts are dealt to the lanes' groups in turn, whose sums are
-// added in a fixed order. Rows of no sequence are left.
-template <class E, int WPR>
-__global__ __launch_bounds__(256) void paged_join(PagedArgs a, int parts) {
-  constexpr int kRows = 4 / WPR;
+// Joins the parts of the rows of an item (own row tile `tile`, kv head): `rows` rows a wave, or (WPR = 4) one by four
+// waves; a lane has four elements, and the parts are dealt to the lanes' groups in turn, whose sums are added in a
+// fixed order. R: rows of a tile of the own keys, PR: of the prefix.
+template <class E, int WPR, int R, int PR>
+__global__ __launch_bounds__(256) void paged_join(PagedArgs a, PartMap m, int tiles, int chunks, int rows) {
   __shared__ float s_max[4], s_sum[4];
   __shared__ float4 s_out[4][32];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, tw = wave % WPR;
-  const int64_t n = int64_t(a.hq) * a.nq;
-  const int64_t row = int64_t(blockIdx.x) * kRows + wave / WPR;  // head * nq + token
-  if (row >= n) return;                                          // the whole team
-  const int head = int(row / a.nq), tok = int(row - int64_t(head) * a.nq);
-  if (a.seqs.cu != nullptr && (tok < a.seqs.cu[0] || tok >= a.seqs.cu[a.seqs.batch])) return;
-  const float* stat = a.part + parts * n * a.dim + row;
-  float mx = -INFINITY;
-  for (int s = tw * 64 + lane; s < parts; s += WPR * 64) mx = fmaxf(mx, stat[s * n]);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
-  if constexpr (WPR > 1) {
-    if (lane == 0) s_max[wave] = mx;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < WPR; ++i) mx = fmaxf(mx, s_max[i]);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, tw = WPR > 1 ? wave : 0;
+  const int group = a.hq / a.hk;
+  const int chunk = blockIdx.x % chunks, tile = (blockIdx.x / chunks) % tiles, kvh = blockIdx.x / chunks / tiles;
+  int inside, b;
+  if (a.seqs.cu == nullptr) {
+    const int per = (a.seqs.each * group + R - 1) / R;
+    b = tile / per;
+    inside = tile - b * per;
+  } else {
+    b = find_sequence(a.seqs.cu, a.seqs.batch, group, R, tile, &inside);
   }
-  const float ms = mx == -INFINITY ? 0.f : mx;
-  const int width = a.dim <= 64 ? 16 : 32;  // lanes of a group
-  const int groups = 64 / width, e4 = lane % width;
-  const bool on = 4 * e4 < a.dim;
-  const float* src = a.part + row * a.dim + 4 * (on ? e4 : 0);
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-#pragma unroll 4
-  for (int s = tw * groups + lane / width; s < parts; s += WPR * groups) {
-    const float w = __builtin_amdgcn_exp2f(stat[s * n] - ms);
-    const float4 x = *reinterpret_cast<const float4*>(src + s * n * a.dim);
-    sum += w;
-    v.x += w * x.x;
-    v.y += w * x.y;
-    v.z += w * x.z;
-    v.w += w * x.w;
-  }
-  for (int o = width; o < 64; o <<= 1) {
-    sum += __shfl_xor(sum, o);
-    v.x += __shfl_xor(v.x, o);
-    v.y += __shfl_xor(v.y, o);
-    v.z += __shfl_xor(v.z, o);
-    v.w += __shfl_xor(v.w, o);
-  }
-  if constexpr (WPR > 1) {
-    if (lane < 32) s_out[wave][lane] = v;
-    if (lane == 0) s_sum[wave] = sum;
-    __syncthreads();
-    if (wave > 0) return;
-#pragma unroll
-    for (int i = 1; i < WPR; ++i) {
-      const float4 x = s_out[i][lane & 31];
-      sum += s_sum[i];
-      v.x += x.x;
-      v.y += x.y;
-      v.z += x.z;
-      v.w += x.w;
+  const OwnSeq s = paged_sequence(a, b);
+  if (inside < 0 || inside >= row_tiles<R>(a, s)) return;
+  char* const ws = reinterpret_cast<char*>(a.part);
+  const Lists lists = *reinterpret_cast<const Lists*>(ws + m.head);
+  const Entry entry = reinterpret_cast<const Entry*>(ws + m.table)[tile];
+  // The runs that hold parts, [0] the own keys', [1] the prefix's: no table of a malformed batch leads out of them.
+  int first[2] = {0, 0}, n[2] = {0, 0};
+  auto find = [&](int kind, int u, int units) {
+    if (lists.units[kind] <= 0) return;
+    first[kind] = clamp_to(owner(lists.units[kind], lists.runs[kind], u), 0, lists.runs[kind] - 1);
+    n[kind] = clamp_to(owner(lists.units[kind], lists.runs[kind], u + units - 1) - first[kind] + 1, 0,
+                       lists.runs[kind] - first[kind]);
+  };
+  find(0, entry.first, entry.n);
+  if (a.prefix_len == 0 && n[0] == 1) return;  // stored
+  const int64_t all = int64_t(a.hq) * a.nq;
+  for (int i = 0; i < rows; ++i) {
+    const int in_tile = WPR > 1 ? chunk : (chunk * 4 + wave) * rows + i;
+    const int row = inside * R + in_tile;
+    if (in_tile >= R || row >= s.lq * group) return;  // WPR > 1: the whole workgroup
+    const int tok = s.q0 + row / group, head = kvh * group + row % group;
+    const int64_t out_row = int64_t(head) * a.nq + tok;
+    int pre_in_tile = 0;
+    if (a.prefix_len > 0) {
+      const int pre_row = tok * group + row % group, pre_tile = pre_row / PR;
+      pre_in_tile = pre_row - pre_tile * PR;
+      find(1, pre_tile * lists.pre_n, lists.pre_n);
     }
+    const int parts = n[0] + n[1];
+    // part p: its elements' row and its statistic
+    auto part = [&](int p, const float*& stat) -> const float* {
+      const int kind = p >= n[0];
+      if (kind) p -= n[0];
+      const float* base;
+      int64_t at, count;
+      if (n[kind] == 1) {
+        base = reinterpret_cast<const float*>(ws + m.whole[kind]);
+        at = out_row;
+        count = all;
+      } else {
+        base = reinterpret_cast<const float*>(ws + m.slots[kind]);
+        at = ((int64_t(first[kind] + p) * a.hk + kvh) * 2 + (p == 0)) * m.rows[kind] + (kind ? pre_in_tile : in_tile);
+        count = m.slot_count[kind] * m.rows[kind];
+      }
+      stat = base + count * a.dim + at;
+      return base + at * a.dim;
+    };
+    float mx = -INFINITY;
+    for (int p = tw * 64 + lane; p < parts; p += WPR * 64) {
+      const float* stat;
+      part(p, stat);
+      mx = fmaxf(mx, *stat);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
+    if constexpr (WPR > 1) {
+      if (lane == 0) s_max[wave] = mx;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) mx = fmaxf(mx, s_max[w]);
+    }
+    const float ms = mx == -INFINITY ? 0.f : mx;
+    const int width = a.dim <= 64 ? 16 : 32;  // lanes of a group
+    const int groups = 64 / width, e4 = lane % width;
+    const bool on = 4 * e4 < a.dim;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int p = tw * groups + lane / width; p < parts; p += WPR * groups) {
+      const float* stat;
+      const float4 x = *reinterpret_cast<const float4*>(part(p, stat) + 4 * (on ? e4 : 0));
+      const float w = __builtin_amdgcn_exp2f(*stat - ms);
+      sum += w;
+      v.x += w * x.x;
+      v.y += w * x.y;
+      v.z += w * x.z;
+      v.w += w * x.w;
+    }
+    for (int o = width; o < 64; o <<= 1) {
+      sum += __shfl_xor(sum, o);
+      v.x += __shfl_xor(v.x, o);
+      v.y += __shfl_xor(v.y, o);
+      v.z += __shfl_xor(v.z, o);
+      v.w += __shfl_xor(v.w, o);
+    }
+    if constexpr (WPR > 1) {
+      if (lane < 32) s_out[wave][lane] = v;
+      if (lane == 0) s_sum[wave] = sum;
+      __syncthreads();
+      if (wave > 0) return;
+#pragma unroll
+      for (int w = 1; w < WPR; ++w) {
+        const float4 x = s_out[w][lane & 31];
+        sum += s_sum[w];
+        v.x += x.x;
+        v.y += x.y;
+        v.z += x.z;
+        v.w += x.w;
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (on && lane < width) {
+      typedef E out4 __attribute__((ext_vector_type(4)));
+      E* op = static_cast<E*>(const_cast<void*>(a.o.p)) + tok * a.o.ts + head * a.o.hs + 4 * e4;
+      *reinterpret_cast<out4*>(op) = out4{static_cast<E>(v.x * inv), static_cast<E>(v.y * inv),
+                                          static_cast<E>(v.z * inv), static_cast<E>(v.w * inv)};
+    }
+    if (a.lse != nullptr && lane == 0)
+      a.lse[out_row] = sum == 0.f ? -INFINITY : (ms + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  if (on && lane < width) {
-    typedef E out4 __attribute__((ext_vector_type(4)));
-    E* op = static_cast<E*>(const_cast<void*>(a.o.p)) + tok * a.o.ts + head * a.o.hs + 4 * e4;
-    *reinterpret_cast<out4*>(op) = out4{static_cast<E>(v.x * inv), static_cast<E>(v.y * inv),
-                                        static_cast<E>(v.z * inv), static_cast<E>(v.w * inv)};
-  }
-  if (a.lse != nullptr && lane == 0)
-    a.lse[row] = sum == 0.f ? -INFINITY : (ms + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
 }
 
 int64_t own_tiles(const PagedArgs& a, int rows) {
@@ -574,84 +1144,139 @@ int64_t own_tiles(const PagedArgs& a, int rows) {
   if (a.seqs.cu == nullptr) return int64_t(a.seqs.batch) * ((int64_t(a.seqs.each) * group + rows - 1) / rows);
   return tiles_of(a.nq, a.seqs.batch, group, rows);
 }
-int64_t prefix_tiles(const PagedArgs& a, int rows) { return (int64_t(a.nq) * (a.hq / a.hk) + rows - 1) / rows; }
 
-template <class E, int NB, bool TOKEN, bool PREFIX>
-hipError_t launch_run(const PagedArgs& a, int splits, int slot0, int parts, hipStream_t st) {
-  constexpr int kRows = PagedShape<E, NB, TOKEN>::kRows;
-  const int64_t tiles = PREFIX ? prefix_tiles(a, kRows) : own_tiles(a, kRows);
-  const int64_t wgs = tiles * a.hk * splits;
-  if (wgs >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-  paged_attn<E, NB, TOKEN, PREFIX><<<unsigned(wgs), 256, 0, st>>>(a, int(tiles), splits, slot0, parts);
-  return hipGetLastError();
+// f(E{}, width in blocks of 32) for the call's type and head size.
+template <class E, class F>
+hipError_t with_width(const PagedArgs& a, const F& f) {
+  switch ((a.dim + 31) / 32) {
+    case 1: return f(E(), std::integral_constant<int, 1>());
+    case 2: return f(E(), std::integral_constant<int, 2>());
+    case 3: return f(E(), std::integral_constant<int, 3>());
+    default: return f(E(), std::integral_constant<int, 4>());
+  }
+}
+template <class F>
+hipError_t with_shape(const PagedArgs& a, const F& f) {
+  if (a.dtype == TR_SC_BF16) return with_width<__bf16>(a, f);
+  if (a.dtype == TR_SC_F16) return with_width<_Float16>(a, f);
+  return with_width<float>(a, f);
 }
 
-template <class E, int NB>
-hipError_t launch_shape(const PagedArgs& a, const PagedPlan& p, hipStream_t st) {
-  const int parts = p.prefix_splits + p.splits;
-  hipError_t e = hipSuccess;
-  if (p.prefix_splits > 0)
-    e = p.prefix_token_form ? launch_run<E, NB, true, true>(a, p.prefix_splits, 0, parts, st)
-                            : launch_run<E, NB, false, true>(a, p.prefix_splits, 0, parts, st);
-  if (e != hipSuccess) return e;
-  return p.token_form ? launch_run<E, NB, true, false>(a, p.splits, p.prefix_splits, parts, st)
-                      : launch_run<E, NB, false, false>(a, p.splits, p.prefix_splits, parts, st);
+PartMap part_map(const PagedArgs& a, const PagedPlan& p) {
+  PartMap m{};
+  const bool tiles = p.form == PagedForm::tiles, mixed = p.form == PagedForm::mixed;
+  const int64_t rows = int64_t(a.nq) * (a.hq / a.hk), each = int64_t(a.seqs.each) * (a.hq / a.hk);
+  const auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
+  int64_t at = 256;
+  const auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at = (at + bytes + 255) / 256 * 256;
+    return here;
+  };
+  m.table = take(own_tiles(a, tiles ? 128 : 32) * int64_t(sizeof(Entry)));
+  if (a.prefix_len > 0)
+    for (int i = 0; i < 2; ++i) m.whole[i] = take(int64_t(a.hq) * a.nq * (a.dim + 1) * 4);
+  // two slots a run; where one list holds both kinds they share them
+  m.rows[0] = int(least(tiles ? 128 : 32, a.seqs.cu == nullptr && (a.prefix_len == 0 || mixed) ? each : rows));
+  m.slot_count[0] = int64_t(2) * p.grid * (tiles ? 1 : 4);
+  m.slots[0] = take(m.slot_count[0] * m.rows[0] * (a.dim + 1) * 4);
+  m.rows[1] = mixed ? int(least(128, rows)) : m.rows[0];
+  m.slot_count[1] = mixed ? int64_t(2) * p.grid : m.slot_count[0];
+  m.slots[1] = mixed ? take(m.slot_count[1] * m.rows[1] * (a.dim + 1) * 4) : m.slots[0];
+  m.head = 0;
+  return m;
+}
+int64_t part_bytes(const PagedArgs& a, const PartMap& m, bool mixed) {
+  const int last = mixed ? 1 : 0;
+  return m.slots[last] + m.slot_count[last] * m.rows[last] * (a.dim + 1) * 4;
 }
 
-template <class E>
-hipError_t launch_type(const PagedArgs& a, const PagedPlan& p, hipStream_t st) {
-  const int nb = (a.dim + 31) / 32;
-  const hipError_t e = nb == 1   ? launch_shape<E, 1>(a, p, st)
-                       : nb == 2 ? launch_shape<E, 2>(a, p, st)
-                       : nb == 3 ? launch_shape<E, 3>(a, p, st)
-                                 : launch_shape<E, 4>(a, p, st);
-  const int parts = p.prefix_splits + p.splits;
-  if (e != hipSuccess || parts == 1) return e;
-  const int64_t rows = int64_t(a.hq) * a.nq;
-  if (parts > 8)
-    paged_join<E, 4><<<unsigned(rows), 256, 0, st>>>(a, parts);
+template <class E, int R, int PR>
+hipError_t launch_join(const PagedArgs& a, const PagedPlan& p, const PartMap& m, hipStream_t st) {
+  const int64_t tiles = own_tiles(a, R), items = tiles * a.hk;
+  const int64_t in_tile = a.seqs.cu == nullptr && int64_t(a.seqs.each) * (a.hq / a.hk) < R
+                              ? int64_t(a.seqs.each) * (a.hq / a.hk)
+                              : R;
+  // runs a part of an item has on average: many of few rows, four waves a row
+  const bool wide = int64_t(p.grid) * (R == 32 ? 4 : 1) / items > 16;
+  const int rows = R == 32 ? 1 : 4;
+  const int64_t chunks = wide ? in_tile : (in_tile + 4 * rows - 1) / (4 * rows);
+  if (items * chunks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+  if (wide)
+    paged_join<E, 4, R, PR><<<unsigned(items * chunks), 256, 0, st>>>(a, m, int(tiles), int(chunks), 1);
   else
-    paged_join<E, 1><<<unsigned((rows + 3) / 4), 256, 0, st>>>(a, parts);
+    paged_join<E, 1, R, PR><<<unsigned(items * chunks), 256, 0, st>>>(a, m, int(tiles), int(chunks), rows);
   return hipGetLastError();
-}
-
-// Splits of a walk over `span` keys by `tiles` row tiles.
-int splits_for(const PagedArgs& a, int64_t tiles, int64_t span, bool token) {
-  const int keys = token || a.dtype == TR_SC_F32 ? 32 : 64;
-  const int64_t rounds = (span + keys * (token ? 4 : 1) - 1) / (keys * (token ? 4 : 1));
-  const int64_t want = token && (a.dim > 64 || a.dtype == TR_SC_F32) ? 256 : 512;
-  const int64_t least = token || a.dtype == TR_SC_F32 ? 2 : 8;
-  int64_t s = (want + tiles - 1) / tiles;
-  if (s > rounds / least) s = rounds / least;
-  return s > 256 ? 256 : s < 1 ? 1 : int(s);
 }
 
 }  // namespace
 
 PagedPlan plan_paged_attention(const PagedArgs& a) {
   PagedPlan p{};
-  p.splits = 1;
+  p.form = PagedForm::shorts;
+  p.fits = true;
   if (a.nq == 0) return p;
   const int group = a.hq / a.hk;
-  p.token_form = int64_t(a.nq) * group <= int64_t(32) * a.seqs.batch;
-  const int64_t reach = int64_t(a.left) + a.right + 1 + a.sinks + (p.token_form ? 32 : 128) / group;
+  const bool few = int64_t(a.nq) * group <= int64_t(32) * a.seqs.batch;  // rows a sequence
   const int64_t room = int64_t(a.pool.table_pages) << a.pool.log2;
-  p.splits = splits_for(a, own_tiles(a, p.token_form ? 32 : 128) * a.hk, reach < room ? reach : room, p.token_form);
-  if (a.prefix_len > 0) {
-    p.prefix_token_form = int64_t(a.nq) * group <= 32;
-    const int64_t tiles = prefix_tiles(a, p.prefix_token_form ? 32 : 128) * a.hk;
-    p.prefix_splits = splits_for(a, tiles, a.prefix_len, p.prefix_token_form);
+  const int64_t reach = int64_t(a.left) + a.right + 1 + a.sinks + 32 / group;
+  const int64_t span = reach < room ? reach : room;
+  if (a.prefix_len > 0)
+    p.form = !few ? PagedForm::tiles : int64_t(a.nq) * group <= 32 ? PagedForm::tokens : PagedForm::mixed;
+  else if (few)
+    p.form = span <= 1024 ? PagedForm::shorts : PagedForm::tokens;
+  else
+    p.form = PagedForm::tiles;
+  (void)with_shape(a, [&](auto e, auto nb) {
+    typedef decltype(e) E;
+    constexpr int NB = decltype(nb)::value;
+    p.grid = p.form == PagedForm::tiles   ? ModeShape<E, NB, kTiles>::kGrid
+             : p.form == PagedForm::mixed ? ModeShape<E, NB, kMixed>::kGrid
+                                          : ModeShape<E, NB, kTokens>::kGrid;
+    return hipSuccess;
+  });
+  const int heads = p.form == PagedForm::tiles ? a.hk : p.form == PagedForm::mixed ? 2 * a.hk : (a.hk + 3) / 4;
+  if (p.grid < heads) p.grid = heads;
+  // items enough for the chip to even them out by itself: no parts
+  if (p.form == PagedForm::tiles && a.prefix_len == 0 && own_tiles(a, 128) * a.hk >= int64_t(4) * p.grid)
+    p.form = PagedForm::whole_tiles;
+  if (p.form == PagedForm::tokens || p.form == PagedForm::tiles || p.form == PagedForm::mixed)
+    p.part_floats = size_t(part_bytes(a, part_map(a, p), p.form == PagedForm::mixed)) / 4;
+  if (p.part_floats > 0) {  // the units of the list, each 32 keys at least, are counted in 32 bits
+    const int rows = p.form == PagedForm::tiles ? 128 : 32, keys = rows == 128 && a.dtype != TR_SC_F32 ? 64 : 32;
+    const int64_t pre = (int64_t(a.nq) * group + rows - 1) / rows * (a.prefix_len / 32 + 3);
+    p.fits = pre + own_tiles(a, rows) * (room / keys + 4) < (int64_t(1) << 31);
   }
-  const int parts = p.splits + p.prefix_splits;
-  if (parts > 1) p.part_floats = size_t(parts) * a.hq * a.nq * (a.dim + 1);
   return p;
 }
 
 hipError_t launch_paged_attention(const PagedArgs& a, const PagedPlan& p, hipStream_t st) {
   if (a.nq == 0) return hipSuccess;
-  if (a.dtype == TR_SC_BF16) return launch_type<__bf16>(a, p, st);
-  if (a.dtype == TR_SC_F16) return launch_type<_Float16>(a, p, st);
-  return launch_type<float>(a, p, st);
+  return with_shape(a, [&](auto e, auto nb) -> hipError_t {
+    typedef decltype(e) E;
+    constexpr int NB = decltype(nb)::value;
+    if (p.form == PagedForm::shorts || p.form == PagedForm::whole_tiles) {
+      const int64_t tiles = own_tiles(a, p.form == PagedForm::shorts ? 32 : 128), n = tiles * a.hk;
+      if (n >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+      if (p.form == PagedForm::shorts)
+        paged_short<E, NB><<<unsigned(n), 256, 0, st>>>(a, int(tiles));
+      else
+        paged_tiles<E, NB><<<unsigned(n), 256, 0, st>>>(StreamArgs{a, PartMap{}}, int(tiles));
+      return hipGetLastError();
+    }
+    const PartMap m = part_map(a, p);
+    if (p.form == PagedForm::tokens)
+      paged_stream<E, NB, kTokens><<<p.grid, 256, 0, st>>>(StreamArgs{a, m});
+    else if (p.form == PagedForm::tiles)
+      paged_stream<E, NB, kTiles><<<p.grid, 256, 0, st>>>(StreamArgs{a, m});
+    else
+      paged_stream<E, NB, kMixed><<<p.grid, 256, 0, st>>>(StreamArgs{a, m});
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    return p.form == PagedForm::tokens  ? launch_join<E, 32, 32>(a, p, m, st)
+           : p.form == PagedForm::tiles ? launch_join<E, 128, 128>(a, p, m, st)
+                                        : launch_join<E, 32, 128>(a, p, m, st);
+  });
 }
 
 }  // namespace trsc
