@@ -67,31 +67,35 @@ struct PagedCopy {
     }
   }
   // base: the head's first element in the pool; ids: page of row l of the tile in lane l, -1 for none; t0: the tile's
-  // first key, left: keys from there on. Rows without a page and past the end read as zero.
+  // first key, left: keys from there on. Rows without a page read as zero; ZEROS: rows past the end too, in a page that
+  // goes on behind them. (What lies there would spoil a product with a weight of zero; a score is hidden as it is.)
+  template <bool ZEROS>
   __device__ __forceinline__ void run(unsigned char* lds, const E* base, int ids, int page_mask, int t0, int left) const {
     const uint64_t at = reinterpret_cast<uint64_t>(base);
     const uint64_t from = (uint64_t(uint32_t(uni(int(at >> 32)))) << 32) | uint32_t(uni(int(at)));
     page_mask = uni(page_mask);
     t0 = uni(t0);
     left = uni(left);
-    if (left >= ROWS)
-      copies<true>(lds, from, ids, page_mask, t0, left);
-    else
-      copies<false>(lds, from, ids, page_mask, t0, left);
-  }
-  template <bool WHOLE>
-  __device__ __forceinline__ void copies(unsigned char* lds, uint64_t base, int ids, int page_mask, int t0, int left) const {
+    uint64_t p = 0;
+    uint32_t most = 0;
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
       const int copy = first + j * STEP;
       if (!((j + 1) * STEP <= kCopies || copy < kCopies)) continue;
-      const int row = copy * kRows;
-      const int page = __builtin_amdgcn_readlane(ids, row);
-      uint32_t bytes = full;
-      if constexpr (!WHOLE) bytes = full - uint32_t(kRows - clamp_to(left - row, 1, kRows)) * slot16 * 16;
-      bytes = page < 0 ? 0u : bytes;  // a row past the end has no page
-      const uint64_t at = uint64_t(uint32_t(page < 0 ? 0 : page)) * page16 + uint32_t((t0 + row) & page_mask) * slot16;
-      copy_lds16(buffer_of(reinterpret_cast<const void*>(base + (at << 4)), bytes), off[j], lds + copy * 1024);
+      const int row = copy * kRows, slot = (t0 + row) & page_mask;
+      if (j == 0 || slot < STEP * kRows) {  // another page than the copy before
+        const int page = __builtin_amdgcn_readlane(ids, row);
+        most = page < 0 ? 0u : full;  // a row past the end has no page unless one before it has
+        p = from + ((uint64_t(uint32_t(page < 0 ? 0 : page)) * page16 + uint32_t(slot) * slot16) << 4);
+      } else {
+        p += uint64_t(STEP * kRows * 16) * slot16;
+      }
+      uint32_t bytes = most;
+      if constexpr (ZEROS) {
+        if (left - row < kRows) bytes = left <= row ? 0u : most - uint32_t(kRows - (left - row)) * slot16 * 16;
+        if (most == 0) bytes = 0;
+      }
+      copy_lds16(buffer_of(reinterpret_cast<const void*>(p), bytes), off[j], lds + copy * 1024);
     }
   }
 };
@@ -349,6 +353,9 @@ struct List {
   int pre_units, units;  // the prefix's; all (below 2^31, checked by the caller)
   int pre_tiles;         // row tiles of the prefix in this list
   KeyTiles pre;          // its key tiles, of all rows together
+  // the lane's: units of the sequences before its own, behind the prefix's, and the first of them
+  int start;
+  OwnSeq s;
 };
 // No member smaller than 32 bits: the compiler puts the copied padding into LDS, and finds its place there by a read of
 // the dispatch packet in host memory, 8 us of the kernel's time.
@@ -387,19 +394,21 @@ __device__ __forceinline__ int first_entry(const PagedArgs& a, int b, const OwnS
   return a.seqs.cu == nullptr ? b * ((a.seqs.each * group + R - 1) / R) : s.q0 * group / R + b;
 }
 
-// Sums up the list: every workgroup for itself, 256 threads. cum: kCum ints of LDS, the first 257 the sums of the
-// threads' sequences' units. (Part of the kernel's one LDS array: with others beside it the compiler has every read of
-// a tile wait for the next tile's copies: 32 caches of up to 4100 keys, 72 us for 67.) The
-// prefix's positions are those of all sequences: what a tile of its rows does not see costs no products.
-constexpr int kCum = 272;
+// Sums up the list: every wave for itself, each lane over batch / 64 sequences. The prefix's positions are those of
+// all sequences: what a tile of its rows does not see costs no products. (A sum by the whole workgroup takes three
+// barriers, and an array in LDS; where that is not part of the tiles' array, the compiler has every read of a tile wait
+// for the next tile's copies: 32 caches of up to 4100 keys, 72 us for 67.)
+__device__ __forceinline__ int lane_sequences(const PagedArgs& a) { return uni((a.seqs.batch + 63) / 64); }
 template <int R, int KT, int PR, int PKT>
-__device__ __forceinline__ List sum_up(const PagedArgs& a, bool with_prefix, int* cum, Entry* table) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int per = (a.seqs.batch + 255) / 256;
-  int mine = 0;
-  int p0 = 0x7fffffff, p1 = -0x7fffffff;
-  for (int b = tid * per; b < min(a.seqs.batch, (tid + 1) * per); ++b) {
+__device__ __forceinline__ List sum_up(const PagedArgs& a, bool with_prefix, Entry* table) {
+  const int lane = threadIdx.x & 63;
+  const int per = lane_sequences(a), from = lane * per, to = min(a.seqs.batch, from + per);
+  List l{};
+  int mine = 0, p0 = 0x7fffffff, p1 = -0x7fffffff;
+#pragma unroll 2
+  for (int b = from; b < to; ++b) {
     const OwnSeq s = paged_sequence(a, b);
+    if (b == from) l.s = s;
     const int tiles = row_tiles<R>(a, s);
     for (int i = 0; i < tiles; ++i) {
       Item it;
@@ -417,32 +426,24 @@ __device__ __forceinline__ List sum_up(const PagedArgs& a, bool with_prefix, int
     const int x = __shfl_up(sum, o);
     if (lane >= o) sum += x;
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    p0 = min(p0, __shfl_xor(p0, o));
-    p1 = max(p1, __shfl_xor(p1, o));
-  }
-  int *const s_sum = cum + 257, *const s_p = cum + 261;
-  if (lane == 63) s_sum[wave] = sum;
-  if (lane == 0) s_p[wave] = p0, s_p[4 + wave] = p1;
-  __syncthreads();
-  for (int w = 0; w < wave; ++w) sum += s_sum[w];
-  cum[tid + 1] = sum;
-  if (tid == 0) cum[0] = 0;
-  List l{};
+  l.start = sum - mine;
   if (a.prefix_len > 0) {
-    p0 = min(min(s_p[0], s_p[1]), min(s_p[2], s_p[3]));
-    p1 = max(max(s_p[4], s_p[5]), max(s_p[6], s_p[7]));
-    l.pre = key_tiles<PKT>(a.left, a.right, min(a.sinks, a.prefix_len), p0, p1, a.prefix_len);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+      p0 = min(p0, __shfl_xor(p0, o));
+      p1 = max(p1, __shfl_xor(p1, o));
+    }
+    l.pre = key_tiles<PKT>(a.left, a.right, min(a.sinks, a.prefix_len), uni(p0), uni(p1), a.prefix_len);
+    l.pre = KeyTiles{uni(l.pre.sink), uni(l.pre.band), uni(l.pre.n)};
     if (with_prefix) {
       l.pre_tiles = uni((a.nq * (a.hq / a.hk) + PR - 1) / PR);
       l.pre_units = l.pre_tiles * max(l.pre.n, 1);
     }
   }
-  l.units = l.pre_units + s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+  l.units = l.pre_units + __builtin_amdgcn_readlane(sum, 63);
   if (table != nullptr) {
-    int at = l.pre_units + sum - mine;
-    for (int b = tid * per; b < min(a.seqs.batch, (tid + 1) * per); ++b) {
+    int at = l.pre_units + l.start;
+    for (int b = from; b < to; ++b) {
       const OwnSeq s = paged_sequence(a, b);
       const int tiles = row_tiles<R>(a, s), first = first_entry<R>(a, b, s);
       for (int i = 0; i < tiles; ++i) {
@@ -453,10 +454,6 @@ __device__ __forceinline__ List sum_up(const PagedArgs& a, bool with_prefix, int
       }
     }
   }
-  __syncthreads();
-  l.pre_units = uni(l.pre_units);
-  l.units = uni(l.units);
-  l.pre = KeyTiles{uni(l.pre.sink), uni(l.pre.band), uni(l.pre.n)};
   return l;
 }
 
@@ -481,7 +478,7 @@ __device__ __forceinline__ void to_scalars(const PagedArgs& a, Item& it) {
 }
 // The item of unit u, and the unit's number in it.
 template <int R, int KT>
-__device__ __forceinline__ int locate(const PagedArgs& a, const List& l, const int* cum, int u, Item& it) {
+__device__ __forceinline__ int locate(const PagedArgs& a, const List& l, int u, Item& it) {
   if (u < l.pre_units) {
     const int n = max(l.pre.n, 1), item = uni(u / n);
     prefix_item(a, l, item, it);
@@ -490,15 +487,17 @@ __device__ __forceinline__ int locate(const PagedArgs& a, const List& l, const i
     return u - item * n;
   }
   u -= l.pre_units;
-  const int lane = threadIdx.x & 63;
-  int t = 0;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) t += __popcll(__ballot(cum[64 * q + lane] <= u));
-  t = uni(t) - 1;
-  u -= uni(cum[t]);
-  const int per = uni((a.seqs.batch + 255) / 256), last = min(a.seqs.batch, (t + 1) * per);
-  for (int b = t * per; b < last; ++b) {  // u is less than this thread's sequences' units
-    const OwnSeq s = uniform_sequence(a, b);
+  // the last lane whose sequences start at u or before: u is less than their units
+  const int t = uni(__popcll(__ballot(l.start <= u))) - 1;
+  u -= __builtin_amdgcn_readlane(l.start, t);
+  const int per = lane_sequences(a), last = min(a.seqs.batch, (t + 1) * per);
+  for (int b = t * per; b < last; ++b) {
+    OwnSeq s;
+    if (b == t * per)
+      s = OwnSeq{__builtin_amdgcn_readlane(l.s.q0, t), __builtin_amdgcn_readlane(l.s.lq, t),
+                 __builtin_amdgcn_readlane(l.s.lk, t)};
+    else
+      s = uniform_sequence(a, b);
     const int tiles = uni(row_tiles<R>(a, s));
     for (int i = 0; i < tiles; ++i) {
       own_tile<R, KT>(a, b, s, i, it);
@@ -515,14 +514,14 @@ __device__ __forceinline__ int locate(const PagedArgs& a, const List& l, const i
 }
 // The item after `it`, whose first unit is u.
 template <int R, int KT>
-__device__ __forceinline__ void advance(const PagedArgs& a, const List& l, const int* cum, int u, Item& it) {
+__device__ __forceinline__ void advance(const PagedArgs& a, const List& l, int u, Item& it) {
   if (it.prefix && it.inside + 1 < l.pre_tiles) {
     ++it.inside;
   } else if (!it.prefix && it.inside + 1 < uni(row_tiles<R>(a, it.s))) {
     own_tile<R, KT>(a, it.b, it.s, it.inside + 1, it);
     to_scalars(a, it);
   } else {
-    locate<R, KT>(a, l, cum, u, it);
+    locate<R, KT>(a, l, u, it);
   }
 }
 
@@ -578,120 +577,111 @@ __device__ __forceinline__ const StreamArgs& arguments() {
   return *(const StreamArgs*)(p);
 }
 
-// Run w of the list for one kv head, one wave: items of 32 rows, the next tile always on its way to LDS, over items' borders too.
+// Run w of the list for one kv head, one wave: items of 32 rows, the next tile always on its way to LDS, over items'
+// borders too. There is one place that begins an item, one that fetches and one that computes: code that runs once is
+// read from memory, cache line by cache line.
 template <class E, int NB>
-__device__ __forceinline__ void token_run(const List& l, const int* cum, int kvh, int w, int runs, unsigned char* mem) {
+__device__ __forceinline__ void token_run(const List& l, int kvh, int w, int runs, unsigned char* mem) {
   typedef PagedShape<E, NB, true> F;
   typedef Tile<E, NB> T;
-  constexpr int KB = 1;
+  constexpr int KB = 1, NBUF = F::kBuffers;
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
-  int u = run_start(l.units, runs, w);
   const int u_end = run_start(l.units, runs, w + 1);
+  int u = run_start(l.units, runs, w);  // next unit to fetch
   if (u >= u_end) return;
   const typename T::Lane at = T::lane_of(lane);
   PagedCopy<E, NB, F::kKeys, 1> kc, vc;
-  Item item;
-  int t, buf = 0, ids;
+  Item item, next;  // of the tile in work, and of the one to fetch
+  int t, tn, ids;   // their numbers, the pages of the latter
   auto pages = [&](const PagedArgs& a, const Item& i, int tile) {
     return tile < i.kt.n && lane < F::kKeys ? entry_of(a, i.keys, i.kt.at(tile) * F::kKeys + lane) : -1;
   };
-  auto fetch = [&](const PagedArgs& a, const Item& i, int tile, int to, int of) {
-    if (tile >= i.kt.n) return;
-    const int t0 = i.kt.at(tile) * F::kKeys, mask = (1 << a.pool.log2) - 1;
-    unsigned char* dst = mem + to * 2 * F::kTileBytes;
-    of = checked(a, of);
-    kc.run(dst, static_cast<const E*>(a.pool.k) + kvh * a.pool.khs, of, mask, t0, i.keys.n - t0);
-    vc.run(dst + F::kTileBytes, static_cast<const E*>(a.pool.v) + kvh * a.pool.vhs, of, mask, t0, i.keys.n - t0);
+  auto fetch = [&](const PagedArgs& a, int buf) {
+    if (tn < next.kt.n) {
+      const int t0 = next.kt.at(tn) * F::kKeys, mask = (1 << a.pool.log2) - 1;
+      unsigned char* dst = mem + buf * 2 * F::kTileBytes;
+      const int of = checked(a, ids);
+      kc.template run<false>(dst, static_cast<const E*>(a.pool.k) + kvh * a.pool.khs, of, mask, t0, next.keys.n - t0);
+      vc.template run<true>(dst + F::kTileBytes, static_cast<const E*>(a.pool.v) + kvh * a.pool.vhs, of, mask, t0,
+                            next.keys.n - t0);
+    }
+    ++u;
+    if (++tn < next.n) ids = pages(a, next, tn);
   };
   {
     const PagedArgs& a = arguments().a;
     kc.start(a.pool.kps, a.pool.kss, a.dim, 0, lane);
     vc.start(a.pool.vps, a.pool.vss, a.dim, 0, lane);
-    t = locate<F::kRows, F::kKeys>(a, l, cum, u, item);
-    to_scalars(a, item);
-    ids = pages(a, item, t);
+    t = tn = uni(locate<F::kRows, F::kKeys>(a, l, u, next));
+    to_scalars(a, next);
+    ids = pages(a, next, tn);
   }
   RowState<E, NB, KB> st;
-  bool fetched = false;
-  while (u < u_end && item.n > 0) {
-    const int t0 = uni(t), t1 = uni(min(item.n, t + (u_end - u)));
-    u += t1 - t0;
-    Rows r;
-    {
-      const PagedArgs& a = arguments().a;
+  Rows r;
+  int t0 = t, t1 = t, buf = 0, left = next.n > 0 ? u_end - u : 0;  // units to compute
+  bool waiting = NBUF == 2;  // for the run's first tile: nothing to compute yet
+  while (left > 0) {
+    const PagedArgs& a = arguments().a;
+    if (t == t1) {  // an item begins: the one whose tile was fetched last, or is fetched first
+      item = next;
+      t0 = t;
+      t1 = min(item.n, t + left);
       r = item.prefix ? prefix_rows(a, item.keys, item.inside * F::kRows, kvh, l32)
                       : own_rows(a, item.s, item.keys, item.inside * F::kRows, kvh, l32);
       st.start(static_cast<const E*>(a.q.p) + r.tok * a.q.ts + r.head * a.q.hs, r.on, a.dim, lane);
     }
-    {
-      const PagedArgs& a = arguments().a;
-      const float c = a.scale * kLog2e;
-      if (F::kBuffers == 2 && !fetched) {  // the run's first tile, behind the queries
-        fetch(a, item, t, 0, ids);
-        ids = pages(a, item, t + 1);
-        fetched = true;
-      }
-      for (t = t0; t < t1; ++t) {
-        if constexpr (F::kBuffers == 2) {
-          __builtin_amdgcn_s_waitcnt(0);
-          asm volatile("" ::: "memory");
-          if (t + 1 < t1) {
-            fetch(a, item, t + 1, buf ^ 1, ids);
-            ids = pages(a, item, t + 2);
-          }
-          if (t + 1 == t1) break;  // the last tile: below, behind the next item's first
-          if (t < item.kt.n)
-            compute_tile<E, NB, F::kKeys, KB>(a, item.keys, item.kt, r, st, mem + buf * 2 * F::kTileBytes, t, c, at, lane);
-          buf ^= 1;
-        } else {
-          __builtin_amdgcn_s_waitcnt(0);  // the last tile's reads are done
-          fetch(a, item, t, 0, ids);
-          ids = pages(a, item, t + 1);
-          __builtin_amdgcn_s_waitcnt(0);
-          asm volatile("" ::: "memory");
-          if (t < item.kt.n) compute_tile<E, NB, F::kKeys, KB>(a, item.keys, item.kt, r, st, mem, t, c, at, lane);
-        }
-      }
-    }
-    Item next = item;
+    __builtin_amdgcn_s_waitcnt(0);  // the tile, and the queries before the next tile's copies
+    asm volatile("" ::: "memory");
     if (u < u_end) {
-      const PagedArgs& a = arguments().a;
-      advance<F::kRows, F::kKeys>(a, l, cum, u, next);
-      to_scalars(a, next);
-      ids = pages(a, next, 0);
-      if constexpr (F::kBuffers == 2) {
-        fetch(a, next, 0, buf ^ 1, ids);
-        ids = pages(a, next, 1);
+      if (tn == next.n) {
+        advance<F::kRows, F::kKeys>(a, l, u, next);
+        to_scalars(a, next);
+        tn = 0;
+        ids = pages(a, next, 0);
+        __builtin_amdgcn_s_waitcnt(0);  // here, not where they are next set, behind the copies
       }
+      fetch(a, buf);
     }
-    const StreamArgs& sa = arguments();
-    const PagedArgs& a = sa.a;
-    if constexpr (F::kBuffers == 2) {
-      if (t < item.kt.n)
-        compute_tile<E, NB, F::kKeys, KB>(a, item.keys, item.kt, r, st, mem + buf * 2 * F::kTileBytes, t,
-                                          a.scale * kLog2e, at, lane);
-      buf ^= 1;
+    buf ^= NBUF - 1;
+    if (waiting) {
+      waiting = false;
+      continue;
     }
+    if constexpr (NBUF == 1) {
+      __builtin_amdgcn_s_waitcnt(0);
+      asm volatile("" ::: "memory");
+    }
+    if (t < item.kt.n)
+      compute_tile<E, NB, F::kKeys, KB>(a, item.keys, item.kt, r, st, mem + buf * 2 * F::kTileBytes, t,
+                                        a.scale * kLog2e, at, lane);
+    --left;
+    if (++t < t1) continue;
     st.join_halves();
+    const StreamArgs& sa = arguments();
     const Target to = target_of(a, sa.m, item, r, w, kvh, t0, t1, l32);
     const uint32_t bad = bad_rows(r.on ? zero_if_finite<NB>(st.acc) : 0.f);
     const bool mine = (bad >> l32) & 1u;
     if (r.on && !mine) store_row<E, NB>(a, to, r, st.acc, st.mc, st.l, 0, NB, h == 0, h);
     if (bad != 0) {  // again without what the rows do not see; the tile just used is free
-      float* const lds = reinterpret_cast<float*>(mem + (F::kBuffers == 2 ? buf ^ 1 : 0) * 2 * F::kTileBytes);
+      float* const lds = reinterpret_cast<float*>(mem + buf * 2 * F::kTileBytes);
       safe_rows<E, NB, F::kKeys, NB>(a, item.keys, item.kt, t0, min(t1, item.kt.n), r, kvh, 0, lds, lane, st.acc,
                                      st.mc, st.l);
       if (r.on && mine) store_row<E, NB>(a, to, r, st.acc, st.mc, st.l, 0, NB, h == 0, h);
     }
-    item = next;
-    t = 0;
+    t = t1 = 0;
+    if (NBUF == 1 && left > 0) {
+      advance<F::kRows, F::kKeys>(a, l, u, next);
+      to_scalars(a, next);
+      tn = 0;
+      ids = pages(a, next, 0);
+    }
   }
 }
 
 // Units u .. u_end of the list by one workgroup, from unit t of `item` on: items of 128 rows, 32 a wave. WHOLE: one
 // item, straight to out.
 template <class E, int NB, bool WHOLE>
-__device__ __forceinline__ void tile_run(const List& l, const int* cum, int kvh, Item item, int t, int u, int u_end,
+__device__ __forceinline__ void tile_run(const List& l, int kvh, Item item, int t, int u, int u_end,
                                          int w, unsigned char* mem) {
   typedef PagedShape<E, NB, false> F;
   typedef Tile<E, NB> T;
@@ -729,8 +719,8 @@ __device__ __forceinline__ void tile_run(const List& l, const int* cum, int kvh,
         const int j0 = item.kt.at(i) * F::kKeys;
         unsigned char* dst = mem + buf * 2 * F::kTileBytes;
         ids = checked(a, ids);
-        kc.run(dst, kbase, ids, mask, j0, item.keys.n - j0);
-        vc.run(dst + F::kTileBytes, vbase, ids, mask, j0, item.keys.n - j0);
+        kc.template run<false>(dst, kbase, ids, mask, j0, item.keys.n - j0);
+        vc.template run<true>(dst + F::kTileBytes, vbase, ids, mask, j0, item.keys.n - j0);
       };
       if (t0 < end) fetch(t0, 0, pages(t0));
       int ids = pages(t0 + 1);
@@ -765,7 +755,7 @@ __device__ __forceinline__ void tile_run(const List& l, const int* cum, int kvh,
     }
     if constexpr (WHOLE) return;
     if (u < u_end) {
-      advance<F::kRows, F::kKeys>(a, l, cum, u, item);
+      advance<F::kRows, F::kKeys>(a, l, u, item);
       to_scalars(a, item);
       t = 0;
       __builtin_amdgcn_s_waitcnt(0);
@@ -779,7 +769,10 @@ __device__ __forceinline__ int runs_of(int units, int most, int least) {
   const int r = units / least;
   return uni(r < 1 ? 1 : r < most ? r : most);
 }
-constexpr int kLeastTokenUnits = 2, kLeastTileUnits = 4;
+template <class E>
+constexpr int kLeastTokenUnits = sizeof(E) == 4 ? 1 : 2;
+template <class E>
+constexpr int kLeastTileUnits = sizeof(E) == 4 ? 1 : 2;
 
 // Waves take the whole list, or workgroups do, or the first workgroups the prefix and the others' waves the sequences'
 // own keys. The launch has a wave (token runs) or workgroup (tile runs) at least for every kv head.
@@ -797,59 +790,59 @@ struct ModeShape {
   static constexpr int kGrid = 256 * kPerCu;
 };
 // Time of a prefix unit of a workgroup, in those of a wave's own.
-constexpr float kPrefixCost = 1.5f;
+constexpr float kPrefixCost = 0.7f;
 
 template <class E, int NB, int MODE>
 __global__ __launch_bounds__(256, (ModeShape<E, NB, MODE>::kPerCu)) void paged_stream(StreamArgs) {
   typedef ModeShape<E, NB, MODE> M;
   typedef typename M::FT FT;
   typedef typename M::FP FP;
-  __shared__ __attribute__((aligned(1024))) unsigned char s_mem[M::kLds + kCum * 4];
-  int* const s_cum = reinterpret_cast<int*>(s_mem + M::kLds);
+  __shared__ __attribute__((aligned(1024))) unsigned char s_mem[M::kLds];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int grid = gridDim.x, block = blockIdx.x;
   const StreamArgs& sa = arguments();
   const PagedArgs& a = sa.a;
   char* const ws = reinterpret_cast<char*>(a.part);
-  Entry* const table = block == 0 ? reinterpret_cast<Entry*>(ws + sa.m.table) : nullptr;
+  Entry* const table = block == 0 && wave == 0 ? reinterpret_cast<Entry*>(ws + sa.m.table) : nullptr;
   Lists* const lists = reinterpret_cast<Lists*>(ws + sa.m.head);
   if constexpr (MODE == kTokens) {
-    const List l = sum_up<FT::kRows, FT::kKeys, FT::kRows, FT::kKeys>(a, true, s_cum, table);
-    const int runs = runs_of(l.units, 4 * grid / a.hk, kLeastTokenUnits);
+    const List l = sum_up<FT::kRows, FT::kKeys, FT::kRows, FT::kKeys>(a, true, table);
+    const int runs = runs_of(l.units, 4 * grid / a.hk, kLeastTokenUnits<E>);
     if (block == 0 && threadIdx.x == 0) *lists = Lists{{l.units, l.units}, {runs, runs}, max(l.pre.n, 1)};
     const int at = block * 4 + wave, w = uni(at / a.hk);
-    if (w < runs) token_run<E, NB>(l, s_cum, at - w * a.hk, w, runs, s_mem + wave * (FT::kLds / 4));
+    if (w < runs) token_run<E, NB>(l, at - w * a.hk, w, runs, s_mem + wave * (FT::kLds / 4));
   } else if constexpr (MODE == kTiles) {
-    const List l = sum_up<FP::kRows, FP::kKeys, FP::kRows, FP::kKeys>(a, true, s_cum, table);
-    const int runs = runs_of(l.units, grid / a.hk, kLeastTileUnits);
+    const List l = sum_up<FP::kRows, FP::kKeys, FP::kRows, FP::kKeys>(a, true, table);
+    const int runs = runs_of(l.units, grid / a.hk, kLeastTileUnits<E>);
     if (block == 0 && threadIdx.x == 0) *lists = Lists{{l.units, l.units}, {runs, runs}, max(l.pre.n, 1)};
-    const int w = uni(block / a.hk);
-    if (w >= runs) return;
+    if (block >= runs * a.hk) return;
+    const int at = xcd_remap(block, runs * a.hk), kvh = uni(at / runs), w = at - kvh * runs;
     const int u = run_start(l.units, runs, w);
     Item item;
-    const int t = locate<FP::kRows, FP::kKeys>(a, l, s_cum, u, item);
+    const int t = uni(locate<FP::kRows, FP::kKeys>(a, l, u, item));
     to_scalars(a, item);
-    tile_run<E, NB, false>(l, s_cum, block - w * a.hk, item, t, u, run_start(l.units, runs, w + 1), w, s_mem);
+    tile_run<E, NB, false>(l, kvh, item, t, u, run_start(l.units, runs, w + 1), w, s_mem);
   } else {
-    const List l = sum_up<FT::kRows, FT::kKeys, FP::kRows, FP::kKeys>(a, false, s_cum, table);
+    const List l = sum_up<FT::kRows, FT::kKeys, FP::kRows, FP::kKeys>(a, false, table);
     List p = l;
     p.pre_tiles = uni((a.nq * (a.hq / a.hk) + FP::kRows - 1) / FP::kRows);
     p.pre_units = p.units = p.pre_tiles * max(l.pre.n, 1);
     const float cost = kPrefixCost * float(p.units), own = 0.25f * float(l.units);
     int share = int(float(grid) * cost / (cost + own) + 0.5f);
     share = min(max(share, a.hk), grid - (a.hk + 3) / 4);
-    const int pre_runs = runs_of(p.units, share / a.hk, kLeastTileUnits), pre_blocks = pre_runs * a.hk;
-    const int runs = runs_of(l.units, 4 * (grid - pre_blocks) / a.hk, kLeastTokenUnits);
+    const int pre_runs = runs_of(p.units, share / a.hk, kLeastTileUnits<E>), pre_blocks = pre_runs * a.hk;
+    const int runs = runs_of(l.units, 4 * (grid - pre_blocks) / a.hk, kLeastTokenUnits<E>);
     if (block == 0 && threadIdx.x == 0) *lists = Lists{{l.units, p.units}, {runs, pre_runs}, max(l.pre.n, 1)};
     if (block < pre_blocks) {
-      const int w = uni(block / a.hk), u = run_start(p.units, pre_runs, w);
+      const int at = xcd_remap(block, pre_blocks), kvh = uni(at / pre_runs), w = at - kvh * pre_runs;
+      const int u = run_start(p.units, pre_runs, w);
       Item item;
-      const int t = locate<FP::kRows, FP::kKeys>(a, p, s_cum, u, item);
+      const int t = uni(locate<FP::kRows, FP::kKeys>(a, p, u, item));
       to_scalars(a, item);
-      tile_run<E, NB, false>(p, s_cum, block - w * a.hk, item, t, u, run_start(p.units, pre_runs, w + 1), w, s_mem);
+      tile_run<E, NB, false>(p, kvh, item, t, u, run_start(p.units, pre_runs, w + 1), w, s_mem);
     } else {
       const int at = (block - pre_blocks) * 4 + wave, w = uni(at / a.hk);
-      if (w < runs) token_run<E, NB>(l, s_cum, at - w * a.hk, w, runs, s_mem + wave * (FT::kLds / 4));
+      if (w < runs) token_run<E, NB>(l, at - w * a.hk, w, runs, s_mem + wave * (FT::kLds / 4));
     }
   }
 }
@@ -874,7 +867,7 @@ __global__ __launch_bounds__(256, (ModeShape<E, NB, kTiles>::kPerCu)) void paged
   Item item;
   own_tile<F::kRows, F::kKeys>(a, b, s, inside, item);
   to_scalars(a, item);
-  tile_run<E, NB, true>(List{}, nullptr, uni(w / tiles), item, 0, 0, item.n, 0, s_mem);
+  tile_run<E, NB, true>(List{}, uni(w / tiles), item, 0, 0, item.n, 0, s_mem);
 }
 
 // Few rows over few keys: one item a workgroup, whose four waves share its rows and split its keys, straight to out.
@@ -919,8 +912,8 @@ __global__ __launch_bounds__(256, (ModeShape<E, NB, kTokens>::kPerCu)) void page
     const int j0 = item.kt.at(i) * F::kKeys;
     unsigned char* dst = mem + buf * 2 * F::kTileBytes;
     ids = checked(a, ids);
-    kc.run(dst, kbase, ids, mask, j0, item.keys.n - j0);
-    vc.run(dst + F::kTileBytes, vbase, ids, mask, j0, item.keys.n - j0);
+    kc.template run<false>(dst, kbase, ids, mask, j0, item.keys.n - j0);
+    vc.template run<true>(dst + F::kTileBytes, vbase, ids, mask, j0, item.keys.n - j0);
   };
   // each wave its own tiles and LDS: no barrier in the loop
   constexpr int NBUF = F::kBuffers;
@@ -1009,13 +1002,13 @@ __global__ __launch_bounds__(256, (ModeShape<E, NB, kTokens>::kPerCu)) void page
   }
 }
 
-// Joins the parts of the rows of an item (own row tile `tile`, kv head): `rows` rows a wave, or (WPR = 4) one by four
-// waves; a lane has four elements, and the parts are dealt to the lanes' groups in turn, whose sums are added in a
+// Joins the parts of the rows of an item (own row tile `tile`, kv head): `rows` rows a wave, or (WPR = 16) one by as
+// many waves; a lane has four elements, and the parts are dealt to the lanes' groups in turn, whose sums are added in a
 // fixed order. R: rows of a tile of the own keys, PR: of the prefix.
 template <class E, int WPR, int R, int PR>
-__global__ __launch_bounds__(256) void paged_join(PagedArgs a, PartMap m, int tiles, int chunks, int rows) {
-  __shared__ float s_max[4], s_sum[4];
-  __shared__ float4 s_out[4][32];
+__global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void paged_join(PagedArgs a, PartMap m, int tiles, int chunks, int rows) {
+  __shared__ float s_max[WPR], s_sum[WPR];
+  __shared__ float4 s_out[WPR][32];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, tw = WPR > 1 ? wave : 0;
   const int group = a.hq / a.hk;
   const int chunk = blockIdx.x % chunks, tile = (blockIdx.x / chunks) % tiles, kvh = blockIdx.x / chunks / tiles;
@@ -1027,11 +1020,11 @@ __global__ __launch_bounds__(256) void paged_join(PagedArgs a, PartMap m, int ti
   } else {
     b = find_sequence(a.seqs.cu, a.seqs.batch, group, R, tile, &inside);
   }
-  const OwnSeq s = paged_sequence(a, b);
-  if (inside < 0 || inside >= row_tiles<R>(a, s)) return;
   char* const ws = reinterpret_cast<char*>(a.part);
   const Lists lists = *reinterpret_cast<const Lists*>(ws + m.head);
   const Entry entry = reinterpret_cast<const Entry*>(ws + m.table)[tile];
+  const OwnSeq s = paged_sequence(a, b);
+  if (inside < 0 || inside >= row_tiles<R>(a, s)) return;
   // The runs that hold parts, [0] the own keys', [1] the prefix's: no table of a malformed batch leads out of them.
   int first[2] = {0, 0}, n[2] = {0, 0};
   auto find = [&](int kind, int u, int units) {
@@ -1074,59 +1067,68 @@ __global__ __launch_bounds__(256) void paged_join(PagedArgs a, PartMap m, int ti
       stat = base + count * a.dim + at;
       return base + at * a.dim;
     };
-    float mx = -INFINITY;
-    for (int p = tw * 64 + lane; p < parts; p += WPR * 64) {
-      const float* stat;
-      part(p, stat);
-      mx = fmaxf(mx, *stat);
-    }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
-    if constexpr (WPR > 1) {
-      if (lane == 0) s_max[wave] = mx;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < WPR; ++w) mx = fmaxf(mx, s_max[w]);
-    }
-    const float ms = mx == -INFINITY ? 0.f : mx;
     const int width = a.dim <= 64 ? 16 : 32;  // lanes of a group
     const int groups = 64 / width, e4 = lane % width;
     const bool on = 4 * e4 < a.dim;
+    // this group's parts, kParts at a time: their largest statistic, the sum of their weights, the weighted sum
+    float mx = -INFINITY, sum = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-#pragma unroll 4
-    for (int p = tw * groups + lane / width; p < parts; p += WPR * groups) {
-      const float* stat;
-      const float4 x = *reinterpret_cast<const float4*>(part(p, stat) + 4 * (on ? e4 : 0));
-      const float w = __builtin_amdgcn_exp2f(*stat - ms);
-      sum += w;
-      v.x += w * x.x;
-      v.y += w * x.y;
-      v.z += w * x.z;
-      v.w += w * x.w;
-    }
-    for (int o = width; o < 64; o <<= 1) {
-      sum += __shfl_xor(sum, o);
-      v.x += __shfl_xor(v.x, o);
-      v.y += __shfl_xor(v.y, o);
-      v.z += __shfl_xor(v.z, o);
-      v.w += __shfl_xor(v.w, o);
-    }
-    if constexpr (WPR > 1) {
-      if (lane < 32) s_out[wave][lane] = v;
-      if (lane == 0) s_sum[wave] = sum;
-      __syncthreads();
-      if (wave > 0) return;
+    constexpr int kParts = WPR > 1 ? 8 : 4;
+    for (int p = tw * groups + lane / width; p < parts; p += kParts * WPR * groups) {
+      float lg[kParts];
+      float4 x[kParts];
 #pragma unroll
-      for (int w = 1; w < WPR; ++w) {
-        const float4 x = s_out[w][lane & 31];
-        sum += s_sum[w];
-        v.x += x.x;
-        v.y += x.y;
-        v.z += x.z;
-        v.w += x.w;
+      for (int i = 0; i < kParts; ++i) {
+        const int pi = p + i * WPR * groups;
+        lg[i] = -INFINITY;
+        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (pi < parts) {
+          const float* stat;
+          x[i] = *reinterpret_cast<const float4*>(part(pi, stat) + 4 * (on ? e4 : 0));
+          lg[i] = *stat;
+        }
+      }
+      float top = mx;
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) top = fmaxf(top, lg[i]);
+      const float ms = top == -INFINITY ? 0.f : top, f = __builtin_amdgcn_exp2f(mx - ms);
+      sum *= f;
+      v.x *= f;
+      v.y *= f;
+      v.z *= f;
+      v.w *= f;
+      mx = top;
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) {
+        const float w = __builtin_amdgcn_exp2f(lg[i] - ms);
+        sum += w;
+        v.x += w * x[i].x;
+        v.y += w * x[i].y;
+        v.z += w * x[i].z;
+        v.w += w * x[i].w;
       }
     }
+    auto add = [&](float omx, float osum, const float4& o) {
+      const float top = fmaxf(mx, omx), ms = top == -INFINITY ? 0.f : top;
+      const float f = __builtin_amdgcn_exp2f(mx - ms), g = __builtin_amdgcn_exp2f(omx - ms);
+      mx = top;
+      sum = sum * f + osum * g;
+      v.x = v.x * f + o.x * g;
+      v.y = v.y * f + o.y * g;
+      v.z = v.z * f + o.z * g;
+      v.w = v.w * f + o.w * g;
+    };
+    for (int o = width; o < 64; o <<= 1)
+      add(__shfl_xor(mx, o), __shfl_xor(sum, o),
+          make_float4(__shfl_xor(v.x, o), __shfl_xor(v.y, o), __shfl_xor(v.z, o), __shfl_xor(v.w, o)));
+    if constexpr (WPR > 1) {
+      if (lane < 32) s_out[wave][lane] = v;
+      if (lane == 0) s_max[wave] = mx, s_sum[wave] = sum;
+      __syncthreads();
+      if (wave > 0) return;
+      for (int w = 1; w < WPR; ++w) add(s_max[w], s_sum[w], s_out[w][lane & 31]);
+    }
+    const float ms = mx == -INFINITY ? 0.f : mx;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     if (on && lane < width) {
       typedef E out4 __attribute__((ext_vector_type(4)));
@@ -1138,6 +1140,9 @@ __global__ __launch_bounds__(256) void paged_join(PagedArgs a, PartMap m, int ti
       a.lse[out_row] = sum == 0.f ? -INFINITY : (ms + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
   }
 }
+
+// Keys that a call sees at most up to which a workgroup takes an item alone.
+constexpr int64_t kShort16 = 1024, kShort32 = 128;
 
 int64_t own_tiles(const PagedArgs& a, int rows) {
   const int group = a.hq / a.hk;
@@ -1197,13 +1202,13 @@ hipError_t launch_join(const PagedArgs& a, const PagedPlan& p, const PartMap& m,
   const int64_t in_tile = a.seqs.cu == nullptr && int64_t(a.seqs.each) * (a.hq / a.hk) < R
                               ? int64_t(a.seqs.each) * (a.hq / a.hk)
                               : R;
-  // runs a part of an item has on average: many of few rows, four waves a row
+  // runs a part of an item has on average: many of few rows, sixteen waves a row
   const bool wide = int64_t(p.grid) * (R == 32 ? 4 : 1) / items > 16;
   const int rows = R == 32 ? 1 : 4;
   const int64_t chunks = wide ? in_tile : (in_tile + 4 * rows - 1) / (4 * rows);
   if (items * chunks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
   if (wide)
-    paged_join<E, 4, R, PR><<<unsigned(items * chunks), 256, 0, st>>>(a, m, int(tiles), int(chunks), 1);
+    paged_join<E, 16, R, PR><<<unsigned(items * chunks), 1024, 0, st>>>(a, m, int(tiles), int(chunks), 1);
   else
     paged_join<E, 1, R, PR><<<unsigned(items * chunks), 256, 0, st>>>(a, m, int(tiles), int(chunks), rows);
   return hipGetLastError();
@@ -1224,7 +1229,7 @@ PagedPlan plan_paged_attention(const PagedArgs& a) {
   if (a.prefix_len > 0)
     p.form = !few ? PagedForm::tiles : int64_t(a.nq) * group <= 32 ? PagedForm::tokens : PagedForm::mixed;
   else if (few)
-    p.form = span <= 1024 ? PagedForm::shorts : PagedForm::tokens;
+    p.form = span <= (a.dtype == TR_SC_F32 ? kShort32 : kShort16) ? PagedForm::shorts : PagedForm::tokens;
   else
     p.form = PagedForm::tiles;
   (void)with_shape(a, [&](auto e, auto nb) {
