@@ -78,6 +78,20 @@ struct PagedCopy {
     left = uni(left);
     uint64_t p = 0;
     uint32_t most = 0;
+    const uint32_t step = uint32_t(STEP * kRows * 16) * slot16;
+    if (page_mask >= ROWS - 1 && left >= ROWS) {  // one page, no end in it: tiles begin at multiples of ROWS
+      const int page = __builtin_amdgcn_readlane(ids, 0);
+      most = page < 0 ? 0u : full;
+      p = from + ((uint64_t(uint32_t(page < 0 ? 0 : page)) * page16 + uint32_t((t0 & page_mask) + first * kRows) * slot16) << 4);
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        const int copy = first + j * STEP;
+        if (!((j + 1) * STEP <= kCopies || copy < kCopies)) continue;
+        copy_lds16(buffer_of(reinterpret_cast<const void*>(p), most), off[j], lds + copy * 1024);
+        p += step;
+      }
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
       const int copy = first + j * STEP;
@@ -88,7 +102,7 @@ struct PagedCopy {
         most = page < 0 ? 0u : full;  // a row past the end has no page unless one before it has
         p = from + ((uint64_t(uint32_t(page < 0 ? 0 : page)) * page16 + uint32_t(slot) * slot16) << 4);
       } else {
-        p += uint64_t(STEP * kRows * 16) * slot16;
+        p += step;
       }
       uint32_t bytes = most;
       if constexpr (ZEROS) {
@@ -353,9 +367,13 @@ struct List {
   int pre_units, units;  // the prefix's; all (below 2^31, checked by the caller)
   int pre_tiles;         // row tiles of the prefix in this list
   KeyTiles pre;          // its key tiles, of all rows together
-  // the lane's: units of the sequences before its own, behind the prefix's, and the first of them
-  int start;
-  OwnSeq s;
+  // In LDS, for every lane: the units of the sequences before its own, behind the prefix's, and the first of those
+  // sequences. (Not in registers, which the loops over the keys need.)
+  struct Lane {
+    int start;
+    OwnSeq s;
+  };
+  Lane* lanes;
 };
 // No member smaller than 32 bits: the compiler puts the copied padding into LDS, and finds its place there by a read of
 // the dispatch packet in host memory, 8 us of the kernel's time.
@@ -400,15 +418,17 @@ __device__ __forceinline__ int first_entry(const PagedArgs& a, int b, const OwnS
 // for the next tile's copies: 32 caches of up to 4100 keys, 72 us for 67.)
 __device__ __forceinline__ int lane_sequences(const PagedArgs& a) { return uni((a.seqs.batch + 63) / 64); }
 template <int R, int KT, int PR, int PKT>
-__device__ __forceinline__ List sum_up(const PagedArgs& a, bool with_prefix, Entry* table) {
+__device__ __forceinline__ List sum_up(const PagedArgs& a, bool with_prefix, Entry* table, List::Lane* lanes) {
   const int lane = threadIdx.x & 63;
   const int per = lane_sequences(a), from = lane * per, to = min(a.seqs.batch, from + per);
   List l{};
+  l.lanes = lanes;
+  OwnSeq own{0, 0, 0};
   int mine = 0, p0 = 0x7fffffff, p1 = -0x7fffffff;
 #pragma unroll 2
   for (int b = from; b < to; ++b) {
     const OwnSeq s = paged_sequence(a, b);
-    if (b == from) l.s = s;
+    if (b == from) own = s;
     const int tiles = row_tiles<R>(a, s);
     for (int i = 0; i < tiles; ++i) {
       Item it;
@@ -426,7 +446,7 @@ __device__ __forceinline__ List sum_up(const PagedArgs& a, bool with_prefix, Ent
     const int x = __shfl_up(sum, o);
     if (lane >= o) sum += x;
   }
-  l.start = sum - mine;
+  lanes[lane] = List::Lane{sum - mine, own};  // every wave the same
   if (a.prefix_len > 0) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) {
@@ -442,7 +462,7 @@ __device__ __forceinline__ List sum_up(const PagedArgs& a, bool with_prefix, Ent
   }
   l.units = l.pre_units + __builtin_amdgcn_readlane(sum, 63);
   if (table != nullptr) {
-    int at = l.pre_units + l.start;
+    int at = l.pre_units + sum - mine;
     for (int b = from; b < to; ++b) {
       const OwnSeq s = paged_sequence(a, b);
       const int tiles = row_tiles<R>(a, s), first = first_entry<R>(a, b, s);
@@ -488,14 +508,14 @@ __device__ __forceinline__ int locate(const PagedArgs& a, const List& l, int u, 
   }
   u -= l.pre_units;
   // the last lane whose sequences start at u or before: u is less than their units
-  const int t = uni(__popcll(__ballot(l.start <= u))) - 1;
-  u -= __builtin_amdgcn_readlane(l.start, t);
+  const int t = uni(__popcll(__ballot(l.lanes[threadIdx.x & 63].start <= u))) - 1;
+  const List::Lane from = l.lanes[t];
+  u -= uni(from.start);
   const int per = lane_sequences(a), last = min(a.seqs.batch, (t + 1) * per);
   for (int b = t * per; b < last; ++b) {
     OwnSeq s;
     if (b == t * per)
-      s = OwnSeq{__builtin_amdgcn_readlane(l.s.q0, t), __builtin_amdgcn_readlane(l.s.lq, t),
-                 __builtin_amdgcn_readlane(l.s.lk, t)};
+      s = OwnSeq{uni(from.s.q0), uni(from.s.lq), uni(from.s.lk)};
     else
       s = uniform_sequence(a, b);
     const int tiles = uni(row_tiles<R>(a, s));
@@ -797,7 +817,8 @@ __global__ __launch_bounds__(256, (ModeShape<E, NB, MODE>::kPerCu)) void paged_s
   typedef ModeShape<E, NB, MODE> M;
   typedef typename M::FT FT;
   typedef typename M::FP FP;
-  __shared__ __attribute__((aligned(1024))) unsigned char s_mem[M::kLds];
+  __shared__ __attribute__((aligned(1024))) unsigned char s_mem[M::kLds + 64 * sizeof(List::Lane)];
+  List::Lane* const lanes = reinterpret_cast<List::Lane*>(s_mem + M::kLds);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int grid = gridDim.x, block = blockIdx.x;
   const StreamArgs& sa = arguments();
@@ -806,13 +827,13 @@ __global__ __launch_bounds__(256, (ModeShape<E, NB, MODE>::kPerCu)) void paged_s
   Entry* const table = block == 0 && wave == 0 ? reinterpret_cast<Entry*>(ws + sa.m.table) : nullptr;
   Lists* const lists = reinterpret_cast<Lists*>(ws + sa.m.head);
   if constexpr (MODE == kTokens) {
-    const List l = sum_up<FT::kRows, FT::kKeys, FT::kRows, FT::kKeys>(a, true, table);
+    const List l = sum_up<FT::kRows, FT::kKeys, FT::kRows, FT::kKeys>(a, true, table, lanes);
     const int runs = runs_of(l.units, 4 * grid / a.hk, kLeastTokenUnits<E>);
     if (block == 0 && threadIdx.x == 0) *lists = Lists{{l.units, l.units}, {runs, runs}, max(l.pre.n, 1)};
     const int at = block * 4 + wave, w = uni(at / a.hk);
     if (w < runs) token_run<E, NB>(l, at - w * a.hk, w, runs, s_mem + wave * (FT::kLds / 4));
   } else if constexpr (MODE == kTiles) {
-    const List l = sum_up<FP::kRows, FP::kKeys, FP::kRows, FP::kKeys>(a, true, table);
+    const List l = sum_up<FP::kRows, FP::kKeys, FP::kRows, FP::kKeys>(a, true, table, lanes);
     const int runs = runs_of(l.units, grid / a.hk, kLeastTileUnits<E>);
     if (block == 0 && threadIdx.x == 0) *lists = Lists{{l.units, l.units}, {runs, runs}, max(l.pre.n, 1)};
     if (block >= runs * a.hk) return;
@@ -823,7 +844,7 @@ __global__ __launch_bounds__(256, (ModeShape<E, NB, MODE>::kPerCu)) void paged_s
     to_scalars(a, item);
     tile_run<E, NB, false>(l, kvh, item, t, u, run_start(l.units, runs, w + 1), w, s_mem);
   } else {
-    const List l = sum_up<FT::kRows, FT::kKeys, FP::kRows, FP::kKeys>(a, false, table);
+    const List l = sum_up<FT::kRows, FT::kKeys, FP::kRows, FP::kKeys>(a, false, table, lanes);
     List p = l;
     p.pre_tiles = uni((a.nq * (a.hq / a.hk) + FP::kRows - 1) / FP::kRows);
     p.pre_units = p.units = p.pre_tiles * max(l.pre.n, 1);
