@@ -283,8 +283,9 @@ __device__ __forceinline__ void store_row(const PagedArgs& a, const Target& to, 
 }
 
 // A wave's rows again over the key tiles [first, end), adding only what each sees (attn_common.h): blocks d0 ..
-// d0 + DN of O^T, the scaled maximum and the sum. lds: 4 KB of the wave's own.
-template <class E, int NB, int KT, int DN>
+// d0 + DN of O^T, the scaled maximum and the sum, from the start or (MORE) on top of another run of keys. lds: 4 KB of
+// the wave's own.
+template <class E, int NB, int KT, int DN, bool MORE = false>
 __device__ void safe_rows(const PagedArgs& a, const Keys& keys, const KeyTiles& kt, int first, int end, const Rows& r,
                           int kvh, int d0, float* lds, int lane, f32x16 (&acc)[NB], float& mc, float& l) {
   constexpr int ST = NB * 2;
@@ -296,12 +297,17 @@ __device__ void safe_rows(const PagedArgs& a, const Keys& keys, const KeyTiles& 
   typename AttnType<E>::frag qf[ST];
 #pragma unroll
   for (int st = 0; st < ST; ++st) qf[st] = row_from<E>(qp, r.on, st, a.dim, lane);
-#pragma unroll
-  for (int d = 0; d < DN; ++d)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) acc[d][e] = 0.f;
   float m = -INFINITY;
-  l = 0.f;
+  if constexpr (!MORE) {
+#pragma unroll
+    for (int d = 0; d < DN; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[d][e] = 0.f;
+    l = 0.f;
+  } else {  // both halves of the wave hold the whole sum
+    m = mc / c;
+    l *= 0.5f;
+  }
   for (int it = first * (KT / 32); it < end * (KT / 32); ++it) {
     const int j0 = kt.at(it / (KT / 32)) * KT + it % (KT / 32) * 32;
     if (!tile_seen(a, keys, r, j0, j0 + 31)) continue;
@@ -891,12 +897,23 @@ __global__ __launch_bounds__(256, (ModeShape<E, NB, kTiles>::kPerCu)) void paged
   tile_run<E, NB, true>(List{}, uni(w / tiles), item, 0, 0, item.n, 0, s_mem);
 }
 
-// Few rows over few keys: one item a workgroup, whose four waves share its rows and split its keys, straight to out.
+// Few rows over few keys: one row tile and kv head a workgroup, whose waves share its rows and split its keys, the
+// prefix's and its own, straight to out. Eight waves where their tiles fit: a call of this size is as long as one
+// wave's tiles, one after another.
 template <class E, int NB>
-__global__ __launch_bounds__(256, (ModeShape<E, NB, kTokens>::kPerCu)) void paged_short(PagedArgs a, int tiles) {
-  typedef PagedShape<E, NB, true> F;
+struct ShortShape {
   typedef Tile<E, NB> T;
-  constexpr int KB = 1;
+  static constexpr int kRows = 32, kKeys = 32, kTileBytes = kKeys * T::kPitch;
+  static constexpr int kWaves = 16 * kTileBytes <= 128 * 1024 ? 8 : 4;
+  static constexpr int kBuffers = kWaves * 4 * kTileBytes <= 128 * 1024 ? 2 : 1;
+  static constexpr int kLds = kWaves * kBuffers * 2 * kTileBytes;
+  static_assert(kLds >= kWaves * NB * 4096 && kLds >= kWaves * 4096, "the waves' sums and factors");
+};
+template <class E, int NB>
+__global__ __launch_bounds__((64 * ShortShape<E, NB>::kWaves)) void paged_short(PagedArgs a, int tiles) {
+  typedef ShortShape<E, NB> F;
+  typedef Tile<E, NB> T;
+  constexpr int KB = 1, NBUF = F::kBuffers, W = F::kWaves;
   __shared__ __attribute__((aligned(1024))) unsigned char s_mem[F::kLds];
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -914,57 +931,75 @@ __global__ __launch_bounds__(256, (ModeShape<E, NB, kTokens>::kPerCu)) void page
   Item item;
   own_tile<F::kRows, F::kKeys>(a, b, s, inside, item);
   to_scalars(a, item);
-  const Rows r = own_rows(a, s, item.keys, inside * F::kRows, kvh, l32);
+  const Rows own = own_rows(a, s, item.keys, inside * F::kRows, kvh, l32);
+  // the prefix as this tile's rows see it
+  const Keys pre_keys{a.prefix, a.prefix_len, min(a.sinks, a.prefix_len)};
+  Rows pre = own;
+  see(a, pre_keys, own.lo + a.left + a.prefix_len, pre);
+  pre.p0 += a.prefix_len;
+  pre.p1 += a.prefix_len;
+  KeyTiles pre_kt{0, 0, 0};
+  if (a.prefix_len > 0) pre_kt = key_tiles<F::kKeys>(a.left, a.right, pre_keys.sinks, pre.p0, pre.p1, a.prefix_len);
+  pre_kt = KeyTiles{uni(pre_kt.sink), uni(pre_kt.band), uni(pre_kt.n)};
   const typename T::Lane at = T::lane_of(lane);
   RowState<E, NB, KB> st;
-  st.start(static_cast<const E*>(a.q.p) + r.tok * a.q.ts + r.head * a.q.hs, r.on, a.dim, lane);
+  st.start(static_cast<const E*>(a.q.p) + own.tok * a.q.ts + own.head * a.q.hs, own.on, a.dim, lane);
   const E* kbase = static_cast<const E*>(a.pool.k) + kvh * a.pool.khs;
   const E* vbase = static_cast<const E*>(a.pool.v) + kvh * a.pool.vhs;
   const float c = a.scale * kLog2e;
-  const int mask = (1 << a.pool.log2) - 1, end = item.kt.n;
-  unsigned char* const mem = s_mem + wave * F::kBuffers * 2 * F::kTileBytes;
+  const int mask = (1 << a.pool.log2) - 1, end = pre_kt.n + item.kt.n;
+  unsigned char* const mem = s_mem + wave * NBUF * 2 * F::kTileBytes;
   PagedCopy<E, NB, F::kKeys, 1> kc, vc;
   kc.start(a.pool.kps, a.pool.kss, a.dim, 0, lane);
   vc.start(a.pool.vps, a.pool.vss, a.dim, 0, lane);
-  auto pages = [&](int i) {
-    return i < end && lane < F::kKeys ? entry_of(a, item.keys, item.kt.at(i) * F::kKeys + lane) : -1;
-  };
+  // tile i: of the prefix, then of the own keys
+  auto keys_of = [&](int i) { return i < pre_kt.n ? pre_keys : item.keys; };
+  auto key_of = [&](int i) { return (i < pre_kt.n ? pre_kt.at(i) : item.kt.at(i - pre_kt.n)) * F::kKeys; };
+  auto pages = [&](int i) { return i < end && lane < F::kKeys ? entry_of(a, keys_of(i), key_of(i) + lane) : -1; };
   auto fetch = [&](int i, int buf, int ids) {
-    const int j0 = item.kt.at(i) * F::kKeys;
+    const int j0 = key_of(i), left = keys_of(i).n - j0;
     unsigned char* dst = mem + buf * 2 * F::kTileBytes;
     ids = checked(a, ids);
-    kc.template run<false>(dst, kbase, ids, mask, j0, item.keys.n - j0);
-    vc.template run<true>(dst + F::kTileBytes, vbase, ids, mask, j0, item.keys.n - j0);
+    kc.template run<false>(dst, kbase, ids, mask, j0, left);
+    vc.template run<true>(dst + F::kTileBytes, vbase, ids, mask, j0, left);
+  };
+  auto compute = [&](int i, int buf) {
+    const bool p = i < pre_kt.n;
+    Rows r = own;
+    r.lo = p ? pre.lo : own.lo;
+    r.hi = p ? pre.hi : own.hi;
+    r.p0 = p ? pre.p0 : own.p0;
+    r.p1 = p ? pre.p1 : own.p1;
+    const KeyTiles kt{0, p ? pre_kt.at(i) : item.kt.at(i - pre_kt.n), 1};
+    compute_tile<E, NB, F::kKeys, KB>(a, keys_of(i), kt, r, st, mem + buf * 2 * F::kTileBytes, 0, c, at, lane);
   };
   // each wave its own tiles and LDS: no barrier in the loop
-  constexpr int NBUF = F::kBuffers;
   int i = wave, buf = 0, ids = pages(i);
   if (NBUF == 2 && i < end) {
     fetch(i, 0, ids);
-    ids = pages(i + 4);
+    ids = pages(i + W);
   }
-  for (; i < end; i += 4) {
+  for (; i < end; i += W) {
     if constexpr (NBUF == 2) {
       __builtin_amdgcn_s_waitcnt(0);
       asm volatile("" ::: "memory");
-      if (i + 4 < end) {
-        fetch(i + 4, buf ^ 1, ids);
-        ids = pages(i + 8);
+      if (i + W < end) {
+        fetch(i + W, buf ^ 1, ids);
+        ids = pages(i + 2 * W);
       }
-      compute_tile<E, NB, F::kKeys, KB>(a, item.keys, item.kt, r, st, mem + buf * 2 * F::kTileBytes, i, c, at, lane);
+      compute(i, buf);
       buf ^= 1;
     } else {
       __builtin_amdgcn_s_waitcnt(0);  // the last tile's reads are done
       fetch(i, 0, ids);
-      ids = pages(i + 4);
+      ids = pages(i + W);
       __builtin_amdgcn_s_waitcnt(0);
       asm volatile("" ::: "memory");
-      compute_tile<E, NB, F::kKeys, KB>(a, item.keys, item.kt, r, st, mem, i, c, at, lane);
+      compute(i, 0);
     }
   }
   st.join_halves();
-  // the four waves hold the same rows over different keys: join them in wave
-  // order; wave w sums the blocks d = w, w + 4, ...
+  // the waves hold the same rows over different keys: join them in wave order; wave w sums block w
   float* red = reinterpret_cast<float*>(s_mem);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
@@ -975,10 +1010,10 @@ __global__ __launch_bounds__(256, (ModeShape<E, NB, kTokens>::kPerCu)) void page
   __syncthreads();
   float mc = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) mc = fmaxf(mc, red[w * 64 + l32]);
+  for (int w = 0; w < W; ++w) mc = fmaxf(mc, red[w * 64 + l32]);
   float l = 0.f, mine = 0.f;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < W; ++w) {
     const float mw = red[w * 64 + l32];
     const float f = mw == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mw - mc);
     l += f * red[w * 64 + 32 + l32];
@@ -998,33 +1033,36 @@ __global__ __launch_bounds__(256, (ModeShape<E, NB, kTokens>::kPerCu)) void page
     for (int e = 0; e < 16; ++e) {
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) v += red[((w * NB + wave) * 16 + e) * 64 + lane];
+      for (int w = 0; w < W; ++w) v += red[((w * NB + wave) * 16 + e) * 64 + lane];
       st.acc[0][e] = v;
-      if (r.on) zero = fmaf(v, 0.f, zero);
+      if (own.on) zero = fmaf(v, 0.f, zero);
     }
   }
   // rows whose sums are not finite, again without what they do not see; each wave has seen some of the columns: the
-  // rows of all four
+  // rows of all
   uint32_t bad = bad_rows(zero);
   uint32_t* flags = reinterpret_cast<uint32_t*>(s_mem);
   __syncthreads();
   if (lane == 0) flags[wave] = bad;
   __syncthreads();
-  bad = flags[0] | flags[1] | flags[2] | flags[3];
+  bad = 0;
+#pragma unroll
+  for (int w = 0; w < NB; ++w) bad |= flags[w];
   const Target to{nullptr, 0, 0};
   const bool again = (bad >> l32) & 1u;
-  if (r.on && writer && !again) store_row<E, NB>(a, to, r, st.acc, mc, l, wave, 1, h == 0 && wave == 0, h);
+  if (own.on && writer && !again) store_row<E, NB>(a, to, own, st.acc, mc, l, wave, 1, h == 0 && wave == 0, h);
   if (bad != 0) {
     __syncthreads();  // the flags are read
     if (!writer) return;
-    safe_rows<E, NB, F::kKeys, 1>(a, item.keys, item.kt, 0, end, r, kvh, wave,
-                                  reinterpret_cast<float*>(s_mem) + wave * 1024, lane, st.acc, mc, l);
-    if (r.on && again) store_row<E, NB>(a, to, r, st.acc, mc, l, wave, 1, h == 0 && wave == 0, h);
+    float* const lds = reinterpret_cast<float*>(s_mem) + wave * 1024;
+    safe_rows<E, NB, F::kKeys, 1>(a, pre_keys, pre_kt, 0, pre_kt.n, pre, kvh, wave, lds, lane, st.acc, mc, l);
+    safe_rows<E, NB, F::kKeys, 1, true>(a, item.keys, item.kt, 0, item.kt.n, own, kvh, wave, lds, lane, st.acc, mc, l);
+    if (own.on && again) store_row<E, NB>(a, to, own, st.acc, mc, l, wave, 1, h == 0 && wave == 0, h);
   }
 }
 
-// Joins the parts of the rows of an item (own row tile `tile`, kv head): `rows` rows a wave, or (WPR = 16) one by as
-// many waves; a lane has four elements, and the parts are dealt to the lanes' groups in turn, whose sums are added in a
+// Joins the parts of the rows of an item (own row tile `tile`, kv head): `rows` rows a wave, or (WPR > 1) one by WPR
+// waves; a lane has four elements, and the parts are dealt to the lanes' groups in turn, whose sums are added in a
 // fixed order. R: rows of a tile of the own keys, PR: of the prefix.
 template <class E, int WPR, int R, int PR>
 __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void paged_join(PagedArgs a, PartMap m, int tiles, int chunks, int rows) {
@@ -1162,8 +1200,18 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void paged_join(PagedArgs
   }
 }
 
-// Keys that a call sees at most up to which a workgroup takes an item alone.
-constexpr int64_t kShort16 = 1024, kShort32 = 128;
+// Whether a workgroup takes a row tile alone (one launch) or the chip's waves share the units (two, and the work list
+// first). Measured, GPU time of a call, alone / shared: bf16, 8 sequences, 8 heads of 64, 1024 keys 12.0 / 17.2 us, 2048
+// 17.8 / 19.0, 4096 24.6 / 22.9; 32, 4 heads of 128, 2048 keys 25.0 / 31.5, 4096 60 / 46; 128 (512 tiles) 1024 keys
+// 46 / 51; 128, 8 heads of 64 (1024 tiles) 256 keys 27 / 23. fp32, 8 sequences, 8 heads of 64, 512 keys 14.1 / 14.0, 1024
+// 27 / 23; 4 heads of 128, 256 keys 18.7 / 19.9, 512 25 / 20.5. Behind a prefix, which each tile reads for itself: bf16, 4
+// sequences, 16 heads of 64, 1280 keys 13.5 / 17.9, 2304 19.4 / 18.4; 4 heads of 128, 1280 keys 18.0 / 21.9, 2304 27 / 22;
+// 32, 16 heads of 64 (512 tiles) 768 keys 21.1 / 20.7.
+bool takes_alone(const PagedArgs& a, int64_t tiles, int64_t span) {
+  const bool wide = a.dim > 64, prefix = a.prefix_len > 0;
+  const int64_t most = a.dtype == TR_SC_F32 ? (wide ? 256 : 512) : wide && prefix ? 1536 : 2048;
+  return tiles <= (prefix ? 256 : 512) && span <= most;
+}
 
 int64_t own_tiles(const PagedArgs& a, int rows) {
   const int group = a.hq / a.hk;
@@ -1223,15 +1271,26 @@ hipError_t launch_join(const PagedArgs& a, const PagedPlan& p, const PartMap& m,
   const int64_t in_tile = a.seqs.cu == nullptr && int64_t(a.seqs.each) * (a.hq / a.hk) < R
                               ? int64_t(a.seqs.each) * (a.hq / a.hk)
                               : R;
-  // runs a part of an item has on average: many of few rows, sixteen waves a row
-  const bool wide = int64_t(p.grid) * (R == 32 ? 4 : 1) / items > 16;
+  // parts of a row, on average: its item's runs, and the prefix's
+  const int64_t workers = int64_t(p.grid) * (R == 32 ? 4 : 1), heads = a.hk;
+  int64_t parts = workers / (items > 0 ? items : 1) + 1;
+  if (a.prefix_len > 0) {
+    const int64_t pre_tiles = (int64_t(a.nq) * (a.hq / a.hk) + PR - 1) / PR;
+    parts += (PR == 128 ? p.grid / 2 : workers / 2) / (pre_tiles * heads) + 1;
+  }
+  // Many parts of few rows: sixteen waves a row (one cache in 256 parts 9 us, with four 12), or four.
+  const int64_t rows_all = int64_t(a.hq) * a.nq;
+  const int wpr = parts > 48 && rows_all <= 1024 ? 16 : parts > 8 && rows_all <= 16384 ? 4 : 1;
   const int rows = R == 32 ? 1 : 4;
-  const int64_t chunks = wide ? in_tile : (in_tile + 4 * rows - 1) / (4 * rows);
+  const int64_t chunks = wpr > 1 ? in_tile : (in_tile + 4 * rows - 1) / (4 * rows);
   if (items * chunks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-  if (wide)
-    paged_join<E, 16, R, PR><<<unsigned(items * chunks), 1024, 0, st>>>(a, m, int(tiles), int(chunks), 1);
+  const unsigned grid = unsigned(items * chunks);
+  if (wpr == 16)
+    paged_join<E, 16, R, PR><<<grid, 1024, 0, st>>>(a, m, int(tiles), int(chunks), 1);
+  else if (wpr == 4)
+    paged_join<E, 4, R, PR><<<grid, 256, 0, st>>>(a, m, int(tiles), int(chunks), 1);
   else
-    paged_join<E, 1, R, PR><<<unsigned(items * chunks), 256, 0, st>>>(a, m, int(tiles), int(chunks), rows);
+    paged_join<E, 1, R, PR><<<grid, 256, 0, st>>>(a, m, int(tiles), int(chunks), rows);
   return hipGetLastError();
 }
 
@@ -1246,13 +1305,13 @@ PagedPlan plan_paged_attention(const PagedArgs& a) {
   const bool few = int64_t(a.nq) * group <= int64_t(32) * a.seqs.batch;  // rows a sequence
   const int64_t room = int64_t(a.pool.table_pages) << a.pool.log2;
   const int64_t reach = int64_t(a.left) + a.right + 1 + a.sinks + 32 / group;
-  const int64_t span = reach < room ? reach : room;
-  if (a.prefix_len > 0)
-    p.form = !few ? PagedForm::tiles : int64_t(a.nq) * group <= 32 ? PagedForm::tokens : PagedForm::mixed;
-  else if (few)
-    p.form = span <= (a.dtype == TR_SC_F32 ? kShort32 : kShort16) ? PagedForm::shorts : PagedForm::tokens;
-  else
+  const int64_t span = reach < room + a.prefix_len ? reach : room + a.prefix_len;  // keys that a row tile sees at most
+  if (few && takes_alone(a, own_tiles(a, 32) * a.hk, span))
+    p.form = PagedForm::shorts;
+  else if (!few)
     p.form = PagedForm::tiles;
+  else
+    p.form = a.prefix_len == 0 || int64_t(a.nq) * group <= 32 ? PagedForm::tokens : PagedForm::mixed;
   (void)with_shape(a, [&](auto e, auto nb) {
     typedef decltype(e) E;
     constexpr int NB = decltype(nb)::value;
@@ -1285,7 +1344,7 @@ hipError_t launch_paged_attention(const PagedArgs& a, const PagedPlan& p, hipStr
       const int64_t tiles = own_tiles(a, p.form == PagedForm::shorts ? 32 : 128), n = tiles * a.hk;
       if (n >= (int64_t(1) << 31)) return hipErrorInvalidValue;
       if (p.form == PagedForm::shorts)
-        paged_short<E, NB><<<unsigned(n), 256, 0, st>>>(a, int(tiles));
+        paged_short<E, NB><<<unsigned(n), 64 * ShortShape<E, NB>::kWaves, 0, st>>>(a, int(tiles));
       else
         paged_tiles<E, NB><<<unsigned(n), 256, 0, st>>>(StreamArgs{a, PartMap{}}, int(tiles));
       return hipGetLastError();

@@ -277,6 +277,18 @@ PAGED = [
     ([2] * 70, [(37 * i) % 200 for i in range(70)], 16, 8, 2, 48, "bf16", -1, 0, 0, "plain"),
     ([1] * 3, [2600, 17, 1300], 256, 32, 1, 112, "f16", 100, 0, 128, "beside"),
     ([33, 1, 1, 1, 1, 1], [60, 900, 901, 902, 1, 30], 16, 8, 2, 128, "f32", -1, 0, 0, "plain"),
+    # few rows over many keys: units dealt to waves
+    ([1] * 6, [2600, 17, 0, 5000, 4097, 64], 16, 8, 4, 64, "bf16", -1, 0, 0, "beside"),
+    ([2] * 3, [3000, 1, 2300], 8, 8, 2, 128, "bf16", -1, 0, 0, "heads"),
+    ([1, 0, 7, 3], [2500, 40, 2900, 3], 32, 6, 3, 96, "f16", -1, 0, 0, "halves"),
+    ([4] * 2, [900, 1300], 16, 4, 2, 40, "f32", -1, 0, 0, "plain"),
+    ([1] * 5, [700, 5, 0, 33, 1200], 8, 8, 2, 128, "f32", 600, 0, 9, "beside"),
+    ([1] * 600, [(7 * i) % 64 for i in range(600)], 16, 2, 2, 32, "bf16", -1, 0, 0, "plain"),  # many short sequences
+    ([3] * 2, [2200, 2300], 64, 80, 40, 16, "f16", -1, 0, 0, "plain"),  # many heads
+    # many rows: units dealt to workgroups, and a workgroup an item
+    ([300, 0, 5, 290], [700, 40, 5, 1500], 16, 8, 4, 128, "f16", 500, 0, 4, "heads"),
+    ([160, 90], [200, 90], 8, 2, 2, 72, "f32", -1, 0, 0, "halves"),
+    ([1400, 3], [1400, 77], 32, 256, 256, 8, "bf16", 30, 0, 0, "beside"),
 ]
 
 
@@ -306,6 +318,19 @@ PREFIX = [
     ([1] * 3, [30, 31, 32], 4000, 16, 8, 1, 128, "f16", 24, 0, 0, "beside"),  # the prefix hardly in the window
     ([1] * 6, [5, 5, 5, 5, 5, 5], 64, 8, 2, 2, 16, "f32", 2, 0, 0, "halves"),  # not at all
     ([1] * 33, list(range(33)), 2100, 64, 12, 3, 40, "f32", -1, 0, 0, "plain"),
+    # units dealt to waves, prefix and own keys in one list
+    ([1] * 4, [500, 0, 77, 1300], 2500, 16, 8, 4, 64, "bf16", -1, 0, 0, "halves"),
+    ([2, 0, 1], [30, 9, 700], 3000, 8, 4, 2, 128, "f16", -1, 0, 0, "beside"),
+    ([1] * 3, [50, 60, 3], 1500, 8, 4, 1, 96, "f32", 1300, 0, 5, "heads"),
+    # the prefix to workgroups, the own keys to waves
+    ([1] * 20, [(31 * i) % 300 for i in range(20)], 3000, 16, 16, 4, 128, "bf16", -1, 0, 0, "beside"),
+    ([2, 0, 1, 3, 1, 1, 2, 1, 1, 1] * 3, [(17 * i) % 150 + 3 for i in range(30)], 2600, 16, 4, 2, 64, "f16", -1, 0, 0, "heads"),
+    ([1] * 40, [(9 * i) % 70 for i in range(40)], 4100, 64, 4, 2, 80, "bf16", 4000, 0, 3, "plain"),
+    ([1] * 300, [i % 5 for i in range(300)], 700, 8, 4, 2, 32, "f32", -1, 0, 0, "plain"),
+    ([2] * 9, [3] * 9, 2100, 16, 96, 48, 16, "bf16", -1, 0, 0, "plain"),  # many heads
+    # workgroups take both
+    ([140, 3, 0, 90], [300, 3, 20, 90], 1100, 16, 4, 2, 128, "f16", -1, 0, 0, "beside"),
+    ([70, 66], [70, 200], 400, 8, 2, 1, 64, "f32", 300, 0, 2, "halves"),
 ]
 
 
@@ -338,7 +363,8 @@ def test_scale(scale):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("new,prefix", [([1, 1], 0), ([1, 1], 96), ([150, 3], 0), ([150, 3], 96)])
+@pytest.mark.parametrize("new,prefix", [([1, 1], 0), ([1, 1], 96), ([1, 1], 3000), ([12, 12], 3000), ([150, 3], 0),
+                                        ([150, 3], 96)])
 def test_pages_that_are_none_read_as_zeros(dtype, new, prefix):
     """Page numbers past the pool or negative inside a sequence or the prefix: keys and values of zero, and no read outside."""
     keys, page, dim = [300, 180], 16, 64
@@ -388,7 +414,8 @@ def test_no_tokens():
 # What is not finite
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("new,prefix", [([6, 6], 0), ([6, 6], 70), ([140, 20], 0), ([140, 20], 70)])
+@pytest.mark.parametrize("new,prefix", [([6, 6], 0), ([6, 6], 70), ([6, 6], 2500), ([20, 20], 2500), ([140, 20], 0),
+                                        ([140, 20], 70)])
 def test_not_finite(dtype, new, prefix):
     """NaN and infinities in keys and values that a row does not see do not reach it; rows that do see them have what
     the formula gives: NaN, or the infinity of a value."""
@@ -399,8 +426,9 @@ def test_not_finite(dtype, new, prefix):
         own[b][what][j, 1, e] = value
         (kp, vp)[what][int(table[b, j // page]), j % page, 1, e] = value
     if prefix:
-        pre[1][60, 0, 9] = math.nan
-        vp[int(pre_pages[60 // page]), 60 % page, 0, 9] = math.nan
+        for j in (60, prefix - 2):
+            pre[1][j, 0, 9] = math.nan
+            vp[int(pre_pages[j // page]), j % page, 0, 9] = math.nan
     out, lse = attend(q, kp, vp, table, keys, new, pre_pages, prefix, left=left, right=0, sinks=0)
     t = 0
     for b, n in enumerate(new):
@@ -571,16 +599,16 @@ def test_prompts_then_tokens_as_from_a_contiguous_cache(dtype):
 
 
 def test_workspace_of_the_callers():
-    new, keys = [1] * 3, [900, 30, 400]
-    q, own, pre, kp, vp, table, pre_pages = attend_inputs(new, keys, 16, 8, 2, 64, "bf16", "plain", 500)
-    want = attend(q, kp, vp, table, keys, new, pre_pages, 500)[0]
-    ws = sc.Workspace(1 << 24, DEV)
+    new, keys, n = [1] * 3, [900, 30, 400], 5000
+    q, own, pre, kp, vp, table, pre_pages = attend_inputs(new, keys, 16, 8, 2, 64, "bf16", "plain", n)
+    want = attend(q, kp, vp, table, keys, new, pre_pages, n)[0]
+    ws = sc.Workspace(1 << 25, DEV)
     ws.buf.fill_(0xFF)  # NaN
-    assert torch.equal(attend(q, kp, vp, table, keys, new, pre_pages, 500, workspace=ws)[0], want)
+    assert torch.equal(attend(q, kp, vp, table, keys, new, pre_pages, n, workspace=ws)[0], want)
     with pytest.raises(ValueError, match="needed"):
-        attend(q, kp, vp, table, keys, new, pre_pages, 500, workspace=sc.Workspace(64, DEV))
+        attend(q, kp, vp, table, keys, new, pre_pages, n, workspace=sc.Workspace(64, DEV))
     with pytest.raises(ValueError, match="workspace is on cpu"):
-        attend(q, kp, vp, table, keys, new, pre_pages, 500, workspace=sc.Workspace(1 << 24, "cpu"))
+        attend(q, kp, vp, table, keys, new, pre_pages, n, workspace=sc.Workspace(1 << 25, "cpu"))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
