@@ -122,6 +122,7 @@ SIGNATURES = [
 ]
 
 _lib = None
+_binding = None
 
 
 class TrSparseConvError(RuntimeError):
@@ -149,3 +150,22 @@ def check(code: int) -> None:
     if code != OK:
         msg = lib().tr_sparseconv_last_error()
         raise TrSparseConvError(code, msg.decode() if msg else "")
+
+
+def binding():
+    """The native part of the binding (csrc/binding.cpp), bound to the library's functions."""
+    global _binding
+    if _binding is None:
+        L = lib()
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise ImportError("the native binding is not built; run `python -m submanifold_sparse_conv_amd.build`") from e
+        stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        names = ("qk_norm_rope_append", "paged_attention_workspace_bytes", "paged_window_attention",
+                 "shared_prefix_attention")
+        module.bind(*(ctypes.cast(getattr(L, "tr_sparseconv_" + n), _P).value for n in names), check, stream, device)
+        _binding = module
+    return _binding
