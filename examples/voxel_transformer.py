@@ -9,6 +9,9 @@ norm and rotation of the queries and keys by the voxels' own coordinates
 window_attention_backward, qk_norm_rope_backward, backward_data and
 backward_weights. `decode` then runs the trained block causally over one object,
 a prompt first and then token by token against its key-value cache.
+`continuations` serves several sequences behind one prompt from a paged cache: the
+prompt's keys and values once in pages of their own, every step appended
+(qk_norm_rope_append) and attended (shared_prefix_attention) for all at once.
 
     python examples/voxel_transformer.py [--steps 20]
 """
@@ -117,6 +120,35 @@ class Block(torch.nn.Module):
             outs.append(t[at - m:at] + o.flatten(1) @ self.proj)
         return torch.cat(outs)
 
+    @torch.no_grad()
+    def continuations(self, t, pos, tails, tail_pos, page_size=16):
+        """The block's causal output for the embedded tokens tails [sequences, m,
+        width] at tail_pos [sequences, m, axes], each sequence behind the prompt t
+        [n, width] at pos: the prompt in one call, then a token of every sequence at
+        a time."""
+        (n, dev), (count, m, _) = (t.shape[0], t.device), tails.shape
+        shared, own = -(-n // page_size), -(-m // page_size)
+        pages = torch.randperm(shared + count * own, device=dev).int()
+        prefix, table = pages[:shared], pages[shared:].view(count, own)
+        pool = torch.empty(pages.shape[0], page_size, 2 * self.kv_heads, self.dim, dtype=t.dtype, device=dev)
+        keys, values = pool.split([self.kv_heads, self.kv_heads], 2)
+
+        def append(t, pos, table, lens):
+            qkv = (t @ self.qkv).view(t.shape[0], -1, self.dim)
+            q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], 1)
+            return sc.qk_norm_rope_append(q, k, v, pos, self.freqs, keys, values, table, lens, q_gain=self.q_gain,
+                                          k_gain=self.k_gain)
+
+        append(t, pos, prefix[None], torch.tensor([n], dtype=torch.int32, device=dev))
+        lens, outs = torch.zeros(count, dtype=torch.int32, device=dev), []
+        for i in range(m):
+            lens += 1
+            q = append(tails[:, i], tail_pos[:, i], table, lens)
+            o = sc.shared_prefix_attention(q, keys, values, table, lens, prefix, n, left=self.left, right=0,
+                                           sinks=self.sinks)
+            outs.append(tails[:, i] + o.flatten(1) @ self.proj)
+        return torch.stack(outs, 1)
+
 
 def voxels(objects=2, device="cuda"):
     """Coordinates (b, x, y, z) of `objects` 64^3 objects in Morton order, their
@@ -165,7 +197,10 @@ def main(argv=None):
         n = min(256, int(cu[1]))
         t = sc.forward(kmap, x, block.conv.detach())[:n]
         out = block.decode(t, coords[:n, 1:], prompt=n - 64)
-    print(f"decoded 64 tokens after a prompt of {n - 64}: output {tuple(out.shape)}, rms {out.float().square().mean().sqrt():.3f}")
+        print(f"decoded 64 tokens after a prompt of {n - 64}: output {tuple(out.shape)}, rms {out.float().square().mean().sqrt():.3f}")
+        tails, at = t[-64:].view(4, 16, -1), coords[n - 64:n, 1:].view(4, 16, 3)
+        more = block.continuations(t[:-64], coords[:n - 64, 1:], tails, at)
+        print(f"4 continuations of 16 tokens behind them: output {tuple(more.shape)}, rms {more.float().square().mean().sqrt():.3f}")
 
 
 if __name__ == "__main__":

@@ -1281,7 +1281,7 @@ hipError_t launch_join(const PagedArgs& a, const PagedPlan& p, const PartMap& m,
   // Many parts of few rows: sixteen waves a row (one cache in 256 parts 9 us, with four 12), or four.
   const int64_t rows_all = int64_t(a.hq) * a.nq;
   const int wpr = parts > 48 && rows_all <= 1024 ? 16 : parts > 8 && rows_all <= 16384 ? 4 : 1;
-  const int rows = R == 32 ? 1 : 4;
+  const int rows = R == 32 ? 1 : 2;
   const int64_t chunks = wpr > 1 ? in_tile : (in_tile + 4 * rows - 1) / (4 * rows);
   if (items * chunks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
   const unsigned grid = unsigned(items * chunks);

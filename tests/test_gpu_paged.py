@@ -285,6 +285,8 @@ PAGED = [
     ([1] * 5, [700, 5, 0, 33, 1200], 8, 8, 2, 128, "f32", 600, 0, 9, "beside"),
     ([1] * 600, [(7 * i) % 64 for i in range(600)], 16, 2, 2, 32, "bf16", -1, 0, 0, "plain"),  # many short sequences
     ([3] * 2, [2200, 2300], 64, 80, 40, 16, "f16", -1, 0, 0, "plain"),  # many heads
+    ([i % 3 for i in range(200)], [(11 * i) % 90 for i in range(200)], 8, 8, 4, 24, "bf16", -1, 0, 0, "halves"),
+    ([1] * 3, [500, 1, 2400], 16, 40, 1, 64, "bf16", -1, 0, 0, "plain"),  # more rows a token than a wave holds
     # many rows: units dealt to workgroups, and a workgroup an item
     ([300, 0, 5, 290], [700, 40, 5, 1500], 16, 8, 4, 128, "f16", 500, 0, 4, "heads"),
     ([160, 90], [200, 90], 8, 2, 2, 72, "f32", -1, 0, 0, "halves"),
@@ -328,6 +330,8 @@ PREFIX = [
     ([1] * 40, [(9 * i) % 70 for i in range(40)], 4100, 64, 4, 2, 80, "bf16", 4000, 0, 3, "plain"),
     ([1] * 300, [i % 5 for i in range(300)], 700, 8, 4, 2, 32, "f32", -1, 0, 0, "plain"),
     ([2] * 9, [3] * 9, 2100, 16, 96, 48, 16, "bf16", -1, 0, 0, "plain"),  # many heads
+    ([i % 2 for i in range(130)], [(5 * i) % 40 for i in range(130)], 2050, 16, 4, 1, 40, "f16", -1, 0, 0, "halves"),
+    ([1] * 3, [40, 1, 9], 600, 16, 72, 1, 32, "f32", -1, 0, 0, "plain"),  # more rows a token than a wave holds
     # workgroups take both
     ([140, 3, 0, 90], [300, 3, 20, 90], 1100, 16, 4, 2, 128, "f16", -1, 0, 0, "beside"),
     ([70, 66], [70, 200], 400, 8, 2, 1, 64, "f32", 300, 0, 2, "halves"),
@@ -477,6 +481,25 @@ def test_offsets_past_32_bits():
     place(vp, pre_pages, page, pre[1])
     out, lse = attend(q, kp, vp, table.to(DEV), keys, new, pre_pages.to(DEV), 100, right=0)
     verify(out, lse, q, own, pre, new, -1, 0, 0, dim ** -0.5)
+
+
+@pytest.mark.parametrize("prefix", [0, 40, 2300])
+def test_strided_tables_and_outputs(prefix):
+    """A page table inside a wider one, the sequences' rows a slice of larger tensors, the output's too."""
+    new, keys, dim = [2] * 3, [70, 9, 150], 64
+    q, own, pre, kp, vp, table, pre_pages = attend_inputs(new, keys, 16, 4, 2, dim, "bf16", "heads", prefix)
+    wide = torch.full((3, table.shape[1] + 5), -7, dtype=torch.int32, device=DEV)
+    wide[:, 2:2 + table.shape[1]] = table
+    big_q = torch.randn(9, 7, dim, dtype=torch.bfloat16, device=DEV)
+    big_q[2:8, 1:5] = q.to(DEV)
+    room = torch.full((8, 6, dim), 7.0, dtype=torch.bfloat16, device=DEV)
+    lens = torch.tensor(keys, dtype=torch.int32, device=DEV)
+    out, lse = sc.shared_prefix_attention(big_q[2:8, 1:5], kp, vp, wide[:, 2:2 + table.shape[1]], lens, pre_pages, prefix,
+                                          right=0, return_lse=True, out=room[1:7, 1:5])
+    assert out.data_ptr() == room[1:7, 1:5].data_ptr()
+    verify(out, lse, q, own, pre, new, -1, 0, 0, dim ** -0.5)
+    room[1:7, 1:5] = 7
+    assert bool((room == 7).all())
 
 
 def test_one_page_in_many_places():
