@@ -499,8 +499,13 @@ __device__ __forceinline__ List sum_up(const PagedArgs& a, bool with_prefix, Ent
   return l;
 }
 
-__device__ __forceinline__ int run_start(int units, int runs, int w) { return uni(int(int64_t(units) * w / runs)); }
-__device__ __forceinline__ int owner(int units, int runs, int u) { return int(((int64_t(u) + 1) * runs - 1) / units); }
+// First unit of run w, floor(units w / runs), and the run of unit u. In 64-bit floats: the products, below 2^31 units
+// times 2^16 runs, are exact, and a quotient that is no whole number is 2^-47 of itself from the next one at least, more
+// than the division's rounding. (64-bit integer divisions are loops of a few hundred instructions.)
+__device__ __forceinline__ int run_start(int units, int runs, int w) { return uni(int(double(units) * w / runs)); }
+__device__ __forceinline__ int owner(int units, int runs, int u) {
+  return int(((double(u) + 1.0) * runs - 1.0) / units);
+}
 
 __device__ __forceinline__ void prefix_item(const PagedArgs& a, const List& l, int tile, Item& it) {
   it.prefix = true;
@@ -741,9 +746,15 @@ __device__ __forceinline__ void tile_run(const List& l, int kvh, Item item, int 
   while (u < u_end && item.n > 0) {
     const int t0 = uni(t), t1 = uni(min(item.n, t + (u_end - u))), end = min(t1, item.kt.n);
     u += t1 - t0;
+    auto pages = [&](const PagedArgs& a, int i) {
+      return i < end && lane < F::kKeys ? entry_of(a, item.keys, item.kt.at(i) * F::kKeys + lane) : -1;
+    };
     Rows r;
+    int first_ids, ids;
     {
       const PagedArgs& a = arguments().a;
+      first_ids = pages(a, t0);  // on their way while the rows are worked out
+      ids = pages(a, t0 + 1);
       r = item.prefix ? prefix_rows(a, item.keys, item.inside * F::kRows + 32 * wave, kvh, l32)
                       : own_rows(a, item.s, item.keys, item.inside * F::kRows + 32 * wave, kvh, l32);
       st.start(static_cast<const E*>(a.q.p) + r.tok * a.q.ts + r.head * a.q.hs, r.on, a.dim, lane);
@@ -754,9 +765,6 @@ __device__ __forceinline__ void tile_run(const List& l, int kvh, Item item, int 
       const E* vbase = static_cast<const E*>(a.pool.v) + kvh * a.pool.vhs;
       const float c = a.scale * kLog2e;
       const int mask = (1 << a.pool.log2) - 1;
-      auto pages = [&](int i) {
-        return i < end && lane < F::kKeys ? entry_of(a, item.keys, item.kt.at(i) * F::kKeys + lane) : -1;
-      };
       auto fetch = [&](int i, int buf, int ids) {
         const int j0 = item.kt.at(i) * F::kKeys;
         unsigned char* dst = mem + buf * 2 * F::kTileBytes;
@@ -764,8 +772,7 @@ __device__ __forceinline__ void tile_run(const List& l, int kvh, Item item, int 
         kc.template run<false>(dst, kbase, ids, mask, j0, item.keys.n - j0);
         vc.template run<true>(dst + F::kTileBytes, vbase, ids, mask, j0, item.keys.n - j0);
       };
-      if (t0 < end) fetch(t0, 0, pages(t0));
-      int ids = pages(t0 + 1);
+      if (t0 < end) fetch(t0, 0, first_ids);
       __builtin_amdgcn_s_waitcnt(0);
       __syncthreads();
       for (int i = t0; i < end; i += 2) {  // two tiles a round: the buffers' addresses are constants
@@ -774,7 +781,7 @@ __device__ __forceinline__ void tile_run(const List& l, int kvh, Item item, int 
           if (i + buf >= end) break;
           if (i + buf + 1 < end) {
             fetch(i + buf + 1, buf ^ 1, ids);
-            ids = pages(i + buf + 2);
+            ids = pages(a, i + buf + 2);
           }
           compute_tile<E, NB, F::kKeys, KB>(a, item.keys, item.kt, r, st, mem + buf * 2 * F::kTileBytes, i + buf, c, at,
                                             lane);
@@ -826,8 +833,10 @@ struct ModeShape {
   static constexpr int kLds = MODE == kTokens  ? FT::kLds
                               : MODE == kTiles ? FP::kLds
                                                : (FT::kLds > FP::kLds ? FT::kLds : FP::kLds);
-  // workgroups that a CU holds
-  static constexpr int kPerCu = MODE == kTiles ? (sizeof(E) == 4 ? (NB == 4 ? 1 : 2) : NB <= 2 ? 4 : 2)
+  // Workgroups that a CU holds. (Tile runs, 16 heads of 64, 1401 rows over up to 8192 keys: three 96 us, four, whose
+  // registers spill, 111, two 99; the kernel without runs holds four.)
+  static constexpr int kWhole = sizeof(E) == 4 ? (NB == 4 ? 1 : 2) : NB <= 2 ? 4 : 2;
+  static constexpr int kPerCu = MODE == kTiles ? (sizeof(E) == 2 && NB <= 2 ? 3 : kWhole)
                                                : (kLds > 80 * 1024 ? 1 : 2);
   static constexpr int kGrid = 256 * kPerCu;
 };
@@ -892,7 +901,7 @@ __global__ __launch_bounds__(256, (ModeShape<E, NB, MODE>::kPerCu)) void paged_s
 
 // One item a workgroup, straight to out: prompts of many rows.
 template <class E, int NB>
-__global__ __launch_bounds__(256, (ModeShape<E, NB, kTiles>::kPerCu)) void paged_tiles(StreamArgs, int tiles) {
+__global__ __launch_bounds__(256, (ModeShape<E, NB, kTiles>::kWhole)) void paged_tiles(StreamArgs, int tiles) {
   typedef PagedShape<E, NB, false> F;
   __shared__ __attribute__((aligned(1024))) unsigned char s_mem[F::kLds];
   const PagedArgs& a = arguments().a;
@@ -947,31 +956,37 @@ __global__ __launch_bounds__((64 * ShortShape<E, NB>::kWaves)) void paged_short(
   Item item;
   own_tile<F::kRows, F::kKeys>(a, b, s, inside, item);
   to_scalars(a, item);
-  const Rows own = own_rows(a, s, item.keys, inside * F::kRows, kvh, l32);
   // the prefix as this tile's rows see it
   const Keys pre_keys{a.prefix, a.prefix_len, min(a.sinks, a.prefix_len)};
+  KeyTiles pre_kt{0, 0, 0};
+  if (a.prefix_len > 0) {
+    const int rows = s.lq * group, p = a.prefix_len + s.lk - s.lq;
+    pre_kt = key_tiles<F::kKeys>(a.left, a.right, pre_keys.sinks, inside * F::kRows / group + p,
+                                 (min(rows, (inside + 1) * F::kRows) - 1) / group + p, a.prefix_len);
+    pre_kt = KeyTiles{uni(pre_kt.sink), uni(pre_kt.band), uni(pre_kt.n)};
+  }
+  const int end = pre_kt.n + item.kt.n;
+  // tile i: of the prefix, then of the own keys
+  auto keys_of = [&](int i) { return i < pre_kt.n ? pre_keys : item.keys; };
+  auto key_of = [&](int i) { return (i < pre_kt.n ? pre_kt.at(i) : item.kt.at(i - pre_kt.n)) * F::kKeys; };
+  auto pages = [&](int i) { return i < end && lane < F::kKeys ? entry_of(a, keys_of(i), key_of(i) + lane) : -1; };
+  int i = wave, buf = 0, ids = pages(i);  // on their way while the rows are worked out
+  const Rows own = own_rows(a, s, item.keys, inside * F::kRows, kvh, l32);
   Rows pre = own;
   see(a, pre_keys, own.lo + a.left + a.prefix_len, pre);
   pre.p0 += a.prefix_len;
   pre.p1 += a.prefix_len;
-  KeyTiles pre_kt{0, 0, 0};
-  if (a.prefix_len > 0) pre_kt = key_tiles<F::kKeys>(a.left, a.right, pre_keys.sinks, pre.p0, pre.p1, a.prefix_len);
-  pre_kt = KeyTiles{uni(pre_kt.sink), uni(pre_kt.band), uni(pre_kt.n)};
   const typename T::Lane at = T::lane_of(lane);
   RowState<E, NB, KB> st;
   st.start(static_cast<const E*>(a.q.p) + own.tok * a.q.ts + own.head * a.q.hs, own.on, a.dim, lane);
   const E* kbase = static_cast<const E*>(a.pool.k) + kvh * a.pool.khs;
   const E* vbase = static_cast<const E*>(a.pool.v) + kvh * a.pool.vhs;
   const float c = a.scale * kLog2e;
-  const int mask = (1 << a.pool.log2) - 1, end = pre_kt.n + item.kt.n;
+  const int mask = (1 << a.pool.log2) - 1;
   unsigned char* const mem = s_mem + wave * NBUF * 2 * F::kTileBytes;
   PagedCopy<E, NB, F::kKeys, 1> kc, vc;
   kc.start(a.pool.kps, a.pool.kss, a.dim, 0, lane);
   vc.start(a.pool.vps, a.pool.vss, a.dim, 0, lane);
-  // tile i: of the prefix, then of the own keys
-  auto keys_of = [&](int i) { return i < pre_kt.n ? pre_keys : item.keys; };
-  auto key_of = [&](int i) { return (i < pre_kt.n ? pre_kt.at(i) : item.kt.at(i - pre_kt.n)) * F::kKeys; };
-  auto pages = [&](int i) { return i < end && lane < F::kKeys ? entry_of(a, keys_of(i), key_of(i) + lane) : -1; };
   auto fetch = [&](int i, int buf, int ids) {
     const int j0 = key_of(i), left = keys_of(i).n - j0;
     unsigned char* dst = mem + buf * 2 * F::kTileBytes;
@@ -990,7 +1005,6 @@ __global__ __launch_bounds__((64 * ShortShape<E, NB>::kWaves)) void paged_short(
     compute_tile<E, NB, F::kKeys, KB>(a, keys_of(i), kt, r, st, mem + buf * 2 * F::kTileBytes, 0, c, at, lane);
   };
   // each wave its own tiles and LDS: no barrier in the loop
-  int i = wave, buf = 0, ids = pages(i);
   if (NBUF == 2 && i < end) {
     fetch(i, 0, ids);
     ids = pages(i + W);
