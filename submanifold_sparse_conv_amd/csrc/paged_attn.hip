@@ -39,7 +39,7 @@
 // 16 query heads): 76.7 GFLOP in 110 us, 100 and the join of 45 MB of parts, matrix
 // units busy in a third of the cycles: 36 units a workgroup, two workgroups a CU,
 // which start and end a run 1.4 times on average. 256 sequences behind 8192 common
-// keys: 79 us, where the prefix's half of the chip has one workgroup a CU, since a
+// keys: 77 to 79 us, where the prefix's half of the chip has one workgroup a CU, since a
 // wave's own tiles take 128 KB of LDS. Small calls: latency; 8 caches of up to 450
 // keys 7.8 us, 4 sequences behind 1369 keys 16.
 #include <type_traits>
