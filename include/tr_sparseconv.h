@@ -514,7 +514,8 @@ typedef struct {
  * q_out    as q, may be q itself (same strides). Rows of tokens in no sequence are
  *          left as they are.
  * q_out must not overlap k, v or the pages, the pages not the inputs, k's pages
- * not v's (side by side in one tensor is fine). Where the tables give two tokens
+ * not v's (side by side in one tensor is fine, with gaps too; pages of unlike
+ * strides in one range count as overlapping). Where the tables give two tokens
  * the same place, one of them is stored. */
 int tr_sparseconv_qk_norm_rope_append(const tr_sc_heads* q, const tr_sc_heads* k, const tr_sc_heads* v,
                                       const tr_sc_rotation* rotation, const float* q_gain, int q_gain_rows,

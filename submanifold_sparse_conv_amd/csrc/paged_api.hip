@@ -21,48 +21,49 @@ struct PoolView {
   bool empty() const { return count[0] == 0; }
 };
 
+// The levels of more than one element, the inner ones first; returns their number.
+int levels_of(const PoolView& p, int (&order)[3]) {
+  int n = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (p.count[i] <= 1) continue;
+    int at = n++;
+    for (; at > 0 && p.step[order[at - 1]] > p.step[i]; --at) order[at] = order[at - 1];
+    order[at] = i;
+  }
+  return n;
+}
+
 // Whether each level's elements fit between two of the next: no element is another's.
 bool pool_rows_overlap(const PoolView& p) {
   if (p.empty()) return false;
-  int order[3] = {0, 1, 2};
-  for (int i = 0; i < 3; ++i)
-    for (int j = i + 1; j < 3; ++j)
-      if (p.step[order[j]] < p.step[order[i]]) {
-        const int t = order[i];
-        order[i] = order[j];
-        order[j] = t;
-      }
+  int order[3];
+  const int n = levels_of(p, order);
   wide_t extent = p.row;
-  for (int i = 0; i < 3; ++i) {
-    if (p.count[order[i]] <= 1) continue;
+  for (int i = 0; i < n; ++i) {
     if (p.step[order[i]] < extent) return true;
     extent += wide_t(p.count[order[i]] - 1) * p.step[order[i]];
   }
   return false;
 }
 
-// Keys and values side by side at some level of the same strides (in a token's row, in a page, page by page), or in
-// ranges of their own; anything else is taken to overlap.
+// Whether two pools whose own rows do not overlap share an element. Of equal strides: rows that are i_l steps apart at
+// level l have the distance d + sum i_l step_l. What the inner levels add to is less than a step, so two i_l at each
+// level can bring it within a row. Unlike strides in one range are taken to overlap.
+bool rows_meet(const PoolView& p, const int* order, int levels, wide_t d) {
+  if (levels == 0) return -p.row < d && d < p.row;
+  const int64_t step = p.step[order[levels - 1]], most = p.count[order[levels - 1]] - 1;
+  const wide_t i = -(d / step) - (d % step > 0 ? 1 : 0);  // the last with d + i step <= 0
+  for (int k = 0; k < 2; ++k)
+    if (-most <= i + k && i + k <= most && rows_meet(p, order, levels - 1, d + (i + k) * step)) return true;
+  return false;
+}
 bool pools_overlap(const PoolView& a, const PoolView& b) {
   if (a.empty() || a.end() <= b.at || b.end() <= a.at) return false;
   for (int i = 0; i < 3; ++i)
     if (a.count[i] > 1 && a.step[i] != b.step[i]) return true;
-  for (int level = 0; level < 3; ++level) {  // the two alternate between steps of this level
-    const int64_t step = a.step[level];
-    if (a.count[level] <= 1 || step == 0) continue;
-    wide_t extent = a.row;  // of the levels inside
-    bool fits = true;
-    for (int i = 0; i < 3; ++i)
-      if (i != level && a.count[i] > 1) {
-        if (a.step[i] < step)
-          extent += wide_t(a.count[i] - 1) * a.step[i];
-        else if (a.step[i] % step != 0)
-          fits = false;  // the levels outside must keep the phase
-      }
-    const int64_t d = ((b.at - a.at) % step + step) % step;
-    if (fits && d >= extent && d + extent <= step) return false;
-  }
-  return true;
+  int order[3];
+  const int n = levels_of(a, order);
+  return rows_meet(a, order, n, wide_t(b.at) - a.at);
 }
 
 bool meets_pool(const View& v, const PoolView& p) {
