@@ -28,6 +28,9 @@ PyObject* check_fn = nullptr;   // check(code): raises for an error of the libra
 PyObject* stream_fn = nullptr;  // stream of a device index
 PyObject* device_fn = nullptr;  // current device index
 
+// A number past its C field would be taken modulo its range.
+constexpr int64_t kFieldMost = int64_t(1) << 31;
+
 [[noreturn]] void refuse(const std::string& what) {
   C10_THROW_ERROR(ValueError, what);
 }
@@ -68,6 +71,8 @@ tr_sc_heads heads_of(PyObject* o, const char* name, const at::Tensor* like = nul
   if (t == nullptr || !t->is_cuda()) refuse(std::string(name) + " must be a GPU tensor");
   if (t->dim() != 3) refuse(std::string(name) + " must be [tokens, heads, dim], got " + shape_text(*t));
   const int64_t n = t->size(0), h = t->size(1), d = t->size(2);
+  if (h >= kFieldMost || d >= kFieldMost)
+    refuse(std::string(name) + " has " + std::to_string(h) + " heads of " + std::to_string(d) + " elements, past 2^31");
   if (like != nullptr) {
     if (d != like->size(2) || (tokens >= 0 && n != tokens) || (heads >= 0 && h != heads))
       refuse(std::string(name) + " must be [" + (tokens < 0 ? "*" : std::to_string(tokens)) + ", " +
@@ -128,9 +133,7 @@ tr_sc_pages pages_of(PyObject* ko, PyObject* vo, PyObject* to, PyObject* lo, con
   if (batch < 1) refuse("page_table needs a sequence at least");
   if (lo == Py_None) refuse("k_len must be given");
   const int32_t* len = ints_of(lo, "k_len", batch, device);
-  // a number past its C field would be taken modulo its range
-  const int64_t most = int64_t(1) << 31;
-  if (size >= most || heads >= most || width >= most || batch >= most) refuse("the pages or their table are too large");
+  if (size >= kFieldMost || heads >= kFieldMost || width >= kFieldMost || batch >= kFieldMost) refuse("the pages or their table are too large");
   // a stride that is never taken may be anything
   const auto st = [](const at::Tensor& t, int d) { return t.size(d) > 1 ? t.stride(d) : int64_t(0); };
   tr_sc_pages p;
