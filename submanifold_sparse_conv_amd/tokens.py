@@ -22,6 +22,7 @@ from ._lib import Heads, Rotation, Window, check
 _DTYPES = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16, torch.float16: _lib.F16}
 _byref = ctypes.byref
 _Pairs = ctypes.c_int * 3
+_FIELD_MOST = 1 << 31  # a number past its C field would be taken modulo its range
 
 
 def _heads(t, name: str, tokens=None, heads=None, dim=None, like: torch.Tensor | None = None) -> Heads:
@@ -31,6 +32,8 @@ def _heads(t, name: str, tokens=None, heads=None, dim=None, like: torch.Tensor |
     if len(shape) != 3:
         raise ValueError(f"{name} must be [tokens, heads, dim], got {tuple(shape)}")
     n, h, d = shape
+    if h >= _FIELD_MOST or d >= _FIELD_MOST:
+        raise ValueError(f"{name} has {h} heads of {d} elements, past 2^31")
     if like is not None:
         if d != dim or (tokens is not None and n != tokens) or (heads is not None and h != heads):
             want = ["*" if w is None else w for w in (tokens, heads, dim)]
@@ -207,10 +210,11 @@ def _window(cu_q, cu_k, k_len, left, right, sinks, scale, dim, device) -> Window
         raise ValueError("cu_q and cu_k go together")
     if cu_q is not None and isinstance(cu_q, torch.Tensor) and cu_q.dim() == 1 and cu_q.shape[0] < 2:
         raise ValueError("cu_q needs two elements at least (one sequence)")
-    # a number past its C field would be taken modulo its range
-    if not (-1 <= left < 1 << 63 and -1 <= right < 1 << 63 and 0 <= sinks < 1 << 31):
+    if not (-1 <= left < 1 << 63 and -1 <= right < 1 << 63 and 0 <= sinks < _FIELD_MOST):
         raise ValueError(f"window ({left}, {right}) with {sinks} sinks: sides are -1 or more, sinks 0 or more")
     batch = 1 if cu_q is None else len(cu_q) - 1
+    if batch >= _FIELD_MOST:
+        raise ValueError(f"{batch} sequences, past 2^31")
     return Window(_ints(cu_q, "cu_q", -1, device), _ints(cu_k, "cu_k", batch + 1, device),
                   _ints(k_len, "k_len", batch, device), batch, left, right, sinks,
                   dim ** -0.5 if scale is None else scale)

@@ -50,3 +50,23 @@ def test_paged_elements():
     q = torch.zeros(0, 4, dim, dtype=torch.bfloat16, device=DEV)
     with pytest.raises(ValueError, match="q has"):
         sc.paged_window_attention(q, **cache(dim))
+
+
+@pytest.mark.parametrize("far,tokens", [("q", 0), ("k", 0), ("both", 0), ("k", 1)])
+def test_token_operators_heads(far, tokens):
+    q, k = rows(tokens, FAR + 4 if far != "k" else 4), rows(tokens, FAR + 2 if far != "q" else 2)
+    name = "k has" if far == "k" else "q has"
+    with pytest.raises(ValueError, match=name):
+        sc.qk_norm_rope(q, k, **turn(tokens), k_out=rows(tokens, 2))
+    with pytest.raises(ValueError, match=name):
+        sc.qk_norm_rope_backward(q, k, q, k, **turn(tokens), dk=rows(tokens, 2))
+    with pytest.raises(ValueError, match=name):
+        sc.window_attention(q, k, k)
+    with pytest.raises(ValueError, match=name):
+        sc.window_attention_backward(q, q, k, k, q, torch.zeros(4, tokens, device=DEV))
+
+
+def test_token_operators_elements():
+    q = torch.zeros(0, 4, FAR + 64, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="q has"):
+        sc.window_attention(q, q, q)
