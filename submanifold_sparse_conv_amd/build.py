@@ -65,13 +65,13 @@ def build(verbose: bool = False) -> str:
     with ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
         binding = ex.submit(_build_binding)
         objs = list(ex.map(_compile, srcs))
-        binding.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    binding.result()  # raises where the binding failed: the library is there for users of the C ABI
     if verbose:
         print(f"built {LIB} from {len(srcs)} sources")
     return LIB
