@@ -8,8 +8,9 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
-import torch  # noqa: F401  (maps the HIP runtime first)
+import torch  # maps the HIP runtime first
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtr_sparseconv.so")
 
@@ -152,6 +153,11 @@ def check(code: int) -> None:
         raise TrSparseConvError(code, msg.decode() if msg else "")
 
 
+def torch_and_python() -> str:
+    """What the native part of the binding is built for."""
+    return f"torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
 def binding():
     """The native part of the binding (csrc/binding.cpp), bound to the library's functions."""
     global _binding
@@ -161,6 +167,10 @@ def binding():
             from . import _binding as module
         except ImportError as e:
             raise ImportError("the native binding is not built; run `python -m submanifold_sparse_conv_amd.build`") from e
+        of = getattr(module, "built_for", "something older")
+        if of != torch_and_python():
+            raise ImportError(f"the native binding was built for {of}, this is {torch_and_python()}; run "
+                              "`python -m submanifold_sparse_conv_amd.build`")
         stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
         device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device

@@ -43,13 +43,16 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _build_binding() -> None:
+def _compile_binding() -> None:
     import torch
+
+    from ._lib import torch_and_python
 
     at = os.path.join(os.path.dirname(torch.__file__), "include")
     tmp = BINDING + ".tmp%d" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-I", at, "-I",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DTR_SC_BUILT_FOR="{torch_and_python()}"', "-I", INCLUDE, "-I", at, "-I",
            os.path.join(at, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
            os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", os.path.join(os.path.dirname(at), "lib"), "-ltorch_python",
            "-ltorch_cpu", "-lc10"]
@@ -57,6 +60,15 @@ def _build_binding() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+
+
+def _build_binding() -> None:
+    try:
+        _compile_binding()
+    except Exception:  # an earlier build's must not meet the new library
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+        raise
 
 
 def build(verbose: bool = False) -> str:

@@ -391,4 +391,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&module);
+  // torch's C++ types have no stable layout: the package compares this before it binds
+  if (m != nullptr && PyModule_AddStringConstant(m, "built_for", TR_SC_BUILT_FOR) != 0) Py_CLEAR(m);
+  return m;
+}
