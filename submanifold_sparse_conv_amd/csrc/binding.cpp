@@ -328,17 +328,21 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   size_t bytes = bytes_fn(&pages, &win, prefixed ? prefix_len : 0, tokens, q.heads, int(dim), dt);
   void* ws = nullptr;
   if (a[14] != Py_None) {  // a Workspace
-    PyObject *size = PyObject_GetAttrString(a[14], "nbytes"), *buf = PyObject_GetAttrString(a[14], "buf");
-    const at::Tensor* t = buf ? tensor_or_null(buf) : nullptr;
-    const int64_t have = size ? PyLong_AsLongLong(size) : -1;
-    Py_XDECREF(size);
-    Py_XDECREF(buf);  // the Workspace holds it
+    PyObject* size = PyObject_GetAttrString(a[14], "nbytes");
+    if (size == nullptr) throw python_error();
+    const int64_t have = PyLong_AsLongLong(size);
+    Py_DECREF(size);
     if (PyErr_Occurred()) throw python_error();
-    if (t == nullptr) refuse("workspace must be a Workspace");
+    PyObject* buf = PyObject_GetAttrString(a[14], "buf");
+    if (buf == nullptr) throw python_error();
+    const at::Tensor* t = tensor_or_null(buf);
+    if (t != nullptr) space = *t;  // the object may be made for this question alone
+    Py_DECREF(buf);
+    if (!space.defined()) refuse("workspace must be a Workspace");
     if (have < int64_t(bytes))
       refuse("workspace of " + std::to_string(have) + " bytes, " + std::to_string(bytes) + " needed");
-    if (t->device() != device) refuse("the workspace is on " + t->device().str() + ", the tensors on " + device.str());
-    const uintptr_t p = reinterpret_cast<uintptr_t>(t->data_ptr());
+    if (space.device() != device) refuse("the workspace is on " + space.device().str() + ", the tensors on " + device.str());
+    const uintptr_t p = reinterpret_cast<uintptr_t>(space.data_ptr());
     ws = reinterpret_cast<void*>((p + 255) / 256 * 256);
     bytes = size_t(have);
   } else if (bytes > 0) {  // torch's own blocks are aligned to 256 bytes and more
