@@ -515,8 +515,10 @@ typedef struct {
  *          left as they are.
  * q_out must not overlap k, v or the pages, the pages not the inputs, k's pages
  * not v's (side by side in one tensor is fine, with gaps too; pages of unlike
- * strides in one range count as overlapping). Where the tables give two tokens
- * the same place, one of them is stored. */
+ * strides in one range count as overlapping). Every token of a call needs a place
+ * of its own: where the tables give several the same one, it is unspecified what
+ * the place holds afterwards (elements of any of them; its key and its value need
+ * not be one token's). Nothing else depends on it. */
 int tr_sparseconv_qk_norm_rope_append(const tr_sc_heads* q, const tr_sc_heads* k, const tr_sc_heads* v,
                                       const tr_sc_rotation* rotation, const float* q_gain, int q_gain_rows,
                                       const float* k_gain, int k_gain_rows, int norm, float eps,

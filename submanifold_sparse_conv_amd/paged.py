@@ -32,7 +32,9 @@ def qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: 
     sections, interleaved and eps as in qk_norm_rope; norm=False: rotation alone,
     without gains. Token i of a sequence's Lq is its key k_len[b] - Lq + i. Tokens
     of no sequence (behind cu_q's last) are neither stored nor written to q_out;
-    one whose key is none of the table is not stored. q_out may be q itself."""
+    one whose key is none of the table is not stored. q_out may be q itself. The
+    table must not give two of the call's tokens the same place: it is unspecified
+    what that place holds then."""
     return (_lib._binding or _lib.binding()).append(q, k, v, pos, freqs, k_pages, v_pages, page_table, k_len, cu_q, q_gain,
                                                     k_gain, sections, interleaved, eps, norm, q_out)
 

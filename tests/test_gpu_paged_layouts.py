@@ -1,5 +1,5 @@
 """Pages whose strides are no multiples of each other's, through the append and both attentions: the same bits as from
-pages without gaps, and what lies in the gaps is left as it is."""
+pages without gaps, and what lies in the gaps is left as it is. Tables that give two tokens one place."""
 import pytest
 import torch
 
@@ -54,3 +54,26 @@ def test_gaps(dtype, hk, dim, order):
     kp.fill_(7.0)
     vp.fill_(7.0)
     assert bool((flat == 7).all())
+
+
+@pytest.mark.parametrize("dtype,dim", [("bf16", 64), ("f32", 72)])
+def test_tokens_with_one_place(dtype, dim):
+    """Two sequences that share a page, a page that a sequence has twice: every other place, and every query, as if each
+    token had a place of its own. What the shared places hold is unspecified."""
+    g, dt, page, hq, hk, n = gen(32), TD[dtype], 8, 4, 2, 40
+    say("[one place]", dtype, dim)
+    qkv = randn(g, 3 * n, hq + 2 * hk, dim, dtype=dt).to(DEV)
+    table = torch.tensor([[0, 1, 2, 3, 4], [5, 6, 2, 7, 8], [9, 10, 11, 9, 12]], dtype=torch.int32, device=DEV)
+    pos = torch.arange(3 * n, dtype=torch.int32, device=DEV)
+    freqs = sc.rope_frequencies(dim, device=DEV)
+    kp, vp = (torch.full((14, page, hk, dim), 7.0, dtype=dt, device=DEV) for _ in range(2))
+    q, k, v = qkv.split([hq, hk, hk], 1)
+    want_q, want_k = sc.qk_norm_rope(q, k, pos, freqs)
+    lens = torch.full((3,), n, dtype=torch.int32, device=DEV)
+    assert torch.equal(bits(sc.qk_norm_rope_append(q, k, v, pos, freqs, kp, vp, table, lens)), bits(want_q))
+    for b in range(3):
+        for i in range(5):
+            p, t = int(table[b, i]), n * b + page * i
+            if p not in (2, 9):
+                assert torch.equal(bits(kp[p]), bits(want_k[t:t + page])) and torch.equal(bits(vp[p]), bits(v[t:t + page]))
+    assert bool((kp[13] == 7).all()) and bool((vp[13] == 7).all())
