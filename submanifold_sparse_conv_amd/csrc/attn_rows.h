@@ -11,7 +11,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // representable. A tile is weighed with the maximum so far, and only where its
 // sum leaves [0, kMostSum) is the maximum taken again, the sums rescaled and the
 // tile weighed anew. (fp16 holds weights up to 65504.) With the maximum of every
-// tile taken the two bf16 sizes above took 1.24 ms and 622 us.
+// tile taken a causal prompt of 32,768 tokens (bf16, 16 heads of 128 over 4, 4096 keys back)
+// took 1.24 ms for 0.99, 73,881 tokens (16 heads of 64, 512 keys either way) 622 us for 411.
 constexpr float kMostSum = 16384.f;
 // fp16 holds weights from 2^-14 (its smallest normal) to 65504, so the base moves down as well: where a lane's sum
 // of up to 32 keys falls below kLeastSum16 (a leading key before them, a sink say), the tile's own largest weight

@@ -11,14 +11,20 @@
 // group, in tiles of 32 (few rows: one wave holds them) or 128 rows (four waves
 // that share the key tiles). The prefix: the rows of all sequences are one
 // matrix, so its keys are read once for a tile, whatever sequence its rows
-// belong to; each row has its own position. A query that is i-th of Lq stands at
+// belong to (small calls: for each sequence's tile); each row has its own position. A query that is i-th of Lq stands at
 // i + P + Lk - Lq.
 //
 // Work. An item is a row tile with all key tiles that it sees; a unit is one of
 // those. The units of all items in a row are dealt out evenly, each wave (32
 // rows) or workgroup (128) taking one contiguous run of them for one kv head:
-// lengths differ and only the device knows them, so every workgroup sums them up
-// (one read of the lengths) and finds its run. An item that two runs share leaves
+// lengths differ and only the device knows them, so every wave sums them up and
+// finds its run. A lane sums batch / 64 sequences, tile of rows by tile of rows, and
+// where an item begins its sequence is searched from its lane's first one: short
+// for a few hundred sequences or tiles; 4096 sequences of 50 keys take 597 us where
+// 256 of 800 take 83 (4 kv heads of 128), one prompt of 16,384 tokens, 8 heads over
+// 1 of 128, 1023 keys back, 567 us for a floor of 53, and behind a prefix, where
+// there is no form without runs, 65,536 tokens of 8 heads over 1 of 64 2.8 ms for
+// 128 us without one. An item that two runs share leaves
 // parts in the workspace that the join adds up in order. The heads' runs are cut
 // at the same places and lie in neighbouring waves, which so read neighbouring
 // memory at the same time.
@@ -208,7 +214,8 @@ __device__ __forceinline__ Rows prefix_rows(const PagedArgs& a, const Keys& keys
     const OwnSeq s = paged_sequence(a, r.tok / a.seqs.each);
     p = r.tok - s.q0 + s.lk - s.lq;
   } else {
-    // a sequence at a time: that of the first row which has none yet
+    // a sequence at a time: that of the first row which has none yet (256 single tokens of 4 heads behind 8192 keys, 32
+    // sequences a wave: 152 us with offsets, 49 without)
     bool found = false;
     uint64_t open = __ballot(r.on);
     while (open != 0) {
@@ -833,14 +840,17 @@ struct ModeShape {
   static constexpr int kLds = MODE == kTokens  ? FT::kLds
                               : MODE == kTiles ? FP::kLds
                                                : (FT::kLds > FP::kLds ? FT::kLds : FP::kLds);
-  // Workgroups that a CU holds. (Tile runs, 16 heads of 64, 1401 rows over up to 8192 keys: three 96 us, four, whose
-  // registers spill, 111, two 99; the kernel without runs holds four.)
+  // Workgroups that a CU holds. (Tile runs, 16 heads of 64, 1401 rows over up to 8192 keys: three 96 us, four 111, two
+  // 99; the kernel without runs holds four. Three spill 2 vector registers; two at half heads of 128 9, at fp32 heads of 96
+  // 37.)
   static constexpr int kWhole = sizeof(E) == 4 ? (NB == 4 ? 1 : 2) : NB <= 2 ? 4 : 2;
   static constexpr int kPerCu = MODE == kTiles ? (sizeof(E) == 2 && NB <= 2 ? 3 : kWhole)
                                                : (kLds > 80 * 1024 ? 1 : 2);
   static constexpr int kGrid = 256 * kPerCu;
 };
-// Time of a prefix unit of a workgroup, in those of a wave's own.
+// Time of a prefix unit of a workgroup, in those of a wave's own. Swept at one shape, bf16 heads of 128, 256 sequences
+// behind 8192 keys: 0.7 77.6 us, 0.55 92, 0.86 85. Other types and widths, whose units and workgroups a CU differ, use
+// the same.
 constexpr float kPrefixCost = 0.7f;
 
 template <class E, int NB, int MODE>
@@ -1308,7 +1318,10 @@ hipError_t launch_join(const PagedArgs& a, const PagedPlan& p, const PartMap& m,
     const int64_t pre_tiles = (int64_t(a.nq) * (a.hq / a.hk) + PR - 1) / PR;
     parts += (PR == 128 ? p.grid / 2 : workers / 2) / (pre_tiles * heads) + 1;
   }
-  // Many parts of few rows: sixteen waves a row (one cache in 256 parts 9 us, with four 12), or four.
+  // Many parts of few rows: sixteen waves a row, or four. Whole calls with 16 / 4 / 1, us: one cache of 99,000 keys, 8
+  // heads over 2 of 128 (takes 16) 37.5 / 42 / 91; 32 sequences of 16 heads behind 16,219 keys (4) 35 / 31 / 33; 256 behind
+  // 8192 (1) 116 / 82 / 75; parts of prompts, 1401 rows of 16 heads (1) 354 / 151 / 118; 30 rows of 6 heads, fp32 (16) 17.9 /
+  // 17.2 / 17.3. The borders lie between these sizes; nearer to them nothing is measured.
   const int64_t rows_all = int64_t(a.hq) * a.nq;
   const int wpr = parts > 48 && rows_all <= 1024 ? 16 : parts > 8 && rows_all <= 16384 ? 4 : 1;
   const int rows = R == 32 ? 1 : 2;
