@@ -537,7 +537,8 @@ int tr_sparseconv_qk_norm_rope_append(const tr_sc_heads* q, const tr_sc_heads* k
  * up]), then its own len[b]; the window and the sinks go over both. The
  * prefix's keys and values are read once for a tile of 32 or 128 rows of whatever
  * sequences, in small calls (up to 256 tiles of rows and heads over a short
- * prefix) once for every sequence's tile. prefix_len = 0: the same as paged_window_attention.
+ * prefix) once for every sequence's tile. prefix_len = 0: the same as
+ * paged_window_attention.
  *
  * workspace: >= the bytes of the query (which reads no device array; prefix_len 0
  * for paged_window_attention), 256-byte aligned; 0 bytes: may be NULL. */

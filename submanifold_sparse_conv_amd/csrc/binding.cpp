@@ -133,7 +133,8 @@ tr_sc_pages pages_of(PyObject* ko, PyObject* vo, PyObject* to, PyObject* lo, con
   if (batch < 1) refuse("page_table needs a sequence at least");
   if (lo == Py_None) refuse("k_len must be given");
   const int32_t* len = ints_of(lo, "k_len", batch, device);
-  if (size >= kFieldMost || heads >= kFieldMost || width >= kFieldMost || batch >= kFieldMost) refuse("the pages or their table are too large");
+  if (size >= kFieldMost || heads >= kFieldMost || width >= kFieldMost || batch >= kFieldMost)
+    refuse("the pages or their table are too large");
   // a stride that is never taken may be anything
   const auto st = [](const at::Tensor& t, int d) { return t.size(d) > 1 ? t.stride(d) : int64_t(0); };
   tr_sc_pages p;

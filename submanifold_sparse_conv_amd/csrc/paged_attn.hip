@@ -11,8 +11,8 @@
 // group, in tiles of 32 (few rows: one wave holds them) or 128 rows (four waves
 // that share the key tiles). The prefix: the rows of all sequences are one
 // matrix, so its keys are read once for a tile, whatever sequence its rows
-// belong to (small calls: for each sequence's tile); each row has its own position. A query that is i-th of Lq stands at
-// i + P + Lk - Lq.
+// belong to (small calls: for each sequence's tile); each row has its own
+// position. A query that is i-th of Lq stands at i + P + Lk - Lq.
 //
 // Work. An item is a row tile with all key tiles that it sees; a unit is one of
 // those. The units of all items in a row are dealt out evenly, each wave (32

@@ -62,8 +62,8 @@ def shared_prefix_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: tor
     """paged_window_attention of sequences whose keys begin with a common prefix
     (tr_sparseconv_shared_prefix_attention): prefix_len keys in the pool's pages
     prefix_pages (int32 vector), which are read for rows of all sequences together
-    (in small calls for each sequence). A sequence's
-    keys are the prefix's, then its own k_len[b]; positions, window and sinks count
+    (in small calls for each sequence). A sequence's keys are the prefix's, then
+    its own k_len[b]; positions, window and sinks count
     over both, query i standing at p = i + prefix_len + k_len - Lq."""
     if not 0 <= prefix_len <= 1 << 30:
         raise ValueError(f"prefix_len = {prefix_len} out of [0, 2^30]")
